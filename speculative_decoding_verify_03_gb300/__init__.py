@@ -18,11 +18,15 @@ _ROOT = os.path.dirname(_HERE)
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 _SOURCES = [os.path.join(_HERE, "csrc", f) for f in ("spec_verify.cu", "spec_strip.cu", "spec_row.cu",
                                                       "spec_commit.cu", "spec_law.cu",
-                                                      "spec_cascade.cu")]
+                                                      "spec_cascade.cu", "kv_cache.cu",
+                                                      "kv_attend.cu", "kv_span_e4m3_64_80.cu",
+                                                      "kv_span_e4m3_96_128.cu",
+                                                      "kv_span_bf16_64_80.cu",
+                                                      "kv_span_bf16_96_128.cu")]
 _DEPS = _SOURCES + [os.path.join(_HERE, "csrc", f)
                     for f in ("sv_common.cuh", "sv_core.cuh", "sv_strip.h", "sv_row.h",
-                              "sv_verify.h")] + [
-    os.path.join(_ROOT, "include", "spec_verify.h")]
+                              "sv_verify.h", "kv_common.cuh", "kv_span.h", "kv_span.cuh")] + [
+    os.path.join(_ROOT, "include", h) for h in ("spec_verify.h", "spec_kv.h")]
 
 SPEC_F32, SPEC_BF16 = 0, 1
 ROW_BAD_TOKEN, ROW_BAD_LOGIT, ROW_NO_FINITE, ROW_Q_ZERO, ROW_BAD_GAMMA, ROW_BAD_UNIFORM = (
@@ -32,7 +36,8 @@ ROW_ERROR_MASK = ROW_BAD_TOKEN | ROW_BAD_LOGIT | ROW_NO_FINITE | ROW_BAD_GAMMA |
 EXPORTS = ("spec_verify", "spec_sample", "spec_verify_workspace_size", "spec_status_string",
            "spec_read_diagnostics", "spec_verify_noalloc", "spec_commit", "spec_law",
            "spec_cascade_verify", "spec_cascade_workspace_size", "spec_law_ws",
-           "spec_law_workspace_size", "spec_sample_ws", "spec_sample_workspace_size")
+           "spec_law_workspace_size", "spec_sample_ws", "spec_sample_workspace_size",
+           "spec_kv_append", "spec_kv_read", "spec_attend", "spec_attend_workspace_size")
 
 
 class SpecParams(ctypes.Structure):
@@ -101,6 +106,8 @@ def build(force: bool = False, out: str = None, extra=()) -> str:
     return out
 
 
+from . import kv as _kv  # noqa: E402
+
 _lock = threading.Lock()
 _lib = None
 
@@ -149,6 +156,7 @@ def lib():
                                               ctypes.POINTER(SpecParams), vp, vp, vp, vp, vp,
                                               sz, vp]
             L.spec_cascade_verify.restype = ctypes.c_int
+            _kv.declare(L)
             _lib = L
     return _lib
 
@@ -506,3 +514,7 @@ def spec_cascade_verify(levels, draft_tokens, uniforms, temperature, top_k=0, to
         out_tok.data_ptr(), out_len.data_ptr(), stage_acc.data_ptr(), status.data_ptr(),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
     return out_tok, out_len, stage_acc, status
+
+
+from .kv import (KVCache, ROW_BAD_LENGTH, ROW_BAD_PAGE, attend_workspace_bytes,  # noqa: E402,F401
+                 spec_attend, spec_kv_append, spec_kv_read)

@@ -1,0 +1,222 @@
+// kv_attend.cu -- spec_attend: the plan of the span kernels' launches and the
+// merge of their partial results.
+//
+// Merge: row (b, i, h) has one partial result (o_s, lse2_s) for every CTA that
+// worked on its own item and, with a prefix, on its prefix item;
+//   out = sum_s 2^(lse2_s - m) o_s / sum_s 2^(lse2_s - m),
+//   lse = ln 2 (m + log2 sum_s 2^(lse2_s - m)),  m = max_s lse2_s,
+// in the order of the slots (reproducible).  A warp takes a row; the partial
+// results were written just before and are read from L2.
+#include "kv_span.h"
+
+namespace {
+
+using namespace kv;
+
+constexpr int MG_NT = 256;
+constexpr int MG_ROWS = 32;  // rows per CTA
+
+struct MP {
+  View w;
+  Plan plan;
+  const float *po, *pl, *qo, *ql;  // partial results: own, prefix
+  __nv_bfloat16 *out;
+  float *lse;
+  int32_t *status;
+  int32_t G, Hq, D, rto, rtp, co, cp;  // rows per item and CTAs, own and prefix
+};
+
+__global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP P) {
+  const View &w = P.w;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int own, n;
+  int st = row_shape(w, b, own, n);
+  int bad = 0;
+  if (!st) {  // the page ids in use
+    const uint32_t np = static_cast<uint32_t>(w.n_pages);
+    const int pm = (1 << w.ps_log2) - 1;
+    for (int p = threadIdx.x; p < (own + n + pm) >> w.ps_log2; p += MG_NT)
+      bad |= static_cast<uint32_t>(__ldg(w.table + b * w.tstride + p)) >= np;
+    for (int p = threadIdx.x; p < (w.prefix + pm) >> w.ps_log2; p += MG_NT)
+      bad |= static_cast<uint32_t>(__ldg(w.ptable + p)) >= np;
+  }
+  if (__syncthreads_or(bad)) st |= SPEC_ROW_BAD_PAGE;
+  if (P.status && blockIdx.x == 0 && threadIdx.x == 0) P.status[b] = st;
+  cudaGridDependencySynchronize();  // from here on: the span kernels' results
+
+  const int D = P.D, G = P.G;
+  const bool on = lane * 4 < D;
+  const int to = own + n > 0 ? (own + n + kTile - 1) / kTile : 0;
+  const int rto = (n * G + P.rto - 1) / P.rto;
+  const uint32_t Wo = P.plan.tiles[w.B], x0 = P.plan.tiles[b], i0 = P.plan.items[b];
+  const int tp = (w.prefix + kTile - 1) / kTile;
+  const uint32_t pr0 = w.prefix ? P.plan.rows[b] : 0;
+  const int rtp = w.prefix ? (P.plan.rows[w.B] + P.rtp - 1) / P.rtp : 0;
+  const uint32_t Wp = static_cast<uint32_t>(rtp) * w.Hkv * tp;
+  for (int y = warp; y < MG_ROWS; y += MG_NT / 32) {
+    const int row = blockIdx.x * MG_ROWS + y;
+    if (row >= w.N * P.Hq) break;
+    const int i = row / P.Hq, h = row - i * P.Hq;
+    const int head = h / G, r = i * G + h - head * G;
+    float m = -INFINITY, sum = 0.0f;
+    float4 acc = {0, 0, 0, 0};
+    auto join = [&](const float *po, const float *pl, uint32_t first, uint32_t count, int rt, int rr) {
+      for (uint32_t s = first; s < first + count; ++s) {
+        const int64_t at = static_cast<int64_t>(s) * rt + rr;
+        const float v = pl[at];
+        if (v == -INFINITY) continue;
+        float4 x = {0, 0, 0, 0};
+        if (on) x = *reinterpret_cast<const float4 *>(po + at * D + lane * 4);
+        const float nm = v > m ? v : m;  // a NaN does not become the maximum
+        const float a = nm == -INFINITY ? 0.0f : ex2(m - nm), c = ex2(v - nm);
+        sum = sum * a + c;
+        acc.x = acc.x * a + x.x * c;
+        acc.y = acc.y * a + x.y * c;
+        acc.z = acc.z * a + x.z * c;
+        acc.w = acc.w * a + x.w * c;
+        m = nm;
+      }
+    };
+    if (!st && i < n) {
+      if (w.prefix) {
+        const uint32_t k = pr0 + r, item = head * rtp + k / P.rtp;
+        const uint32_t C = min(static_cast<uint32_t>(P.cp), Wp);
+        const uint32_t c0 = owner(item * tp, Wp, C), c1 = owner(item * tp + tp - 1, Wp, C);
+        join(P.qo, P.ql, item + c0, c1 - c0 + 1, P.rtp, k % P.rtp);
+      }
+      const uint32_t j = head * rto + r / P.rto, x = x0 + j * to;
+      const uint32_t C = min(static_cast<uint32_t>(P.co), Wo);
+      const uint32_t c0 = owner(x, Wo, C), c1 = owner(x + to - 1, Wo, C);
+      join(P.po, P.pl, i0 + j + c0, c1 - c0 + 1, P.rto, r % P.rto);
+    }
+    float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    float l = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+    if (st) f = l = __int_as_float(0x7fffffff);
+    const int64_t at = static_cast<int64_t>(b) * w.N * P.Hq + row;
+    if (on) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+      *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4) = lo;
+      *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4 + 2) = hi;
+    }
+    if (lane == 0 && P.lse) P.lse[at] = l;
+  }
+}
+
+int row_warps(int64_t rows) { return rows > 48 ? 4 : static_cast<int>((rows + 15) / 16); }
+
+struct Layout {
+  int wo, wp;               // row warps of own and prefix items
+  int64_t tiles_o, tiles_p; // key tiles at most
+  size_t plan, po, pl, qo, ql, bytes;
+};
+
+// Where each part of the workspace begins; false if the problem is too large.
+bool lay_out(const View &w, int D, int G, Layout &L) {
+  const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const int64_t ro = static_cast<int64_t>(w.N) * G, rp = ro * w.B;
+  if (rp > (1 << 30)) return false;
+  L.wo = row_warps(ro);
+  L.wp = row_warps(rp);
+  const int64_t io = (ro + 16 * L.wo - 1) / (16 * L.wo) * w.Hkv * w.B;
+  const int64_t ip = w.prefix ? (rp + 16 * L.wp - 1) / (16 * L.wp) * w.Hkv : 0;
+  const int64_t cap = (static_cast<int64_t>(w.max_pages) << w.ps_log2);
+  L.tiles_o = io * ((cap + kTile - 1) / kTile);
+  L.tiles_p = ip * ((w.prefix + static_cast<int64_t>(kTile) - 1) / kTile);
+  if (io > INT32_MAX / 2 || ip > INT32_MAX / 2 || L.tiles_o > INT32_MAX || L.tiles_p > INT32_MAX)
+    return false;
+  const size_t so = static_cast<size_t>(io + kMaxGrid) * 16 * L.wo;
+  const size_t sp = ip ? static_cast<size_t>(ip + kMaxGrid) * 16 * L.wp : 0;
+  L.plan = 0;
+  L.po = up(3 * sizeof(uint32_t) * (w.B + 1));
+  L.pl = up(L.po + so * D * 4);
+  L.qo = up(L.pl + so * 4);
+  L.ql = up(L.qo + sp * D * 4);
+  L.bytes = up(L.ql + sp * 4);
+  return true;
+}
+
+span_launch_fn span_of(int format, int D) {
+  if (format == SPEC_KV_E4M3)
+    return D == 64 ? span_e4m3_64 : D == 80 ? span_e4m3_80 : D == 96 ? span_e4m3_96 : span_e4m3_128;
+  return D == 64 ? span_bf16_64 : D == 80 ? span_bf16_80 : D == 96 ? span_bf16_96 : span_bf16_128;
+}
+
+}  // namespace
+
+extern "C" size_t spec_attend_workspace_size(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                                             int32_t n_heads) {
+  View w;
+  Layout L;
+  if (!cache || !batch) return 0;
+  spec_kv_cache c = *cache;  // the size goes by shapes: pointers may be unset
+  spec_kv_batch s = *batch;
+  c.k_pages = c.v_pages = reinterpret_cast<void *>(256);
+  c.k_exp = c.v_exp = reinterpret_cast<int8_t *>(256);
+  s.page_table = s.prefix_table = s.kv_len = reinterpret_cast<const int32_t *>(256);
+  if (make_view(&c, &s, true, w) != SPEC_OK || n_heads < 1 || n_heads % w.Hkv) return 0;
+  return lay_out(w, c.head_dim, n_heads / w.Hkv, L) ? L.bytes : 0;
+}
+
+extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                                   const void *q, int32_t n_heads, const int64_t *q_strides,
+                                   float scale, void *out, float *lse, int32_t *row_status,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+  SpanParams P = {};
+  const spec_status st = make_view(cache, batch, true, P.w);
+  if (st != SPEC_OK) return st;
+  if (n_heads < 1 || n_heads % P.w.Hkv || !q_strides || !(scale >= 0.0f) || !(scale < INFINITY))
+    return SPEC_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (q_strides[i] < 0) return SPEC_ERR_INVALID_ARG;
+  if (P.w.B == 0) return SPEC_OK;
+  const uintptr_t qa = reinterpret_cast<uintptr_t>(q);
+  if (!q || !out || qa % 2 || reinterpret_cast<uintptr_t>(out) % 4 ||
+      reinterpret_cast<uintptr_t>(lse) % 4)
+    return SPEC_ERR_INVALID_ARG;
+  const int G = n_heads / P.w.Hkv, D = cache->head_dim;
+  Layout L;
+  if (!lay_out(P.w, D, G, L)) return SPEC_ERR_UNSUPPORTED;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.bytes)
+    return SPEC_ERR_WORKSPACE;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  P.plan.tiles = reinterpret_cast<uint32_t *>(ws + L.plan);
+  P.plan.items = P.plan.tiles + P.w.B + 1;
+  P.plan.rows = P.plan.items + P.w.B + 1;
+  P.q = static_cast<const __nv_bfloat16 *>(q);
+  P.qs0 = q_strides[0], P.qs1 = q_strides[1], P.qs2 = q_strides[2];
+  P.qvec = ((qa | static_cast<uintptr_t>((q_strides[0] | q_strides[1] | q_strides[2]) * 2)) & 3) == 0;
+  P.c = scale * 1.4426950408889634f;
+  P.G = G;
+  const span_launch_fn span = span_of(cache->format, D);
+  MP m = {};
+  m.w = P.w;
+  m.plan = P.plan;
+  m.G = G, m.Hq = n_heads, m.D = D, m.rto = 16 * L.wo, m.rtp = 16 * L.wp;
+  m.out = static_cast<__nv_bfloat16 *>(out);
+  m.lse = lse;
+  m.status = row_status;
+  if (P.w.prefix) {
+    P.prefix = 1;
+    P.po = reinterpret_cast<float *>(ws + L.qo);
+    P.pl = reinterpret_cast<float *>(ws + L.ql);
+    m.qo = P.po, m.ql = P.pl;
+    if (span(P, L.wp, L.tiles_p, &m.cp, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  }
+  P.prefix = 0;
+  P.po = reinterpret_cast<float *>(ws + L.po);
+  P.pl = reinterpret_cast<float *>(ws + L.pl);
+  m.po = P.po, m.pl = P.pl;
+  if (span(P, L.wo, L.tiles_o, &m.co, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((P.w.N * n_heads + MG_ROWS - 1) / MG_ROWS, P.w.B);
+  cfg.blockDim = dim3(MG_NT);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel, m) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}

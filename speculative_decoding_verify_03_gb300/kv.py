@@ -1,0 +1,279 @@
+"""The key/value cache of the verify step and the attention that reads it:
+the binding of include/spec_kv.h."""
+from __future__ import annotations
+
+import ctypes
+import threading
+
+SPEC_KV_BF16, SPEC_KV_E4M3 = 0, 1
+ROW_BAD_LENGTH, ROW_BAD_PAGE = 1 << 7, 1 << 8
+
+
+class SpecKvCache(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
+
+
+class SpecKvBatch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("gamma_max", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("prefix_len", ctypes.c_int32),
+                ("table_row_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
+                ("prefix_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("gamma_per_row", ctypes.c_void_p)]
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+def declare(L):
+    """Argument types of the library's functions."""
+    vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
+    # structures and stride arrays go by address (ctypes.byref)
+    L.spec_kv_append.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp]
+    L.spec_kv_append.restype = ctypes.c_int
+    L.spec_kv_read.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    L.spec_kv_read.restype = ctypes.c_int
+    L.spec_attend_workspace_size.argtypes = [vp, vp, i32]
+    L.spec_attend_workspace_size.restype = sz
+    L.spec_attend.argtypes = [vp, vp, vp, i32, vp, ctypes.c_float, vp, vp, vp, vp, sz, vp]
+    L.spec_attend.restype = ctypes.c_int
+
+
+class KVCache:
+    """A paged cache on the GPU: k_pages and v_pages [n_pages, n_kv_heads,
+    page_size, head_dim], bfloat16, or float8_e4m3fn with k_exp and v_exp
+    [n_pages, n_kv_heads, page_size] int8 (a stored y stands for y * 2^e).
+    Pages may be strided (both halves of one allocation, say); what is inside
+    a page is contiguous.  The tensors are the caller's: the cache keeps them
+    alive and describes them to the library."""
+
+    def __init__(self, k_pages, v_pages, k_exp=None, v_exp=None):
+        import torch
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages must be [n_pages, n_kv_heads, page_size, head_dim]")
+        if k_pages.dtype != v_pages.dtype or k_pages.dtype not in (torch.bfloat16,
+                                                                   torch.float8_e4m3fn):
+            raise TypeError("pages must be bfloat16 or float8_e4m3fn")
+        n, H, S, D = k_pages.shape
+        if n and not (k_pages[0].is_contiguous() and v_pages[0].is_contiguous()):
+            raise ValueError("the inside of a page must be contiguous")
+        if k_pages.dtype == torch.float8_e4m3fn:
+            for t in (k_exp, v_exp):
+                if t is None or t.dtype != torch.int8:
+                    raise TypeError("an e4m3 cache needs int8 k_exp and v_exp")
+                if t.shape != (n, H, S) or not t.is_contiguous():
+                    raise ValueError("k_exp and v_exp must be contiguous [n_pages, n_kv_heads, page_size]")
+            fmt = SPEC_KV_E4M3
+        else:
+            if k_exp is not None or v_exp is not None:
+                raise ValueError("a bfloat16 cache has no exponents")
+            fmt = SPEC_KV_BF16
+        for t in (v_pages, k_exp, v_exp):
+            if t is not None and t.device != k_pages.device:
+                raise ValueError("the cache's tensors must be on one device")
+        self.k_pages, self.v_pages, self.k_exp, self.v_exp = k_pages, v_pages, k_exp, v_exp
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = n, H, S, D
+        self.device = k_pages.device
+        ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        self.struct = SpecKvCache(ptr(k_pages), ptr(v_pages), ptr(k_exp), ptr(v_exp),
+                                  k_pages.stride(0) if n else H * S * D,
+                                  v_pages.stride(0) if n else H * S * D, n, S, H, D, fmt)
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
+        """A cache of new pages; dtype float8_e4m3fn (the default) or bfloat16."""
+        import torch
+        dtype = dtype or torch.float8_e4m3fn
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+        if dtype == torch.bfloat16:
+            return cls(k, v)
+        return cls(k, v, *(torch.empty(shape[:3], dtype=torch.int8, device=device) for _ in range(2)))
+
+
+
+
+def _int32(name, t, shape, device):
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be {list(shape)} on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _batch(cache, page_table, kv_len, gamma_max, prefix_table, prefix_len, gamma_per_row):
+    import torch
+    B, dev = kv_len.shape[0], cache.device
+    _int32("kv_len", kv_len, (B,), dev)
+    if page_table.dtype != torch.int32:
+        raise TypeError("page_table must be int32")
+    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.device != dev:
+        raise ValueError(f"page_table must be [{B}, max_pages] on {dev}")
+    mp = page_table.shape[1]
+    if B and mp and page_table.stride(1) != 1:
+        raise ValueError("page_table rows must be contiguous")
+    if gamma_per_row is not None:
+        _int32("gamma_per_row", gamma_per_row, (B,), dev)
+    prefix_len = int(prefix_len)
+    pt = None
+    if prefix_len > 0:
+        need = -(-prefix_len // cache.page_size)
+        if prefix_table is None or prefix_table.dim() != 1 or prefix_table.shape[0] < need:
+            raise ValueError(f"prefix_table must hold the prefix's {need} page ids")
+        _int32("prefix_table", prefix_table, prefix_table.shape, dev)
+        pt = prefix_table.data_ptr()
+    return SpecKvBatch(B, gamma_max, mp, prefix_len, page_table.stride(0) if B > 1 else mp,
+                       page_table.data_ptr(), pt, kv_len.data_ptr(),
+                       gamma_per_row.data_ptr() if gamma_per_row is not None else None)
+
+
+def _check(code):
+    if code != 0:
+        from . import _check as check
+        check(code)
+
+
+def _lib_stream(stream, device):
+    from . import lib
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    return lib(), s.cuda_stream
+
+
+def _status(with_status, B, device):
+    import torch
+    return torch.empty(B, dtype=torch.int32, device=device) if with_status else None
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def spec_kv_append(cache, k, v, page_table, kv_len, gamma_per_row=None, prefix_len=0,
+                   with_status=False, stream=None):
+    """Append a step's keys and values to the cache (see spec_kv_append in
+    include/spec_kv.h): k and v [B, n, n_kv_heads, head_dim] float32 or
+    bfloat16 (any strides, contiguous head_dim), token t of sequence b to
+    position kv_len[b] + t; with gamma_per_row [B] int32, sequence b has
+    gamma_b + 1 tokens.  page_table [B, max_pages] int32 holds the sequences'
+    own pages, whose first position is prefix_len.  Updates the cache in
+    place; returns row_status [B] when with_status, else None."""
+    from . import _dtype_code
+    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must be [B, n, n_kv_heads, head_dim] of one dtype")
+    B, n, H, D = k.shape
+    if (H, D) != (cache.n_kv_heads, cache.head_dim) or B != kv_len.shape[0] or n < 1:
+        raise ValueError("k and v do not match the cache's heads or kv_len's rows")
+    if k.device != cache.device or v.device != cache.device:
+        raise ValueError(f"k and v must be on {cache.device}")
+    if k.stride(3) != 1 or v.stride(3) != 1:
+        raise ValueError("the head_dim axis must be contiguous")
+    dtype = _dtype_code(k)
+    b = _batch(cache, page_table, kv_len, n - 1, None, 0, gamma_per_row)
+    b.prefix_len = prefix_len = int(prefix_len)
+    if prefix_len > 0:
+        b.prefix_table = page_table.data_ptr()  # not read: the step is past the prefix
+    st = _status(with_status, B, cache.device)
+    L, s = _lib_stream(stream, cache.device)
+    _check(L.spec_kv_append(cache.ref, ctypes.byref(b), k.data_ptr(), v.data_ptr(), dtype,
+                            ctypes.byref(_Strides(*k.stride()[:3])),
+                            ctypes.byref(_Strides(*v.stride()[:3])), _ptr(st), s))
+    return st
+
+
+def spec_kv_read(cache, page_table, kv_len, n, begin=0, prefix_table=None, prefix_len=0,
+                 dtype=None, with_status=False, stream=None):
+    """Read positions begin .. begin + n - 1 of every sequence back (see
+    spec_kv_read in include/spec_kv.h): returns (k, v) [B, n, n_kv_heads,
+    head_dim] in dtype (bfloat16 by default, or float32), zeros from kv_len[b]
+    on, and row_status [B] when with_status."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("dtype must be bfloat16 or float32")
+    b = _batch(cache, page_table, kv_len, 0, prefix_table, prefix_len, None)
+    shape = (b.B, int(n), cache.n_kv_heads, cache.head_dim)
+    if n < 0 or begin < 0:
+        raise ValueError("begin and n must not be negative")
+    k, v = (torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+    st = _status(with_status, b.B, cache.device)
+    L, s = _lib_stream(stream, cache.device)
+    _check(L.spec_kv_read(cache.ref, ctypes.byref(b), int(begin), int(n),
+                          0 if dtype == torch.float32 else 1, k.data_ptr(), v.data_ptr(), _ptr(st), s))
+    return (k, v, st) if with_status else (k, v)
+
+
+_ws_lock = threading.Lock()
+_ws = {}
+
+
+def attend_workspace_bytes(cache, batch, n_heads) -> int:
+    """Workspace bytes of spec_attend for these shapes (a SpecKvBatch)."""
+    from . import lib
+    return int(lib().spec_attend_workspace_size(cache.ref, ctypes.byref(batch), int(n_heads)))
+
+
+def _attend_workspace(cache, batch, n_heads, stream_ptr):
+    """A workspace cached per device and stream (calls on one stream run in order)."""
+    import torch
+    need = attend_workspace_bytes(cache, batch, n_heads)
+    key = (cache.device.index, stream_ptr)
+    with _ws_lock:
+        buf = _ws.get(key)
+        if buf is None or buf.numel() < need:
+            buf = torch.empty(max(need, 4096), dtype=torch.uint8, device=cache.device)
+            _ws[key] = buf
+    return buf
+
+
+def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, gamma_per_row=None,
+                scale=None, workspace="auto", out=None, with_status=False, stream=None):
+    """The verify step's attention (see spec_attend in include/spec_kv.h): q
+    [B, gamma_max + 1, n_heads, head_dim] bfloat16 (any strides, contiguous
+    head_dim); query i of sequence b attends to positions 0 .. kv_len[b] + i,
+    the first prefix_len of them in the shared pages prefix_table, the others
+    in the sequence's own pages page_table[b].  The step's keys and values are
+    in the cache already.  scale defaults to head_dim ** -0.5.  workspace:
+    "auto" (cached per device and stream) or a uint8 CUDA tensor.  out: a pair
+    of contiguous tensors for the results, or None.  Returns (out [B,
+    gamma_max + 1, n_heads, head_dim] bfloat16, lse [B, gamma_max + 1, n_heads]
+    float32), and row_status [B] when with_status."""
+    import torch
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if q.dim() != 4 or q.shape[0] != kv_len.shape[0] or q.shape[1] < 1 or q.shape[3] != cache.head_dim:
+        raise ValueError("q must be [B, gamma_max + 1, n_heads, head_dim]")
+    if q.device != cache.device:
+        raise ValueError(f"q must be on {cache.device}")
+    if q.stride(3) != 1:
+        raise ValueError("the head_dim axis must be contiguous")
+    B, N, Hq, D = q.shape
+    if Hq < 1 or Hq % cache.n_kv_heads:
+        raise ValueError("n_heads must be a multiple of the cache's n_kv_heads")
+    b = _batch(cache, page_table, kv_len, N - 1, prefix_table, prefix_len, gamma_per_row)
+    L, s = _lib_stream(stream, cache.device)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto' or a tensor")
+        workspace = _attend_workspace(cache, b, Hq, s)
+    if out is None:
+        o = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=cache.device)
+        lse = torch.empty((B, N, Hq), dtype=torch.float32, device=cache.device)
+    else:
+        o, lse = out
+        if (o.shape != (B, N, Hq, D) or o.dtype != torch.bfloat16 or not o.is_contiguous() or
+                lse.shape != (B, N, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+            raise ValueError("out must be contiguous bfloat16 and float32 tensors of the results' shapes")
+    st = _status(with_status, B, cache.device)
+    _check(L.spec_attend(cache.ref, ctypes.byref(b), q.data_ptr(), Hq,
+                         ctypes.byref(_Strides(*q.stride()[:3])),
+                         D ** -0.5 if scale is None else float(scale), o.data_ptr(), lse.data_ptr(),
+                         _ptr(st), workspace.data_ptr(), workspace.numel(), s))
+    return (o, lse, st) if with_status else (o, lse)
