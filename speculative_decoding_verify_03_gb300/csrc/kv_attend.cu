@@ -14,7 +14,7 @@ namespace {
 using namespace kv;
 
 constexpr int MG_NT = 256;
-constexpr int MG_ROWS = 32;  // rows per CTA
+constexpr int MG_ROWS = MG_NT / 32;  // rows per CTA: one per warp
 
 struct MP {
   View w;
@@ -23,7 +23,8 @@ struct MP {
   __nv_bfloat16 *out;
   float *lse;
   int32_t *status;
-  int32_t G, Hq, D, rto, rtp, co, cp;  // rows per item and CTAs, own and prefix
+  int32_t G, Hq, D;
+  int32_t rto, rtp, co, cp, kp;  // rows per item and CTAs, own and prefix; key tokens of a prefix tile
 };
 
 __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP P) {
@@ -40,67 +41,79 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
     for (int p = threadIdx.x; p < (w.prefix + pm) >> w.ps_log2; p += MG_NT)
       bad |= static_cast<uint32_t>(__ldg(w.ptable + p)) >= np;
   }
-  if (__syncthreads_or(bad)) st |= SPEC_ROW_BAD_PAGE;
-  if (P.status && blockIdx.x == 0 && threadIdx.x == 0) P.status[b] = st;
   cudaGridDependencySynchronize();  // from here on: the span kernels' results
+  int lost = 0;
+  if (P.plan.lost)
+    for (int c = threadIdx.x; c < P.cp; c += MG_NT) lost |= P.plan.lost[c];
+  if (__syncthreads_or(bad)) st |= SPEC_ROW_BAD_PAGE;
+  if (__syncthreads_or(lost)) st |= SPEC_ROW_WAIT_TIMEOUT;
+  if (P.status && blockIdx.x == 0 && threadIdx.x == 0) P.status[b] = st;
 
   const int D = P.D, G = P.G;
+  const int row = blockIdx.x * MG_ROWS + warp;
+  if (row >= w.N * P.Hq) return;
   const bool on = lane * 4 < D;
-  const int to = own + n > 0 ? (own + n + kTile - 1) / kTile : 0;
-  const int rto = (n * G + P.rto - 1) / P.rto;
-  const uint32_t Wo = P.plan.tiles[w.B], x0 = P.plan.tiles[b], i0 = P.plan.items[b];
-  const int tp = (w.prefix + kTile - 1) / kTile;
-  const uint32_t pr0 = w.prefix ? P.plan.rows[b] : 0;
-  const int rtp = w.prefix ? (P.plan.rows[w.B] + P.rtp - 1) / P.rtp : 0;
-  const uint32_t Wp = static_cast<uint32_t>(rtp) * w.Hkv * tp;
-  for (int y = warp; y < MG_ROWS; y += MG_NT / 32) {
-    const int row = blockIdx.x * MG_ROWS + y;
-    if (row >= w.N * P.Hq) break;
-    const int i = row / P.Hq, h = row - i * P.Hq;
-    const int head = h / G, r = i * G + h - head * G;
-    float m = -INFINITY, sum = 0.0f;
-    float4 acc = {0, 0, 0, 0};
-    auto join = [&](const float *po, const float *pl, uint32_t first, uint32_t count, int rt, int rr) {
-      for (uint32_t s = first; s < first + count; ++s) {
-        const int64_t at = static_cast<int64_t>(s) * rt + rr;
-        const float v = pl[at];
-        if (v == -INFINITY) continue;
+  const int i = row / P.Hq, h = row - i * P.Hq;
+  const int head = h / G, r = i * G + h - head * G;
+  float m = -INFINITY, sum = 0.0f;
+  float4 acc = {0, 0, 0, 0};
+  // Slots first .. first + count - 1, 32 at a time: a lane per slot for the
+  // weights, then the outputs, whose loads do not depend on one another.
+  auto join = [&](const float *po, const float *pl, uint32_t first, int count, int rt, int rr) {
+    for (int s0 = 0; s0 < count; s0 += 32) {
+      const int k = min(32, count - s0);
+      const int64_t at = static_cast<int64_t>(first + s0) * rt + rr;
+      const float v = lane < k ? pl[at + static_cast<int64_t>(lane) * rt] : -INFINITY;
+      float nm = v;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, o));
+      nm = fmaxf(nm, m);  // a NaN does not become the maximum
+      const float a = nm == -INFINITY ? 1.0f : ex2(m - nm);
+      const float c = v == -INFINITY ? 0.0f : ex2(v - nm);
+      float s = c;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+      sum = sum * a + s;
+      acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
+#pragma unroll 4
+      for (int j = 0; j < k; ++j) {
+        const float f = __shfl_sync(~0u, c, j);
         float4 x = {0, 0, 0, 0};
-        if (on) x = *reinterpret_cast<const float4 *>(po + at * D + lane * 4);
-        const float nm = v > m ? v : m;  // a NaN does not become the maximum
-        const float a = nm == -INFINITY ? 0.0f : ex2(m - nm), c = ex2(v - nm);
-        sum = sum * a + c;
-        acc.x = acc.x * a + x.x * c;
-        acc.y = acc.y * a + x.y * c;
-        acc.z = acc.z * a + x.z * c;
-        acc.w = acc.w * a + x.w * c;
-        m = nm;
+        if (on) x = __ldcg(reinterpret_cast<const float4 *>(po + (at + static_cast<int64_t>(j) * rt) * D + lane * 4));
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
       }
-    };
-    if (!st && i < n) {
-      if (w.prefix) {
-        const uint32_t k = pr0 + r, item = head * rtp + k / P.rtp;
-        const uint32_t C = min(static_cast<uint32_t>(P.cp), Wp);
-        const uint32_t c0 = owner(item * tp, Wp, C), c1 = owner(item * tp + tp - 1, Wp, C);
-        join(P.qo, P.ql, item + c0, c1 - c0 + 1, P.rtp, k % P.rtp);
-      }
-      const uint32_t j = head * rto + r / P.rto, x = x0 + j * to;
-      const uint32_t C = min(static_cast<uint32_t>(P.co), Wo);
-      const uint32_t c0 = owner(x, Wo, C), c1 = owner(x + to - 1, Wo, C);
-      join(P.po, P.pl, i0 + j + c0, c1 - c0 + 1, P.rto, r % P.rto);
+      m = nm;
     }
-    float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-    float l = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
-    if (st) f = l = __int_as_float(0x7fffffff);
-    const int64_t at = static_cast<int64_t>(b) * w.N * P.Hq + row;
-    if (on) {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f);
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-      *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4) = lo;
-      *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4 + 2) = hi;
+  };
+  if (!st && i < n) {
+    if (w.prefix) {
+      const int tp = (w.prefix + P.kp - 1) / P.kp;
+      const int nj = (P.plan.rows[w.B] + P.rtp - 1) / P.rtp;
+      const uint32_t W = static_cast<uint32_t>(nj) * w.Hkv * tp, C = min(static_cast<uint32_t>(P.cp), W);
+      const uint32_t k = P.plan.rows[b] + r, item = head * nj + k / P.rtp;
+      const uint32_t c0 = owner(item * tp, W, C), c1 = owner(item * tp + tp - 1, W, C);
+      join(P.qo, P.ql, item + c0, c1 - c0 + 1, P.rtp, k % P.rtp);
     }
-    if (lane == 0 && P.lse) P.lse[at] = l;
+    const int to = (own + n + kTile - 1) / kTile, nj = (n * G + P.rto - 1) / P.rto;
+    const uint32_t W = P.plan.tiles[w.B], C = min(static_cast<uint32_t>(P.co), W);
+    const uint32_t j = head * nj + r / P.rto, x = P.plan.tiles[b] + j * to;
+    const uint32_t c0 = owner(x, W, C), c1 = owner(x + to - 1, W, C);
+    join(P.po, P.pl, P.plan.items[b] + j + c0, c1 - c0 + 1, P.rto, r % P.rto);
   }
+  float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  float l = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+  if (st) f = l = __int_as_float(0x7fffffff);
+  const int64_t at = static_cast<int64_t>(b) * w.N * P.Hq + row;
+  if (on) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+    *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4) = lo;
+    *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4 + 2) = hi;
+  }
+  if (lane == 0 && P.lse) P.lse[at] = l;
 }
 
 int row_warps(int64_t rows) { return rows > 48 ? 4 : static_cast<int>((rows + 15) / 16); }
@@ -119,7 +132,7 @@ bool lay_out(const View &w, int D, int G, Layout &L) {
   L.wo = row_warps(ro);
   L.wp = row_warps(rp);
   const int64_t io = (ro + 16 * L.wo - 1) / (16 * L.wo) * w.Hkv * w.B;
-  const int64_t ip = w.prefix ? (rp + 16 * L.wp - 1) / (16 * L.wp) * w.Hkv : 0;
+  const int64_t ip = w.prefix && rp ? (rp + 16 * L.wp - 1) / (16 * L.wp) * w.Hkv : 0;
   const int64_t cap = (static_cast<int64_t>(w.max_pages) << w.ps_log2);
   L.tiles_o = io * ((cap + kTile - 1) / kTile);
   L.tiles_p = ip * ((w.prefix + static_cast<int64_t>(kTile) - 1) / kTile);
@@ -193,7 +206,7 @@ extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_bat
   MP m = {};
   m.w = P.w;
   m.plan = P.plan;
-  m.G = G, m.Hq = n_heads, m.D = D, m.rto = 16 * L.wo, m.rtp = 16 * L.wp;
+  m.G = G, m.Hq = n_heads, m.D = D, m.rto = 16 * L.wo, m.rtp = 16 * L.wp, m.kp = kTile;
   m.out = static_cast<__nv_bfloat16 *>(out);
   m.lse = lse;
   m.status = row_status;

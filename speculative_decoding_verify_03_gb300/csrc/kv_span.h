@@ -22,6 +22,7 @@ struct Plan {            // device arrays of B + 1 words
   uint32_t *tiles;       // own: key tiles of the sequences before b
   uint32_t *items;       // own: items of the sequences before b
   uint32_t *rows;        // prefix: query rows (per key/value head) before b
+  uint32_t *lost;        // prefix, per CTA: a wait gave up (null: no kernel with waits ran)
 };
 
 struct SpanParams {

@@ -286,6 +286,24 @@ def test_attend_query_sizes(sv, fmt, q_scale):
     check_attend(got, ref, fmt, g)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("D,Hq,Hkv,N", [(64, 16, 8, 1), (80, 8, 8, 3), (96, 24, 8, 9), (128, 32, 8, 5)])
+def test_attend_many_tiles(sv, fmt, D, Hq, Hkv, N):
+    """More key tiles than any number of CTAs takes at once: long items."""
+    got, ref, g = attend_case(sv, 15, fmt, 4, N, Hq, Hkv, D, 64, 3000, [7000, 1, 4097, 5500])
+    check_attend(got, ref, fmt, g)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("D,Hq,N", [(64, 8, 9), (128, 16, 4)])
+def test_attend_many_items(sv, fmt, D, Hq, N):
+    """More short items than any number of CTAs takes at once."""
+    rng = np.random.default_rng(16)
+    B = 200
+    got, ref, g = attend_case(sv, 16, fmt, B, N, Hq, 8, D, 16, 130, rng.integers(0, 200, B), gammas=rng.integers(0, N, B))
+    check_attend(got, ref, fmt, g)
+
+
 def test_attend_scale(sv):
     got, ref, g = attend_case(sv, 14, "e4m3", 2, 2, 4, 2, 128, 16, 20, [50, 7], scale=0.25)
     check_attend(got, ref, "e4m3", g)
