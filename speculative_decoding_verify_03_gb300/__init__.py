@@ -22,10 +22,12 @@ _SOURCES = [os.path.join(_HERE, "csrc", f) for f in ("spec_verify.cu", "spec_str
                                                       "kv_attend.cu", "kv_span_e4m3_64_80.cu",
                                                       "kv_span_e4m3_96_128.cu",
                                                       "kv_span_bf16_64_80.cu",
-                                                      "kv_span_bf16_96_128.cu")]
+                                                      "kv_span_bf16_96_128.cu", "kv_dense_e4m3.cu",
+                                                      "kv_dense_bf16.cu")]
 _DEPS = _SOURCES + [os.path.join(_HERE, "csrc", f)
                     for f in ("sv_common.cuh", "sv_core.cuh", "sv_strip.h", "sv_row.h",
-                              "sv_verify.h", "kv_common.cuh", "kv_span.h", "kv_span.cuh")] + [
+                              "sv_verify.h", "kv_common.cuh", "kv_span.h", "kv_span.cuh",
+                              "kv_dense.cuh", "kv_tc.cuh")] + [
     os.path.join(_ROOT, "include", h) for h in ("spec_verify.h", "spec_kv.h")]
 
 SPEC_F32, SPEC_BF16 = 0, 1

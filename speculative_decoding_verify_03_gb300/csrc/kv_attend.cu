@@ -118,8 +118,13 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
 
 int row_warps(int64_t rows) { return rows > 48 ? 4 : static_cast<int>((rows + 15) / 16); }
 
+// Query rows (of a key/value head) from which the prefix goes to the dense kernel.
+constexpr int64_t kDenseRows = 65;
+
 struct Layout {
   int wo, wp;               // row warps of own and prefix items
+  bool dense;
+  int rp, kp;               // rows and key tokens of a prefix tile
   int64_t tiles_o, tiles_p; // key tiles at most
   size_t plan, po, pl, qo, ql, bytes;
 };
@@ -131,17 +136,20 @@ bool lay_out(const View &w, int D, int G, Layout &L) {
   if (rp > (1 << 30)) return false;
   L.wo = row_warps(ro);
   L.wp = row_warps(rp);
+  L.dense = w.prefix > 0 && rp >= kDenseRows;
+  L.rp = L.dense ? DN_ROWS : 16 * L.wp;
+  L.kp = L.dense ? 128 : kTile;
   const int64_t io = (ro + 16 * L.wo - 1) / (16 * L.wo) * w.Hkv * w.B;
-  const int64_t ip = w.prefix && rp ? (rp + 16 * L.wp - 1) / (16 * L.wp) * w.Hkv : 0;
+  const int64_t ip = w.prefix && rp ? (rp + L.rp - 1) / L.rp * w.Hkv : 0;
   const int64_t cap = (static_cast<int64_t>(w.max_pages) << w.ps_log2);
   L.tiles_o = io * ((cap + kTile - 1) / kTile);
-  L.tiles_p = ip * ((w.prefix + static_cast<int64_t>(kTile) - 1) / kTile);
+  L.tiles_p = ip * ((w.prefix + static_cast<int64_t>(L.kp) - 1) / L.kp);
   if (io > INT32_MAX / 2 || ip > INT32_MAX / 2 || L.tiles_o > INT32_MAX || L.tiles_p > INT32_MAX)
     return false;
   const size_t so = static_cast<size_t>(io + kMaxGrid) * 16 * L.wo;
-  const size_t sp = ip ? static_cast<size_t>(ip + kMaxGrid) * 16 * L.wp : 0;
+  const size_t sp = ip ? static_cast<size_t>(ip + kMaxGrid) * L.rp : 0;
   L.plan = 0;
-  L.po = up(3 * sizeof(uint32_t) * (w.B + 1));
+  L.po = up(sizeof(uint32_t) * (3 * (w.B + 1) + kMaxGrid));
   L.pl = up(L.po + so * D * 4);
   L.qo = up(L.pl + so * 4);
   L.ql = up(L.qo + sp * D * 4);
@@ -197,16 +205,17 @@ extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_bat
   P.plan.tiles = reinterpret_cast<uint32_t *>(ws + L.plan);
   P.plan.items = P.plan.tiles + P.w.B + 1;
   P.plan.rows = P.plan.items + P.w.B + 1;
+  P.plan.lost = L.dense ? P.plan.rows + P.w.B + 1 : nullptr;
   P.q = static_cast<const __nv_bfloat16 *>(q);
   P.qs0 = q_strides[0], P.qs1 = q_strides[1], P.qs2 = q_strides[2];
-  P.qvec = ((qa | static_cast<uintptr_t>((q_strides[0] | q_strides[1] | q_strides[2]) * 2)) & 3) == 0;
+  const uintptr_t qbits = qa | static_cast<uintptr_t>((q_strides[0] | q_strides[1] | q_strides[2]) * 2);
   P.c = scale * 1.4426950408889634f;
   P.G = G;
   const span_launch_fn span = span_of(cache->format, D);
   MP m = {};
   m.w = P.w;
   m.plan = P.plan;
-  m.G = G, m.Hq = n_heads, m.D = D, m.rto = 16 * L.wo, m.rtp = 16 * L.wp, m.kp = kTile;
+  m.G = G, m.Hq = n_heads, m.D = D, m.rto = 16 * L.wo, m.rtp = L.rp, m.kp = L.kp;
   m.out = static_cast<__nv_bfloat16 *>(out);
   m.lse = lse;
   m.status = row_status;
@@ -215,9 +224,14 @@ extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_bat
     P.po = reinterpret_cast<float *>(ws + L.qo);
     P.pl = reinterpret_cast<float *>(ws + L.ql);
     m.qo = P.po, m.ql = P.pl;
-    if (span(P, L.wp, L.tiles_p, &m.cp, s) != cudaSuccess) return SPEC_ERR_CUDA;
+    P.qvec = qbits % (L.dense ? 16 : 4) == 0;
+    const cudaError_t e = !L.dense ? span(P, L.wp, L.tiles_p, &m.cp, s)
+                          : cache->format == SPEC_KV_E4M3 ? dense_e4m3(P, D, L.tiles_p, &m.cp, s)
+                                                          : dense_bf16(P, D, L.tiles_p, &m.cp, s);
+    if (e != cudaSuccess) return SPEC_ERR_CUDA;
   }
   P.prefix = 0;
+  P.qvec = qbits % 4 == 0;
   P.po = reinterpret_cast<float *>(ws + L.po);
   P.pl = reinterpret_cast<float *>(ws + L.pl);
   m.po = P.po, m.pl = P.pl;

@@ -34,7 +34,7 @@ struct SpanParams {
   float c;                // scale * log2 e
   int32_t G;              // query heads per key/value head
   int32_t prefix;         // 1: prefix items
-  bool qvec;              // q rows are 16-byte aligned
+  bool qvec;              // q rows are 4-byte (span) or 16-byte (dense) aligned
 };
 
 // Launches the span kernel for RT = 16 * wr rows (wr 1 .. 4) on at most
@@ -49,6 +49,11 @@ cudaError_t span_bf16_64(const SpanParams &, int, int64_t, int *, cudaStream_t);
 cudaError_t span_bf16_80(const SpanParams &, int, int64_t, int *, cudaStream_t);
 cudaError_t span_bf16_96(const SpanParams &, int, int64_t, int *, cudaStream_t);
 cudaError_t span_bf16_128(const SpanParams &, int, int64_t, int *, cudaStream_t);
+
+// The dense kernel: prefix items of DN_ROWS rows, tiles of 128 tokens.
+constexpr int DN_ROWS = 256;
+cudaError_t dense_e4m3(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
+cudaError_t dense_bf16(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
 
 // The CTA that works on tile x of W (C <= W CTAs): the largest c with W c / C <= x.
 __host__ __device__ __forceinline__ uint32_t owner(uint32_t x, uint32_t W, uint32_t C) {
