@@ -19,11 +19,11 @@
 // thread has a row of its own, so nothing is reduced across lanes; the weights
 // go back to TMEM over the scores, as the left operand of P V.
 //
-// Roles: warps 0-3 and 4-7 softmax and output of a row tile each; warps 8-11
-// bring queries, keys and values into shared memory (e4m3 through registers as
-// float16, half a tile in flight, bfloat16 by asynchronous copies); warps 12
-// and 13 issue the products of a row tile each, as soon as its operands are
-// there.  Two stages of keys and of values.
+// Roles: warps 0-3 and 4-7 queries, softmax and output of a row tile each; warps
+// 8-15 bring keys and values into shared memory (e4m3 through registers as
+// float16, a tile ahead, bfloat16 by asynchronous copies); warps 16 and 17
+// issue the products of a row tile each, as soon as its operands are there.
+// Two stages of keys and of values.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -33,12 +33,13 @@
 
 namespace kv {
 
-constexpr int DN_NT = 512;     // threads
+constexpr int DN_NT = 640;     // threads
+constexpr int DN_FETCH = 256;  // of them loading
 constexpr int DN_TILE = 128;   // key tokens per tile
 constexpr int DN_RING = 8;     // tiles whose exponents are kept
-// Registers per thread: softmax (2 warpgroups), loading, the rest.
-constexpr int DN_SOFT = 176, DN_LOAD = 112, DN_REST = 48;
-static_assert(2 * DN_SOFT + DN_LOAD + DN_REST <= 4 * 128, "registers");
+// Registers per thread: at launch (5 warpgroups), softmax (2), loading (2), the rest.
+constexpr int DN_REGS = 96, DN_SOFT = 112, DN_LOAD = 104, DN_REST = 48;
+static_assert(2 * DN_SOFT + 2 * DN_LOAD + DN_REST <= 5 * DN_REGS, "registers");
 
 template <int D>
 struct DenseCfg {
@@ -50,9 +51,8 @@ struct DenseCfg {
 struct DenseShared {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t sfull[2], pfull[2], odone[2], drain[2];  // per row tile
-  uint64_t consts[DN_RING], qfull, qempty;
+  uint64_t consts[DN_RING], qfull[2];
   int2 exps[DN_RING];        // E, F
-  float qc[DN_ROWS];         // score factor of a row
   uint32_t tmem, dead;
   uint32_t sum[DN_NT / 32];
 };
@@ -75,17 +75,17 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   // --- rows before each sequence
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      bar_init(s32(&S.kfull[i]), E4M3 ? 4 : 128), bar_init(s32(&S.kempty[i]), 2);
-      bar_init(s32(&S.vfull[i]), E4M3 ? 4 : 128), bar_init(s32(&S.vempty[i]), 2);
+      bar_init(s32(&S.kfull[i]), E4M3 ? DN_FETCH / 32 : DN_FETCH), bar_init(s32(&S.kempty[i]), 2);
+      bar_init(s32(&S.vfull[i]), E4M3 ? DN_FETCH / 32 : DN_FETCH), bar_init(s32(&S.vempty[i]), 2);
       bar_init(s32(&S.sfull[i]), 1), bar_init(s32(&S.pfull[i]), 4);
       bar_init(s32(&S.odone[i]), 1), bar_init(s32(&S.drain[i]), 1);
     }
     for (int i = 0; i < DN_RING; ++i) bar_init(s32(&S.consts[i]), 1);
-    bar_init(s32(&S.qfull), 4), bar_init(s32(&S.qempty), 2);
+    bar_init(s32(&S.qfull[0]), 4), bar_init(s32(&S.qfull[1]), 4);
     S.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) tmem_alloc(&S.tmem, 512);
+  if (warp == 16) tmem_alloc(&S.tmem, 512);
   const int per = (B + DN_NT - 1) / DN_NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
   uint32_t a = 0;
   for (int b = b0; b < b1; ++b) {
@@ -148,11 +148,62 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     int item = item0, tt = first0;
     float M = kNone, l = 0.0f, qc = 0.0f;
     bool fresh = true;
-    int g = 0;
     for (int t = 0; t < tiles; ++t) {
-      if (fresh) {
-        bar_wait(s32(&S.qfull), g & 1, dead);
-        qc = S.qc[r];
+      if (fresh) {  // the row's query; the products with the item before are done
+      {
+        const uint32_t row = item % nj * DN_ROWS + r;
+        uint4 v[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+        if (row < rows) {
+          int b = 0, h = B;
+          while (h - b > 1) {
+            const int m = (b + h) >> 1;
+            if (cum[m] <= row) b = m;
+            else h = m;
+          }
+          const int y = row - cum[b], i = y / G;
+          const __nv_bfloat16 *src = P.q + b * P.qs0 + i * P.qs1 + (item / nj * G + y - i * G) * P.qs2;
+          if (P.qvec) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) v[c] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+          } else {
+            const uint16_t *u = reinterpret_cast<const uint16_t *>(src);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              v[c].x = u[8 * c] | u[8 * c + 1] << 16, v[c].y = u[8 * c + 2] | u[8 * c + 3] << 16;
+              v[c].z = u[8 * c + 4] | u[8 * c + 5] << 16, v[c].w = u[8 * c + 6] | u[8 * c + 7] << 16;
+            }
+          }
+        }
+        qc = P.c;
+        if constexpr (E4M3) {
+          // bring the row's largest finite magnitude to [2^10, 2^11): exact in
+          // float16 for all elements above 2^-28 of it
+          uint32_t m = 0;
+          auto most = [&](uint32_t u) {
+            const uint32_t x = u & 0x7fffu, y = u >> 16 & 0x7fffu;
+            m = max(m, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
+          };
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) most(v[c].x), most(v[c].y), most(v[c].z), most(v[c].w);
+          const int eq = max(static_cast<int>(m >> 7) - 127 - 10, -100);
+          const float f = pow2i(-eq);
+          qc = P.c * pow2i(eq);
+          auto half2 = [&](uint32_t u) {
+            return pack<true>(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
+          };
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            v[c] = make_uint4(half2(v[c].x), half2(v[c].y), half2(v[c].z), half2(v[c].w));
+        }
+        const uint32_t qb = base + C::Q + half * C::OP + (r & 127) * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) sts128(qb + (c >> 3) * (DN_TILE * 128) + (((c ^ r) & 7) << 4), v[c]);
+      }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(s32(&S.qfull[half]));
         M = kNone, l = 0.0f;
       }
       float kt = qc, F = 0.0f, invF = 1.0f;
@@ -165,22 +216,30 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       }
       bar_wait(s32(&S.sfull[half]), t & 1, dead);
       tc_after();
-      float s[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, s + 32 * c);
-      tmem_wait_ld(s, 128);
       const int n = w.prefix - tt * DN_TILE;  // tokens of the tile
-      if (n < DN_TILE) {
+      // 32 scores at a time, the next ones on their way
+      auto over_scores = [&](auto f) {
+        float s[2][32];
+        tmem_ld32(sc, s[0]);
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= n) s[c] = -INFINITY;
-      }
-      float m4[4] = {s[0], s[1], s[2], s[3]};
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld(s[c & 1], 32);
+          if (c < 3) tmem_ld32(sc + 32 * (c + 1), s[c + 1 & 1]);
+          if (n < DN_TILE) {
 #pragma unroll
-      for (int c = 4; c < 128; c += 8) {
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= n) s[c & 1][i] = -INFINITY;
+          }
+          f(c, s[c & 1]);
+        }
+      };
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      over_scores([&](int, const float (&s)[32]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmaxf(m4[i], s[c + i]), c + 4 + i < 128 ? s[c + 4 + i] : s[c + i]);
-      }
+        for (int i = 0; i < 32; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(m4[k], s[i + k]), s[i + 4 + k]);
+      });
       const float m = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kt, F);
       if (__any_sync(~0u, fresh || m > M + SLACK)) {
         const float nm = fmaxf(M, m), f = ex2(M - nm);
@@ -202,18 +261,17 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       }
       const float2 k2 = {kt, kt}, b2 = {F - M + BIAS, F - M + BIAS};
       float2 acc[2] = {{0, 0}, {0, 0}};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      over_scores([&](int c, const float (&s)[32]) {
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          float2 z = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), k2, b2);
+          float2 z = fma2(make_float2(s[2 * i], s[2 * i + 1]), k2, b2);
           z.x = ex2(z.x), z.y = ex2(z.y);
           acc[i & 1] = add2(acc[i & 1], z);
           p[i] = pack<E4M3>(z.x, z.y);
         }
-        tmem_st16(sc + 16 * c, p);
-      }
+        tmem_st16(sc + 16 * c, p);  // over scores that are read
+      });
       acc[0] = add2(acc[0], acc[1]);
       l = fmaf(acc[0].x + acc[0].y, invF, l);
       tmem_wait_st();
@@ -243,119 +301,67 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           }
         }
         tc_before();
-        ++g;
       }
       fresh = last;
       if (++tt == nt) tt = 0, ++item;
     }
-  } else if (warp < 12) {
-    regs_down<DN_LOAD>();
+  } else if (warp < 16) {
+    regs_up<DN_LOAD>();
     // ============================================ queries, keys and values
     const int p = tid - 256;
     const int lg = w.ps_log2, pm = (1 << lg) - 1;
     int item = item0, tt = first0;
-    // The item's queries: a thread per row and row tile.
-    int g = 0;
-    auto queries = [&](int it) {
-      // both row tiles' products with the item before are done
-      if (g > 0) bar_wait(s32(&S.qempty), g - 1 & 1, dead);
-      ++g;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t row = it % nj * DN_ROWS + half * 128 + p;
-        uint4 v[D / 8];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
-        if (row < rows) {
-          int b = 0, h = B;
-          while (h - b > 1) {
-            const int m = (b + h) >> 1;
-            if (cum[m] <= row) b = m;
-            else h = m;
-          }
-          const int r = row - cum[b], i = r / G;
-          const __nv_bfloat16 *src = P.q + b * P.qs0 + i * P.qs1 + (it / nj * G + r - i * G) * P.qs2;
-          if (P.qvec) {
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) v[c] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-          } else {
-            const uint16_t *u = reinterpret_cast<const uint16_t *>(src);
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              v[c].x = u[8 * c] | u[8 * c + 1] << 16, v[c].y = u[8 * c + 2] | u[8 * c + 3] << 16;
-              v[c].z = u[8 * c + 4] | u[8 * c + 5] << 16, v[c].w = u[8 * c + 6] | u[8 * c + 7] << 16;
-            }
-          }
-        }
-        float qc = P.c;
-        if constexpr (E4M3) {
-          // bring the row's largest finite magnitude to [2^10, 2^11): exact in
-          // float16 for all elements above 2^-28 of it
-          uint32_t m = 0;
-          auto most = [&](uint32_t u) {
-            const uint32_t x = u & 0x7fffu, y = u >> 16 & 0x7fffu;
-            m = max(m, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
-          };
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) most(v[c].x), most(v[c].y), most(v[c].z), most(v[c].w);
-          const int eq = max(static_cast<int>(m >> 7) - 127 - 10, -100);
-          const float f = pow2i(-eq);
-          qc = P.c * pow2i(eq);
-          auto half2 = [&](uint32_t u) {
-            return pack<true>(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
-          };
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            v[c] = make_uint4(half2(v[c].x), half2(v[c].y), half2(v[c].z), half2(v[c].w));
-        }
-        S.qc[half * 128 + p] = qc;
-        const uint32_t qb = base + C::Q + half * C::OP + p * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) sts128(qb + (c >> 3) * (DN_TILE * 128) + (((c ^ p) & 7) << 4), v[c]);
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) bar_arrive(s32(&S.qfull));
-    };
     if constexpr (E4M3) {
-      constexpr int CPR = D / 16;  // 16-byte chunks of a row, and chunks per thread
-      auto fetch = [&](uint4 (&q)[CPR], const uint8_t *src, int64_t stride, int it, int tile) {
-        const uint32_t row0 = static_cast<uint32_t>(it / nj) << lg;
+      constexpr int CPR = D / 16, ALL = DN_TILE * CPR;      // 16-byte chunks of a row, of a tile
+      constexpr int PASS = (ALL + DN_FETCH - 1) / DN_FETCH;  // chunks per thread
+      struct Set {
+        uint4 k[PASS], v[PASS];
+        uint32_t ek, ev;  // exponents of the lane's four tokens; -128 where there is none
+      };
+      auto fetch = [&](Set &s, int it, int tile) {
+        const uint32_t head = it / nj, row0 = head << lg;
+        const int t0 = tile * DN_TILE;
 #pragma unroll
-        for (int i = 0; i < CPR; ++i) {
-          const int x = p + i * 128, row = x / CPR, tok = tile * DN_TILE + row;
-          const int id = tok < w.prefix ? __ldg(w.ptable + (tok >> lg)) : -1;
-          q[i] = make_uint4(0, 0, 0, 0);
-          if (static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages))
-            q[i] = ldg_now(src + id * stride + (row0 + (tok & pm)) * D + (x - row * CPR) * 16);
+        for (int i = 0; i < PASS; ++i) {
+          const int x = p + i * DN_FETCH, row = x / CPR, tok = t0 + row;
+          const int id = (ALL % DN_FETCH == 0 || x < ALL) && tok < w.prefix ? __ldg(w.ptable + (tok >> lg)) : -1;
+          s.k[i] = s.v[i] = make_uint4(0, 0, 0, 0);
+          if (static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages)) {
+            const uint32_t at = (row0 + (tok & pm)) * D + (x - row * CPR) * 16;
+            s.k[i] = ldg_now(w.k + id * w.kps + at);
+            s.v[i] = ldg_now(w.v + id * w.vps + at);
+          }
         }
-      };
-      // exponents of the lane's four tokens; -128 where there is none
-      auto exps = [&](const int8_t *src, int it, int tile) {
-        const int tok = tile * DN_TILE + 4 * lane;
-        const int id = tok < w.prefix ? __ldg(w.ptable + (tok >> lg)) : -1;
-        uint32_t v = 0x80808080u;
+        const int tok = t0 + 4 * lane, n = w.prefix - tok;
+        const int id = n > 0 ? __ldg(w.ptable + (tok >> lg)) : -1;
+        s.ek = s.ev = 0x80808080u;
         if (static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages)) {
-          v = __ldg(reinterpret_cast<const uint32_t *>(
-              src + (((static_cast<int64_t>(id) * w.Hkv + it / nj) << lg) + (tok & pm))));
-          const int n = w.prefix - tok;
-          if (n < 4) v = (v & (1u << 8 * n) - 1) | 0x80808080u << 8 * n;
+          const int64_t at = ((static_cast<int64_t>(id) * w.Hkv + head) << lg) + (tok & pm);
+          s.ek = __ldg(reinterpret_cast<const uint32_t *>(w.ke + at));
+          s.ev = __ldg(reinterpret_cast<const uint32_t *>(w.ve + at));
+          if (n < 4) {
+            const uint32_t in = (1u << 8 * n) - 1;
+            s.ek = (s.ek & in) | (0x80808080u & ~in);
+            s.ev = (s.ev & in) | (0x80808080u & ~in);
+          }
         }
-        return v;
       };
-      auto top = [&](uint32_t v) {  // the tile's largest
+      auto top = [&](uint32_t v) {  // seven below the tile's largest
         int m = -128;
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = max(m, static_cast<int>(static_cast<int8_t>(v >> 8 * i)));
         return max(__reduce_max_sync(~0u, m), kExpMin) - 7;
       };
-      auto store = [&](uint32_t dst, const uint4 (&q)[CPR], uint32_t v, int E) {
+      auto store = [&](uint32_t dst, const uint4 (&q)[PASS], uint32_t v, int E) {
 #pragma unroll
-        for (int i = 0; i < CPR; ++i) {
-          const int x = p + i * 128, row = x / CPR, f = 2 * (x - row * CPR);
-          const int d = static_cast<int8_t>(__shfl_sync(~0u, v, row >> 2) >> 8 * (row & 3)) - E;  // <= 7
-          const uint32_t one = d >= -14 ? (d + 15) << 10 : d >= -24 ? 1 << (d + 24) : 0;  // 2^d
-          const __half2 sc = __half2half2(__ushort_as_half(static_cast<uint16_t>(one)));
+        for (int i = 0; i < PASS; ++i) {
+          const int x = p + i * DN_FETCH, row = x / CPR, f = 2 * (x - row * CPR);
+          const uint32_t word = __shfl_sync(~0u, v, row >> 2);
+          if (ALL % DN_FETCH && x >= ALL) break;
+          const int d = static_cast<int8_t>(word >> 8 * (row & 3)) - E;  // <= 7
+          const float one = pow2i(max(d, -126));
+          const uint32_t two = pack<true>(one, one);
+          const __half2 sc = *reinterpret_cast<const __half2 *>(&two);
           auto scaled = [&](uint32_t h) {
             const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), sc);
             return *reinterpret_cast<const uint32_t *>(&y);
@@ -371,45 +377,43 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           sts128(to + (swap ? c0 : c1), swap ? lo4 : hi4);
         }
       };
-      uint4 k[CPR], v[CPR];
-      uint32_t ek = 0, ev = 0;
-      if (tiles > 0) {
-        fetch(k, w.k, w.kps, item, tt);
-        ek = exps(w.ke, item, tt);
-      }
-      for (int t = 0; t < tiles; ++t) {
+      auto next = [&](int &it, int &tile) {
+        if (++tile == nt) tile = 0, ++it;
+      };
+      // tile t from `now`, the loads of tile t + 1 into `then`
+      int ni = item, nx = tt;
+      auto turn = [&](int t, Set &now, Set &then) {
         const int st = t & 1;
-        fetch(v, w.v, w.vps, item, tt);
-        ev = exps(w.ve, item, tt);
-        if (t == 0 || tt == 0) queries(item);
-        const int E = top(ek), F = top(ev);
+        next(ni, nx);
+        if (t + 1 < tiles) fetch(then, ni, nx);
+        const int E = top(now.ek), F = top(now.ev);
         if (t >= 2) bar_wait(s32(&S.kempty[st]), (t >> 1) - 1 & 1, dead);
-        store(base + C::K + st * C::OP, k, ek, E);
+        store(base + C::K + st * C::OP, now.k, now.ek, E);
         if (p == 0) S.exps[t % DN_RING] = make_int2(E, F);
         fence_async();
         __syncwarp();
         if (lane == 0) bar_arrive(s32(&S.kfull[st]));
         if (p == 0) bar_arrive(s32(&S.consts[t % DN_RING]));
-        int ni = item, nx = tt + 1;
-        if (nx == nt) nx = 0, ++ni;
-        if (t + 1 < tiles) {
-          fetch(k, w.k, w.kps, ni, nx);
-          ek = exps(w.ke, ni, nx);
-        }
         if (t >= 2) bar_wait(s32(&S.vempty[st]), (t >> 1) - 1 & 1, dead);
-        store(base + C::V + st * C::OP, v, ev, F);
+        store(base + C::V + st * C::OP, now.v, now.ev, F);
         fence_async();
         __syncwarp();
         if (lane == 0) bar_arrive(s32(&S.vfull[st]));
-        item = ni, tt = nx;
+        next(item, tt);
+      };
+      Set sa, sb;
+      if (tiles > 0) fetch(sa, item, tt);
+      for (int t = 0; t < tiles; t += 2) {
+        turn(t, sa, sb);
+        if (t + 1 < tiles) turn(t + 1, sb, sa);
       }
     } else {
       constexpr int CPR = D / 8;
       auto copy = [&](uint32_t dst, const uint8_t *src, int64_t stride, int it, int tile, uint64_t *bar) {
         const uint32_t row0 = static_cast<uint32_t>(it / nj) << lg;
 #pragma unroll
-        for (int i = 0; i < CPR; ++i) {
-          const int x = p + i * 128, row = x / CPR, f = x - row * CPR, tok = tile * DN_TILE + row;
+        for (int i = 0; i < CPR / 2; ++i) {
+          const int x = p + i * DN_FETCH, row = x / CPR, f = x - row * CPR, tok = tile * DN_TILE + row;
           const int id = tok < w.prefix ? __ldg(w.ptable + (tok >> lg)) : -1;
           const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages);
           const uint32_t at = ((row0 + (tok & pm)) * D + f * 8) * 2;
@@ -423,7 +427,6 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         const int st = t & 1;
         if (t >= 2) bar_wait(s32(&S.kempty[st]), (t >> 1) - 1 & 1, dead);
         copy(base + C::K + st * C::OP, w.k, w.kps, item, tt, &S.kfull[st]);
-        if (t == 0 || tt == 0) queries(item);
         if (t >= 2) bar_wait(s32(&S.vempty[st]), (t >> 1) - 1 & 1, dead);
         copy(base + C::V + st * C::OP, w.v, w.vps, item, tt, &S.vfull[st]);
         if (++tt == nt) tt = 0, ++item;
@@ -433,8 +436,8 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   } else {
     regs_down<DN_REST>();
     // =========================================================== products
-    if (warp < 14) {
-    const int half = warp - 12;
+    if (warp < 18) {
+    const int half = warp - 16;
     constexpr uint32_t sdesc = mma_desc(E4M3, 128, DN_TILE, false, false);
     constexpr uint32_t odesc = mma_desc(E4M3, 128, D, false, true);
     const uint64_t qd = smem_desc(base + C::Q + half * C::OP, 16, 1024), kd = smem_desc(base + C::K, 16, 1024);
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     bool fresh = true;
     for (int t = 0; t < tiles; ++t) {
       const int st = t & 1;
-      if (fresh) bar_wait(s32(&S.qfull), g++ & 1, dead);
+      if (fresh) bar_wait(s32(&S.qfull[half]), g++ & 1, dead);
       if (t > 0) bar_wait(s32(&S.odone[half]), t - 1 & 1, dead);  // P of tile t - 1 is read
       bar_wait(s32(&S.kfull[st]), t >> 1 & 1, dead);
       if (!E4M3) fence_async();  // the copies' writes, before the products' reads
@@ -471,7 +474,6 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           mma_ts(oc, sc + 8 * k, vv + (k * 2048 >> 4), odesc, !fresh || k > 0);
         mma_commit(s32(&S.odone[half]));
         mma_commit(s32(&S.vempty[st]));
-        if (tt + 1 == nt) mma_commit(s32(&S.qempty));  // the item's queries and their factors are read
       }
       __syncwarp();
       fresh = ++tt == nt;
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 12) tmem_free(tmem, 512);
+  if (warp == 16) tmem_free(tmem, 512);
   if (tid == 0) P.plan.lost[blockIdx.x] = S.dead;
 }
 
