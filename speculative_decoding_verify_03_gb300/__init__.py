@@ -108,8 +108,6 @@ def build(force: bool = False, out: str = None, extra=()) -> str:
     return out
 
 
-from . import kv as _kv  # noqa: E402
-
 _lock = threading.Lock()
 _lib = None
 
@@ -158,7 +156,15 @@ def lib():
                                               ctypes.POINTER(SpecParams), vp, vp, vp, vp, vp,
                                               sz, vp]
             L.spec_cascade_verify.restype = ctypes.c_int
-            _kv.declare(L)
+            # the cache operators (kv.py): structures and stride arrays go by address
+            L.spec_kv_append.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp]
+            L.spec_kv_append.restype = ctypes.c_int
+            L.spec_kv_read.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp]
+            L.spec_kv_read.restype = ctypes.c_int
+            L.spec_attend_workspace_size.argtypes = [vp, vp, i32]
+            L.spec_attend_workspace_size.restype = sz
+            L.spec_attend.argtypes = [vp, vp, vp, i32, vp, ctypes.c_float, vp, vp, vp, vp, sz, vp]
+            L.spec_attend.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -518,5 +524,15 @@ def spec_cascade_verify(levels, draft_tokens, uniforms, temperature, top_k=0, to
     return out_tok, out_len, stage_acc, status
 
 
-from .kv import (KVCache, ROW_BAD_LENGTH, ROW_BAD_PAGE, attend_workspace_bytes,  # noqa: E402,F401
-                 spec_attend, spec_kv_append, spec_kv_read)
+_KV = ("KVCache", "ROW_BAD_LENGTH", "ROW_BAD_PAGE", "attend_workspace_bytes", "spec_attend", "spec_kv_append",
+       "spec_kv_read")
+
+
+def __getattr__(name):
+    """The cache operators' names, from kv.py at their first use (it needs torch)."""
+    if name in _KV:
+        from . import kv
+        for n in _KV:
+            globals()[n] = getattr(kv, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

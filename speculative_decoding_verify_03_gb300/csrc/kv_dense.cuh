@@ -53,6 +53,7 @@ struct DenseShared {
   uint64_t sfull[2], pfull[2], odone[2], drain[2];  // per row tile
   uint64_t consts[DN_RING], qfull[2];
   int2 exps[DN_RING];        // E, F
+  uint32_t qmax[DN_ROWS];    // largest finite magnitude of a row, as bfloat16 bits
   uint32_t tmem, dead;
   uint32_t sum[DN_NT / 32];
 };
@@ -150,11 +151,8 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     bool fresh = true;
     for (int t = 0; t < tiles; ++t) {
       if (fresh) {  // the row's query; the products with the item before are done
-      {
         const uint32_t row = item % nj * DN_ROWS + r;
-        uint4 v[D / 8];
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+        int64_t off = -1;
         if (row < rows) {
           int b = 0, h = B;
           while (h - b > 1) {
@@ -163,44 +161,60 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
             else h = m;
           }
           const int y = row - cum[b], i = y / G;
-          const __nv_bfloat16 *src = P.q + b * P.qs0 + i * P.qs1 + (item / nj * G + y - i * G) * P.qs2;
-          if (P.qvec) {
+          off = b * P.qs0 + i * P.qs1 + (item / nj * G + y - i * G) * P.qs2;
+        }
+        // the warp's 32 rows together: neighbouring lanes, neighbouring chunks
+        constexpr int CH = D / 8;
+        uint4 v[CH];
+        if constexpr (E4M3) S.qmax[r] = 0;
+        __syncwarp();
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) v[c] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-          } else {
-            const uint16_t *u = reinterpret_cast<const uint16_t *>(src);
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              v[c].x = u[8 * c] | u[8 * c + 1] << 16, v[c].y = u[8 * c + 2] | u[8 * c + 3] << 16;
-              v[c].z = u[8 * c + 4] | u[8 * c + 5] << 16, v[c].w = u[8 * c + 6] | u[8 * c + 7] << 16;
+        for (int k = 0; k < CH; ++k) {
+          const int x = lane + 32 * k, y = x / CH;
+          const int64_t o = __shfl_sync(~0u, off, y);
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (o >= 0) {
+            const __nv_bfloat16 *src = P.q + o + 8 * (x - y * CH);
+            if (P.qvec) {
+              v[k] = __ldg(reinterpret_cast<const uint4 *>(src));
+            } else {
+              const uint16_t *u = reinterpret_cast<const uint16_t *>(src);
+              v[k] = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
             }
           }
         }
         qc = P.c;
         if constexpr (E4M3) {
-          // bring the row's largest finite magnitude to [2^10, 2^11): exact in
+          // bring each row's largest finite magnitude to [2^10, 2^11): exact in
           // float16 for all elements above 2^-28 of it
-          uint32_t m = 0;
-          auto most = [&](uint32_t u) {
-            const uint32_t x = u & 0x7fffu, y = u >> 16 & 0x7fffu;
-            m = max(m, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
-          };
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) most(v[c].x), most(v[c].y), most(v[c].z), most(v[c].w);
-          const int eq = max(static_cast<int>(m >> 7) - 127 - 10, -100);
-          const float f = pow2i(-eq);
+          for (int k = 0; k < CH; ++k) {
+            uint32_t m = 0;
+            auto most = [&](uint32_t u) {
+              const uint32_t a = u & 0x7fffu, b = u >> 16 & 0x7fffu;
+              m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+            };
+            most(v[k].x), most(v[k].y), most(v[k].z), most(v[k].w);
+            atomicMax(&S.qmax[warp * 32 + (lane + 32 * k) / CH], m);
+          }
+          __syncwarp();
+          const int eq = max(static_cast<int>(S.qmax[r] >> 7) - 127 - 10, -100);
           qc = P.c * pow2i(eq);
-          auto half2 = [&](uint32_t u) {
-            return pack<true>(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
-          };
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            v[c] = make_uint4(half2(v[c].x), half2(v[c].y), half2(v[c].z), half2(v[c].w));
+          for (int k = 0; k < CH; ++k) {
+            const float f = pow2i(-__shfl_sync(~0u, eq, (lane + 32 * k) / CH));
+            auto two = [&](uint32_t u) {
+              return pack<true>(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
+            };
+            v[k] = make_uint4(two(v[k].x), two(v[k].y), two(v[k].z), two(v[k].w));
+          }
         }
-        const uint32_t qb = base + C::Q + half * C::OP + (r & 127) * 128;
+        const uint32_t qb = base + C::Q + half * C::OP + (warp & 3) * 32 * 128;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) sts128(qb + (c >> 3) * (DN_TILE * 128) + (((c ^ r) & 7) << 4), v[c]);
-      }
+        for (int k = 0; k < CH; ++k) {
+          const int x = lane + 32 * k, y = x / CH, c = x - y * CH;
+          sts128(qb + (c >> 3) * (DN_TILE * 128) + y * 128 + (((c ^ y) & 7) << 4), v[k]);
+        }
         fence_async();
         __syncwarp();
         if (lane == 0) bar_arrive(s32(&S.qfull[half]));
@@ -318,27 +332,35 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         uint4 k[PASS], v[PASS];
         uint32_t ek, ev;  // exponents of the lane's four tokens; -128 where there is none
       };
+      int id[PASS], ide = -1;  // page ids of the tile to be fetched next
+      auto pages = [&](int tile) {
+        const int t0 = tile * DN_TILE;
+#pragma unroll
+        for (int i = 0; i < PASS; ++i) {
+          const int x = p + i * DN_FETCH, tok = t0 + x / CPR;
+          id[i] = (ALL % DN_FETCH == 0 || x < ALL) && tok < w.prefix ? ldg_now(w.ptable + (tok >> lg)) : -1;
+        }
+        ide = t0 + 4 * lane < w.prefix ? ldg_now(w.ptable + (t0 + 4 * lane >> lg)) : -1;
+      };
       auto fetch = [&](Set &s, int it, int tile) {
         const uint32_t head = it / nj, row0 = head << lg;
         const int t0 = tile * DN_TILE;
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
-          const int x = p + i * DN_FETCH, row = x / CPR, tok = t0 + row;
-          const int id = (ALL % DN_FETCH == 0 || x < ALL) && tok < w.prefix ? __ldg(w.ptable + (tok >> lg)) : -1;
+          const int x = p + i * DN_FETCH, row = x / CPR;
           s.k[i] = s.v[i] = make_uint4(0, 0, 0, 0);
-          if (static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages)) {
-            const uint32_t at = (row0 + (tok & pm)) * D + (x - row * CPR) * 16;
-            s.k[i] = ldg_now(w.k + id * w.kps + at);
-            s.v[i] = ldg_now(w.v + id * w.vps + at);
+          if (static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(w.n_pages)) {
+            const uint32_t at = (row0 + (t0 + row & pm)) * D + (x - row * CPR) * 16;
+            s.k[i] = ldg_now16(w.k + id[i] * w.kps + at);
+            s.v[i] = ldg_now16(w.v + id[i] * w.vps + at);
           }
         }
         const int tok = t0 + 4 * lane, n = w.prefix - tok;
-        const int id = n > 0 ? __ldg(w.ptable + (tok >> lg)) : -1;
         s.ek = s.ev = 0x80808080u;
-        if (static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages)) {
-          const int64_t at = ((static_cast<int64_t>(id) * w.Hkv + head) << lg) + (tok & pm);
-          s.ek = __ldg(reinterpret_cast<const uint32_t *>(w.ke + at));
-          s.ev = __ldg(reinterpret_cast<const uint32_t *>(w.ve + at));
+        if (static_cast<uint32_t>(ide) < static_cast<uint32_t>(w.n_pages)) {
+          const int64_t at = ((static_cast<int64_t>(ide) * w.Hkv + head) << lg) + (tok & pm);
+          s.ek = ldg_now32(w.ke + at);
+          s.ev = ldg_now32(w.ve + at);
           if (n < 4) {
             const uint32_t in = (1u << 8 * n) - 1;
             s.ek = (s.ek & in) | (0x80808080u & ~in);
@@ -385,7 +407,10 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       auto turn = [&](int t, Set &now, Set &then) {
         const int st = t & 1;
         next(ni, nx);
-        if (t + 1 < tiles) fetch(then, ni, nx);
+        if (t + 1 < tiles) {
+          fetch(then, ni, nx);
+          pages(nx + 1 == nt ? 0 : nx + 1);
+        }
         const int E = top(now.ek), F = top(now.ev);
         if (t >= 2) bar_wait(s32(&S.kempty[st]), (t >> 1) - 1 & 1, dead);
         store(base + C::K + st * C::OP, now.k, now.ek, E);
@@ -402,7 +427,11 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         next(item, tt);
       };
       Set sa, sb;
-      if (tiles > 0) fetch(sa, item, tt);
+      if (tiles > 0) {
+        pages(tt);
+        fetch(sa, item, tt);
+        pages(tt + 1 == nt ? 0 : tt + 1);
+      }
       for (int t = 0; t < tiles; t += 2) {
         turn(t, sa, sb);
         if (t + 1 < tiles) turn(t + 1, sb, sa);
@@ -495,11 +524,11 @@ cudaError_t dense_go(const SpanParams &p, int64_t tiles, int *grid, cudaStream_t
   constexpr int fixed = 1024 + DenseCfg<D>::OPER + sizeof(DenseShared);
   static_assert(fixed + 4 * (kMaxB + 1) <= 232448, "shared memory");
   auto *f = dense_kernel<D, E4M3>;
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, fixed + 4 * (kMaxB + 1));
+  static Slots slots;
+  int sms = 0, occ = 0;
+  constexpr int smem = fixed + 4 * (kMaxB + 1);
+  const cudaError_t e = slots.get(reinterpret_cast<const void *>(f), DN_NT, smem, smem, &sms, &occ);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   int64_t n = sms < kMaxGrid ? sms : kMaxGrid;
   if (n > tiles) n = tiles;
   if (n < 1) n = 1;

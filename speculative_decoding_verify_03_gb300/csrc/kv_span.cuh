@@ -604,14 +604,14 @@ cudaError_t span_go(const SpanParams &p, int64_t tiles, int *grid, cudaStream_t 
   using C = SpanCfg<D, E4M3, WR, WT>;
   const int smem = C::FIXED + 8 * (p.w.B + 1);
   auto *f = span_kernel<D, E4M3, WR, WT>;
-  cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::FIXED + 8 * (kMaxB + 1));
+  static Slots slots;  // of this kernel, per device
+  int sms = 0, occ = 0;
+  const cudaError_t e = slots.get(reinterpret_cast<const void *>(f), C::NT, C::FIXED, C::FIXED + 8 * (kMaxB + 1),
+                                  &sms, &occ);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 0, occ = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, f, C::NT, smem)) != cudaSuccess) return e;
-  int64_t n = static_cast<int64_t>(sms) * (occ > 0 ? occ : 1);
+  // CTAs per SM: what registers allow, and what this call's shared memory does
+  const int by_smem = kSmSmem / (smem + 1024);
+  int64_t n = static_cast<int64_t>(sms) * (occ < by_smem ? occ : by_smem > 0 ? by_smem : 1);
   if (n > kMaxGrid) n = kMaxGrid;
   if (n > tiles) n = tiles;
   if (n < 1) n = 1;

@@ -11,6 +11,8 @@
 // (consecutive CTAs of one item: consecutive slots).
 #pragma once
 
+#include <atomic>
+
 #include "kv_common.cuh"
 
 namespace kv {
@@ -35,6 +37,33 @@ struct SpanParams {
   int32_t G;              // query heads per key/value head
   int32_t prefix;         // 1: prefix items
   bool qvec;              // q rows are 4-byte (span) or 16-byte (dense) aligned
+};
+
+constexpr int kSmSmem = 228 * 1024;  // shared memory of an SM; 1 KB of it a CTA's own
+
+// Multiprocessors and resident CTAs (at `smem` bytes) of one kernel, asked of
+// the runtime once per device; sets the kernel's shared memory limit.
+struct Slots {
+  static constexpr int kDevices = 64;
+  std::atomic<int> sms[kDevices] = {}, occ[kDevices] = {};
+  cudaError_t get(const void *f, int threads, int smem, int most, int *n, int *per) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kDevices) return cudaErrorInvalidDevice;
+    *n = sms[dev].load(std::memory_order_acquire);
+    if (*n == 0) {
+      int s = 0, o = 0;
+      if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return e;
+      if ((e = cudaDeviceGetAttribute(&s, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+      if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, f, threads, smem)) != cudaSuccess) return e;
+      occ[dev].store(o > 0 ? o : 1, std::memory_order_relaxed);
+      sms[dev].store(s, std::memory_order_release);
+      *n = s;
+    }
+    *per = occ[dev].load(std::memory_order_relaxed);
+    return cudaSuccess;
+  }
 };
 
 // Launches the span kernel for RT = 16 * wr rows (wr 1 .. 4) on at most

@@ -5,8 +5,21 @@ from __future__ import annotations
 import ctypes
 import threading
 
+import torch
+
 SPEC_KV_BF16, SPEC_KV_E4M3 = 0, 1
 ROW_BAD_LENGTH, ROW_BAD_PAGE = 1 << 7, 1 << 8
+
+_i32, _f32, _bf16 = torch.int32, torch.float32, torch.bfloat16
+_byref = ctypes.byref
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# torch's own short way to the same address, where it has it (2 us a call less)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 class SpecKvCache(ctypes.Structure):
@@ -29,20 +42,6 @@ class SpecKvBatch(ctypes.Structure):
 _Strides = ctypes.c_int64 * 3
 
 
-def declare(L):
-    """Argument types of the library's functions."""
-    vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
-    # structures and stride arrays go by address (ctypes.byref)
-    L.spec_kv_append.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp]
-    L.spec_kv_append.restype = ctypes.c_int
-    L.spec_kv_read.argtypes = [vp, vp, i32, i32, i32, vp, vp, vp, vp]
-    L.spec_kv_read.restype = ctypes.c_int
-    L.spec_attend_workspace_size.argtypes = [vp, vp, i32]
-    L.spec_attend_workspace_size.restype = sz
-    L.spec_attend.argtypes = [vp, vp, vp, i32, vp, ctypes.c_float, vp, vp, vp, vp, sz, vp]
-    L.spec_attend.restype = ctypes.c_int
-
-
 class KVCache:
     """A paged cache on the GPU: k_pages and v_pages [n_pages, n_kv_heads,
     page_size, head_dim], bfloat16, or float8_e4m3fn with k_exp and v_exp
@@ -52,7 +51,6 @@ class KVCache:
     alive and describes them to the library."""
 
     def __init__(self, k_pages, v_pages, k_exp=None, v_exp=None):
-        import torch
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
             raise ValueError("k_pages and v_pages must be [n_pages, n_kv_heads, page_size, head_dim]")
         if k_pages.dtype != v_pages.dtype or k_pages.dtype not in (torch.bfloat16,
@@ -87,7 +85,6 @@ class KVCache:
     @classmethod
     def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
         """A cache of new pages; dtype float8_e4m3fn (the default) or bfloat16."""
-        import torch
         dtype = dtype or torch.float8_e4m3fn
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         k, v = (torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
@@ -98,40 +95,50 @@ class KVCache:
 
 
 
-def _int32(name, t, shape, device):
-    import torch
-    if t.dtype != torch.int32:
+def _int32(name, t, n, device):
+    """A contiguous int32 vector of n elements on the cache's device."""
+    if t.dtype != _i32:
         raise TypeError(f"{name} must be int32")
-    if t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be {list(shape)} on {device}")
-    if not t.is_contiguous():
+    if t.dim() != 1 or t.shape[0] != n or t.device != device:
+        raise ValueError(f"{name} must be [{n}] on {device}")
+    if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _batch(cache, page_table, kv_len, gamma_max, prefix_table, prefix_len, gamma_per_row):
-    import torch
-    B, dev = kv_len.shape[0], cache.device
-    _int32("kv_len", kv_len, (B,), dev)
-    if page_table.dtype != torch.int32:
+    dev = cache.device
+    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    len_ptr = _int32("kv_len", kv_len, B, dev)
+    if page_table.dtype != _i32:
         raise TypeError("page_table must be int32")
-    if page_table.dim() != 2 or page_table.shape[0] != B or page_table.device != dev:
+    shape = page_table.shape
+    if len(shape) != 2 or shape[0] != B or page_table.device != dev:
         raise ValueError(f"page_table must be [{B}, max_pages] on {dev}")
-    mp = page_table.shape[1]
-    if B and mp and page_table.stride(1) != 1:
+    mp = shape[1]
+    row, col = page_table.stride()
+    if col != 1 and B and mp:
         raise ValueError("page_table rows must be contiguous")
-    if gamma_per_row is not None:
-        _int32("gamma_per_row", gamma_per_row, (B,), dev)
-    prefix_len = int(prefix_len)
-    pt = None
+    gamma = None if gamma_per_row is None else _int32("gamma_per_row", gamma_per_row, B, dev)
+    pt, prefix_len = None, int(prefix_len)
     if prefix_len > 0:
         need = -(-prefix_len // cache.page_size)
         if prefix_table is None or prefix_table.dim() != 1 or prefix_table.shape[0] < need:
             raise ValueError(f"prefix_table must hold the prefix's {need} page ids")
-        _int32("prefix_table", prefix_table, prefix_table.shape, dev)
-        pt = prefix_table.data_ptr()
-    return SpecKvBatch(B, gamma_max, mp, prefix_len, page_table.stride(0) if B > 1 else mp,
-                       page_table.data_ptr(), pt, kv_len.data_ptr(),
-                       gamma_per_row.data_ptr() if gamma_per_row is not None else None)
+        pt = _int32("prefix_table", prefix_table, prefix_table.shape[0], dev)
+    return SpecKvBatch(B, gamma_max, mp, prefix_len, row if B > 1 else mp, page_table.data_ptr(), pt, len_ptr, gamma)
+
+
+_library = None
+
+
+def _lib():
+    """The loaded library, looked up once."""
+    global _library
+    if _library is None:
+        from . import lib
+        _library = lib()
+    return _library
 
 
 def _check(code):
@@ -140,16 +147,15 @@ def _check(code):
         check(code)
 
 
-def _lib_stream(stream, device):
-    from . import lib
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return lib(), s.cuda_stream
+def _stream(stream, device):
+    """Address of the stream to launch on: the given one or the device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(device.index)
 
 
 def _status(with_status, B, device):
-    import torch
-    return torch.empty(B, dtype=torch.int32, device=device) if with_status else None
+    return torch.empty(B, dtype=_i32, device=device) if with_status else None
 
 
 def _ptr(t):
@@ -165,26 +171,30 @@ def spec_kv_append(cache, k, v, page_table, kv_len, gamma_per_row=None, prefix_l
     gamma_b + 1 tokens.  page_table [B, max_pages] int32 holds the sequences'
     own pages, whose first position is prefix_len.  Updates the cache in
     place; returns row_status [B] when with_status, else None."""
-    from . import _dtype_code
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+    dev = cache.device
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 4 or v.shape != shape or v.dtype != dtype:
         raise ValueError("k and v must be [B, n, n_kv_heads, head_dim] of one dtype")
-    B, n, H, D = k.shape
-    if (H, D) != (cache.n_kv_heads, cache.head_dim) or B != kv_len.shape[0] or n < 1:
+    B, n, H, D = shape
+    if H != cache.n_kv_heads or D != cache.head_dim or B != kv_len.shape[0] or n < 1:
         raise ValueError("k and v do not match the cache's heads or kv_len's rows")
-    if k.device != cache.device or v.device != cache.device:
-        raise ValueError(f"k and v must be on {cache.device}")
-    if k.stride(3) != 1 or v.stride(3) != 1:
+    if dtype is not _bf16 and dtype is not _f32:
+        raise TypeError(f"k and v must be float32 or bfloat16, got {dtype}")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must be on {dev}")
+    ks, vs = k.stride(), v.stride()
+    if ks[3] != 1 or vs[3] != 1:
         raise ValueError("the head_dim axis must be contiguous")
-    dtype = _dtype_code(k)
     b = _batch(cache, page_table, kv_len, n - 1, None, 0, gamma_per_row)
-    b.prefix_len = prefix_len = int(prefix_len)
-    if prefix_len > 0:
-        b.prefix_table = page_table.data_ptr()  # not read: the step is past the prefix
-    st = _status(with_status, B, cache.device)
-    L, s = _lib_stream(stream, cache.device)
-    _check(L.spec_kv_append(cache.ref, ctypes.byref(b), k.data_ptr(), v.data_ptr(), dtype,
-                            ctypes.byref(_Strides(*k.stride()[:3])),
-                            ctypes.byref(_Strides(*v.stride()[:3])), _ptr(st), s))
+    if prefix_len:
+        b.prefix_len = int(prefix_len)
+        b.prefix_table = b.page_table  # not read: the step is past the prefix
+    st = _status(with_status, B, dev)
+    code = _lib().spec_kv_append(cache.ref, _byref(b), k.data_ptr(), v.data_ptr(), 0 if dtype is _f32 else 1,
+                                 _byref(_Strides(*ks[:3])), _byref(_Strides(*vs[:3])), _ptr(st),
+                                 _stream(stream, dev))
+    if code:
+        _check(code)
     return st
 
 
@@ -194,19 +204,22 @@ def spec_kv_read(cache, page_table, kv_len, n, begin=0, prefix_table=None, prefi
     spec_kv_read in include/spec_kv.h): returns (k, v) [B, n, n_kv_heads,
     head_dim] in dtype (bfloat16 by default, or float32), zeros from kv_len[b]
     on, and row_status [B] when with_status."""
-    import torch
-    dtype = dtype or torch.bfloat16
-    if dtype not in (torch.bfloat16, torch.float32):
+    dev = cache.device
+    dtype = dtype or _bf16
+    if dtype is not _bf16 and dtype is not _f32:
         raise TypeError("dtype must be bfloat16 or float32")
-    b = _batch(cache, page_table, kv_len, 0, prefix_table, prefix_len, None)
-    shape = (b.B, int(n), cache.n_kv_heads, cache.head_dim)
     if n < 0 or begin < 0:
         raise ValueError("begin and n must not be negative")
-    k, v = (torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
-    st = _status(with_status, b.B, cache.device)
-    L, s = _lib_stream(stream, cache.device)
-    _check(L.spec_kv_read(cache.ref, ctypes.byref(b), int(begin), int(n),
-                          0 if dtype == torch.float32 else 1, k.data_ptr(), v.data_ptr(), _ptr(st), s))
+    b = _batch(cache, page_table, kv_len, 0, prefix_table, prefix_len, None)
+    n, begin = int(n), int(begin)
+    shape = (b.B, n, cache.n_kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=dev)
+    v = torch.empty(shape, dtype=dtype, device=dev)
+    st = _status(with_status, b.B, dev)
+    code = _lib().spec_kv_read(cache.ref, _byref(b), begin, n, 0 if dtype is _f32 else 1, k.data_ptr(), v.data_ptr(),
+                               _ptr(st), _stream(stream, dev))
+    if code:
+        _check(code)
     return (k, v, st) if with_status else (k, v)
 
 
@@ -216,13 +229,11 @@ _ws = {}
 
 def attend_workspace_bytes(cache, batch, n_heads) -> int:
     """Workspace bytes of spec_attend for these shapes (a SpecKvBatch)."""
-    from . import lib
-    return int(lib().spec_attend_workspace_size(cache.ref, ctypes.byref(batch), int(n_heads)))
+    return _lib().spec_attend_workspace_size(cache.ref, _byref(batch), n_heads)
 
 
 def _attend_workspace(cache, batch, n_heads, stream_ptr):
     """A workspace cached per device and stream (calls on one stream run in order)."""
-    import torch
     need = attend_workspace_bytes(cache, batch, n_heads)
     key = (cache.device.index, stream_ptr)
     with _ws_lock:
@@ -245,35 +256,38 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     of contiguous tensors for the results, or None.  Returns (out [B,
     gamma_max + 1, n_heads, head_dim] bfloat16, lse [B, gamma_max + 1, n_heads]
     float32), and row_status [B] when with_status."""
-    import torch
-    if q.dtype != torch.bfloat16:
+    dev = cache.device
+    shape = q.shape
+    if q.dtype is not _bf16:
         raise TypeError("q must be bfloat16")
-    if q.dim() != 4 or q.shape[0] != kv_len.shape[0] or q.shape[1] < 1 or q.shape[3] != cache.head_dim:
+    if len(shape) != 4 or shape[0] != kv_len.shape[0] or shape[1] < 1 or shape[3] != cache.head_dim:
         raise ValueError("q must be [B, gamma_max + 1, n_heads, head_dim]")
-    if q.device != cache.device:
-        raise ValueError(f"q must be on {cache.device}")
-    if q.stride(3) != 1:
+    if q.device != dev:
+        raise ValueError(f"q must be on {dev}")
+    qs = q.stride()
+    if qs[3] != 1:
         raise ValueError("the head_dim axis must be contiguous")
-    B, N, Hq, D = q.shape
+    B, N, Hq, D = shape
     if Hq < 1 or Hq % cache.n_kv_heads:
         raise ValueError("n_heads must be a multiple of the cache's n_kv_heads")
     b = _batch(cache, page_table, kv_len, N - 1, prefix_table, prefix_len, gamma_per_row)
-    L, s = _lib_stream(stream, cache.device)
+    s = _stream(stream, dev)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")
         workspace = _attend_workspace(cache, b, Hq, s)
     if out is None:
-        o = torch.empty((B, N, Hq, D), dtype=torch.bfloat16, device=cache.device)
-        lse = torch.empty((B, N, Hq), dtype=torch.float32, device=cache.device)
+        o = torch.empty(shape, dtype=_bf16, device=dev)
+        lse = torch.empty(shape[:3], dtype=_f32, device=dev)
     else:
         o, lse = out
-        if (o.shape != (B, N, Hq, D) or o.dtype != torch.bfloat16 or not o.is_contiguous() or
-                lse.shape != (B, N, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        if (o.shape != shape or o.dtype is not _bf16 or not o.is_contiguous() or lse.shape != shape[:3] or
+                lse.dtype is not _f32 or not lse.is_contiguous() or o.device != dev or lse.device != dev):
             raise ValueError("out must be contiguous bfloat16 and float32 tensors of the results' shapes")
-    st = _status(with_status, B, cache.device)
-    _check(L.spec_attend(cache.ref, ctypes.byref(b), q.data_ptr(), Hq,
-                         ctypes.byref(_Strides(*q.stride()[:3])),
-                         D ** -0.5 if scale is None else float(scale), o.data_ptr(), lse.data_ptr(),
-                         _ptr(st), workspace.data_ptr(), workspace.numel(), s))
+    st = _status(with_status, B, dev)
+    code = _lib().spec_attend(cache.ref, _byref(b), q.data_ptr(), Hq, _byref(_Strides(*qs[:3])),
+                              D ** -0.5 if scale is None else float(scale), o.data_ptr(), lse.data_ptr(), _ptr(st),
+                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+    if code:
+        _check(code)
     return (o, lse, st) if with_status else (o, lse)
