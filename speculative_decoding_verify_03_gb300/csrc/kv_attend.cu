@@ -116,7 +116,17 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
   if (lane == 0 && P.lse) P.lse[at] = l;
 }
 
-int row_warps(int64_t rows) { return rows > 48 ? 4 : static_cast<int>((rows + 15) / 16); }
+// Row warps (of 16 rows) of an item: an item costs its rows, padding included,
+// and about 24 rows' time for what it does once for all of them.
+int row_warps(int64_t rows) {
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int w = 1; w <= 4; ++w) {
+    const int64_t cost = (rows + 16 * w - 1) / (16 * w) * (16 * w + 24);
+    if (cost < least) least = cost, best = w;
+  }
+  return best;
+}
 
 // Query rows (of a key/value head) from which the prefix goes to the dense kernel.
 constexpr int64_t kDenseRows = 65;
@@ -224,14 +234,14 @@ extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_bat
     P.po = reinterpret_cast<float *>(ws + L.qo);
     P.pl = reinterpret_cast<float *>(ws + L.ql);
     m.qo = P.po, m.ql = P.pl;
-    P.qvec = qbits % (L.dense ? 16 : 4) == 0;
+    P.qvec = qbits % (L.dense || L.wp == 1 ? 16 : 4) == 0;
     const cudaError_t e = !L.dense ? span(P, L.wp, L.tiles_p, &m.cp, s)
                           : cache->format == SPEC_KV_E4M3 ? dense_e4m3(P, D, L.tiles_p, &m.cp, s)
                                                           : dense_bf16(P, D, L.tiles_p, &m.cp, s);
     if (e != cudaSuccess) return SPEC_ERR_CUDA;
   }
   P.prefix = 0;
-  P.qvec = qbits % 4 == 0;
+  P.qvec = qbits % (L.wo == 1 ? 16 : 4) == 0;
   P.po = reinterpret_cast<float *>(ws + L.po);
   P.pl = reinterpret_cast<float *>(ws + L.pl);
   m.po = P.po, m.pl = P.pl;

@@ -88,15 +88,6 @@ __device__ __forceinline__ int row_exp(uint32_t m) {
   return min(max(e, kv::kExpMin), kv::kExpMax);
 }
 
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
-  const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
-  if (fabsf(lo) == inf) lo = nan;  // e4m3 has no infinity
-  if (fabsf(hi) == inf) hi = nan;
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 struct AP {
   View w;
   Rows k, v;
@@ -151,10 +142,10 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ AP P
     if (on) {
       const float sk = kv::pow2i(-ek), sv = kv::pow2i(-ev);
       uint2 a, c;
-      a.x = to_e4m3x2(x[0] * sk, x[1] * sk) | to_e4m3x2(x[2] * sk, x[3] * sk) << 16;
-      a.y = to_e4m3x2(x[4] * sk, x[5] * sk) | to_e4m3x2(x[6] * sk, x[7] * sk) << 16;
-      c.x = to_e4m3x2(y[0] * sv, y[1] * sv) | to_e4m3x2(y[2] * sv, y[3] * sv) << 16;
-      c.y = to_e4m3x2(y[4] * sv, y[5] * sv) | to_e4m3x2(y[6] * sv, y[7] * sv) << 16;
+      a.x = kv::stored2(x[0] * sk, x[1] * sk) | kv::stored2(x[2] * sk, x[3] * sk) << 16;
+      a.y = kv::stored2(x[4] * sk, x[5] * sk) | kv::stored2(x[6] * sk, x[7] * sk) << 16;
+      c.x = kv::stored2(y[0] * sv, y[1] * sv) | kv::stored2(y[2] * sv, y[3] * sv) << 16;
+      c.y = kv::stored2(y[4] * sv, y[5] * sv) | kv::stored2(y[6] * sv, y[7] * sv) << 16;
       *reinterpret_cast<uint2 *>(P.kp + page * w.kps + at * D + lane * 8) = a;
       *reinterpret_cast<uint2 *>(P.vp + page * w.vps + at * D + lane * 8) = c;
     }

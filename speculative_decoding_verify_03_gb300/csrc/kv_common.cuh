@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -116,6 +117,16 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   uint32_t r;
   if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two floats as e4m3, to nearest even, saturating, an infinity (which e4m3 does
+// not have) to NaN.
+__device__ __forceinline__ uint32_t stored2(float lo, float hi) {
+  const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
+  if (fabsf(lo) == inf) lo = nan;
+  if (fabsf(hi) == inf) hi = nan;
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
 // 2^e as a float, e in [-126, 127].

@@ -36,7 +36,7 @@ struct SpanParams {
   float c;                // scale * log2 e
   int32_t G;              // query heads per key/value head
   int32_t prefix;         // 1: prefix items
-  bool qvec;              // q rows are 4-byte (span) or 16-byte (dense) aligned
+  bool qvec;              // q rows are 4-byte aligned; 16-byte (dense kernel, 16 rows)
 };
 
 constexpr int kSmSmem = 228 * 1024;  // shared memory of an SM; 1 KB of it a CTA's own
@@ -86,6 +86,7 @@ cudaError_t dense_bf16(const SpanParams &, int D, int64_t tiles, int *grid, cuda
 
 // The CTA that works on tile x of W (C <= W CTAs): the largest c with W c / C <= x.
 __host__ __device__ __forceinline__ uint32_t owner(uint32_t x, uint32_t W, uint32_t C) {
+  if (W < (1u << 22)) return ((x + 1) * C - 1) / W;  // C <= 640: no overflow
   return static_cast<uint32_t>(((static_cast<uint64_t>(x) + 1) * C - 1) / W);
 }
 
