@@ -5,8 +5,8 @@
 // worked on its own item and, with a prefix, on its prefix item;
 //   out = sum_s 2^(lse2_s - m) o_s / sum_s 2^(lse2_s - m),
 //   lse = ln 2 (m + log2 sum_s 2^(lse2_s - m)),  m = max_s lse2_s,
-// in the order of the slots (reproducible).  A warp takes a row; the partial
-// results were written just before and are read from L2.
+// in the order of the slots (reproducible).  The partial results were written
+// just before and are read from L2.
 #include "kv_span.h"
 
 namespace {
@@ -14,7 +14,6 @@ namespace {
 using namespace kv;
 
 constexpr int MG_NT = 256;
-constexpr int MG_ROWS = MG_NT / 32;  // rows per CTA: one per warp
 
 struct MP {
   View w;
@@ -27,9 +26,11 @@ struct MP {
   int32_t rto, rtp, co, cp, kp;  // rows per item and CTAs, own and prefix; key tokens of a prefix tile
 };
 
+// LPR lanes per row, four elements each: 16 for heads of 64, else a warp.
+template <int LPR>
 __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP P) {
   const View &w = P.w;
-  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.y, lane = threadIdx.x % LPR;
   int own, n;
   int st = row_shape(w, b, own, n);
   int bad = 0;
@@ -50,68 +51,78 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
   if (P.status && blockIdx.x == 0 && threadIdx.x == 0) P.status[b] = st;
 
   const int D = P.D, G = P.G;
-  const int row = blockIdx.x * MG_ROWS + warp;
-  if (row >= w.N * P.Hq) return;
-  const bool on = lane * 4 < D;
+  const int row = blockIdx.x * (MG_NT / LPR) + threadIdx.x / LPR;
+  const bool there = row < w.N * P.Hq;
   const int i = row / P.Hq, h = row - i * P.Hq;
   const int head = h / G, r = i * G + h - head * G;
-  float m = -INFINITY, sum = 0.0f;
-  float4 acc = {0, 0, 0, 0};
-  // Slots first .. first + count - 1, 32 at a time: a lane per slot for the
-  // weights, then the outputs, whose loads do not depend on one another.
-  auto join = [&](const float *po, const float *pl, uint32_t first, int count, int rt, int rr) {
-    for (int s0 = 0; s0 < count; s0 += 32) {
-      const int k = min(32, count - s0);
-      const int64_t at = static_cast<int64_t>(first + s0) * rt + rr;
-      const float v = lane < k ? pl[at + static_cast<int64_t>(lane) * rt] : -INFINITY;
-      float nm = v;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, o));
-      nm = fmaxf(nm, m);  // a NaN does not become the maximum
-      const float a = nm == -INFINITY ? 1.0f : ex2(m - nm);
-      const float c = v == -INFINITY ? 0.0f : ex2(v - nm);
-      float s = c;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-      sum = sum * a + s;
-      acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
-#pragma unroll 4
-      for (int j = 0; j < k; ++j) {
-        const float f = __shfl_sync(~0u, c, j);
-        float4 x = {0, 0, 0, 0};
-        if (on) x = __ldcg(reinterpret_cast<const float4 *>(po + (at + static_cast<int64_t>(j) * rt) * D + lane * 4));
-        acc.x = fmaf(f, x.x, acc.x);
-        acc.y = fmaf(f, x.y, acc.y);
-        acc.z = fmaf(f, x.z, acc.z);
-        acc.w = fmaf(f, x.w, acc.w);
-      }
-      m = nm;
-    }
-  };
-  if (!st && i < n) {
+  // Partial results: those of the prefix item, then those of the own item, at
+  // lse index lo0 + s * rt (and D times that, the outputs).
+  int np = 0, all = 0;
+  int64_t lp = 0, lo = 0;
+  if (!st && there && i < n) {
     if (w.prefix) {
       const int tp = (w.prefix + P.kp - 1) / P.kp;
       const int nj = (P.plan.rows[w.B] + P.rtp - 1) / P.rtp;
       const uint32_t W = static_cast<uint32_t>(nj) * w.Hkv * tp, C = min(static_cast<uint32_t>(P.cp), W);
-      const uint32_t k = P.plan.rows[b] + r, item = head * nj + k / P.rtp;
-      const uint32_t c0 = owner(item * tp, W, C), c1 = owner(item * tp + tp - 1, W, C);
-      join(P.qo, P.ql, item + c0, c1 - c0 + 1, P.rtp, k % P.rtp);
+      const uint32_t k = P.plan.rows[b] + r, y = k / P.rtp, item = head * nj + y;
+      const uint32_t c0 = owner(item * tp, W, C);
+      np = owner(item * tp + tp - 1, W, C) - c0 + 1;
+      lp = static_cast<int64_t>(item + c0) * P.rtp + (k - y * P.rtp);
     }
     const int to = (own + n + kTile - 1) / kTile, nj = (n * G + P.rto - 1) / P.rto;
     const uint32_t W = P.plan.tiles[w.B], C = min(static_cast<uint32_t>(P.co), W);
-    const uint32_t j = head * nj + r / P.rto, x = P.plan.tiles[b] + j * to;
-    const uint32_t c0 = owner(x, W, C), c1 = owner(x + to - 1, W, C);
-    join(P.po, P.pl, P.plan.items[b] + j + c0, c1 - c0 + 1, P.rto, r % P.rto);
+    const int y = r / P.rto;
+    const uint32_t j = head * nj + y, x = P.plan.tiles[b] + j * to;
+    const uint32_t c0 = owner(x, W, C);
+    all = np + owner(x + to - 1, W, C) - c0 + 1;
+    lo = static_cast<int64_t>(P.plan.items[b] + j + c0) * P.rto + (r - y * P.rto);
   }
+  const bool on = lane * 4 < D;
+  const unsigned most = __reduce_max_sync(~0u, static_cast<unsigned>(all));  // of the warp's rows
+  float m = -INFINITY, sum = 0.0f;
+  float4 acc = {0, 0, 0, 0};
+  // LPR of them at a time: a lane each for the weights, then the outputs, whose
+  // loads do not depend on one another.
+  for (int s0 = 0; s0 < static_cast<int>(most); s0 += LPR) {
+    const int s = s0 + lane;
+    float v = -INFINITY;
+    if (s < all) v = s < np ? P.ql[lp + static_cast<int64_t>(s) * P.rtp] : P.pl[lo + static_cast<int64_t>(s - np) * P.rto];
+    float nm = v;
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, o));
+    nm = fmaxf(nm, m);  // a NaN does not become the maximum
+    const float a = nm == -INFINITY ? 1.0f : ex2(m - nm), c = v == -INFINITY ? 0.0f : ex2(v - nm);
+    acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
+    sum *= a;
+    m = nm;
+    const int k = min(LPR, static_cast<int>(most) - s0);
+#pragma unroll 2
+    for (int j = 0; j < k; ++j) {
+      const float f = __shfl_sync(~0u, c, j, LPR);
+      const int t = s0 + j;
+      float4 x = {0, 0, 0, 0};
+      if (on && t < all) {
+        const float *src = t < np ? P.qo + (lp + static_cast<int64_t>(t) * P.rtp) * D
+                                  : P.po + (lo + static_cast<int64_t>(t - np) * P.rto) * D;
+        x = __ldcg(reinterpret_cast<const float4 *>(src + lane * 4));
+      }
+      sum += f;
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
+    }
+  }
+  if (!there) return;
   float f = sum == 0.0f ? 0.0f : 1.0f / sum;
   float l = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
   if (st) f = l = __int_as_float(0x7fffffff);
   const int64_t at = static_cast<int64_t>(b) * w.N * P.Hq + row;
   if (on) {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-    *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4) = lo;
-    *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4 + 2) = hi;
+    const __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+    const __nv_bfloat162 hi2 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+    *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4) = lo2;
+    *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4 + 2) = hi2;
   }
   if (lane == 0 && P.lse) P.lse[at] = l;
 }
@@ -250,10 +261,13 @@ extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_bat
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((P.w.N * n_heads + MG_ROWS - 1) / MG_ROWS, P.w.B);
+  const int per = MG_NT / (D == 64 ? 16 : 32);  // rows per CTA
+  cfg.gridDim = dim3((P.w.N * n_heads + per - 1) / per, P.w.B);
   cfg.blockDim = dim3(MG_NT);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel, m) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  const cudaError_t e = D == 64 ? cudaLaunchKernelEx(&cfg, merge_kernel<16>, m)
+                                : cudaLaunchKernelEx(&cfg, merge_kernel<32>, m);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

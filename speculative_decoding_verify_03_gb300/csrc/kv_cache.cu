@@ -30,33 +30,46 @@ struct Rows {  // a tensor [B, n, Hkv, D] with strides in elements
   int64_t s0, s1, s2;
 };
 
-// Eight elements of a source row as float, `vec`: 16-byte aligned.
+// Eight elements of a source row as they are; `vec`: 16-byte aligned.
 template <bool F32>
-__device__ __forceinline__ void load8(const void *base, int64_t off, bool vec, float (&x)[8]) {
+struct Raw {
+  uint4 q[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ void load8(const void *base, int64_t off, bool vec, Raw<F32> &r) {
   if constexpr (F32) {
     const float *p = static_cast<const float *>(base) + off;
     if (vec) {
-      const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
-      const float4 b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+      r.q[0] = __ldcs(reinterpret_cast<const uint4 *>(p));
+      r.q[1] = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = p[i];
+      const uint32_t *u = reinterpret_cast<const uint32_t *>(p);
+      r.q[0] = make_uint4(u[0], u[1], u[2], u[3]);
+      r.q[1] = make_uint4(u[4], u[5], u[6], u[7]);
     }
   } else {
     const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(base) + off;
     if (vec) {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
-      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      }
+      r.q[0] = __ldcs(reinterpret_cast<const uint4 *>(p));
     } else {
+      const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
+      r.q[0] = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+    }
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void values(const Raw<F32> &r, float (&x)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __bfloat162float(p[i]);
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    const uint32_t u[4] = {r.q[i].x, r.q[i].y, r.q[i].z, r.q[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (F32) {
+        x[4 * i + k] = __uint_as_float(u[k]);
+      } else {
+        x[2 * k] = __uint_as_float(u[k] << 16);
+        x[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+      }
     }
   }
 }
@@ -98,14 +111,15 @@ struct AP {
   bool vec;
 };
 
-template <int D, bool E4M3, bool F32>
+// U rows per group of lanes, whose loads come first: one where the call is
+// small (latency), four (two of float32) where it streams.
+template <int D, bool E4M3, bool F32, int U>
 __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ AP P) {
   constexpr int LPR = D == 64 ? 8 : 16;   // lanes per row
   constexpr int RPC = NT / LPR;           // rows per CTA and pass
   const View &w = P.w;
   const int lane = threadIdx.x % LPR;
   const bool on = lane * 8 < D;
-  const uint32_t r = blockIdx.x * RPC + threadIdx.x / LPR;
   if (P.status) {  // one thread per sequence reports
     const uint32_t b = blockIdx.x * NT + threadIdx.x;
     if (b < static_cast<uint32_t>(w.B)) {
@@ -119,49 +133,57 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ AP P
       P.status[b] = st;
     }
   }
-  if (blockIdx.x * static_cast<uint64_t>(RPC) >= P.total) return;  // a CTA for status only
-  bool live = r < P.total;
-  const uint32_t h = r % w.Hkv, bt = r / w.Hkv;
-  const uint32_t t = bt % w.N, b = live ? bt / w.N : 0;
-  float x[8] = {}, y[8] = {};
-  if (live && on) {
-    load8<F32>(P.k.p, b * P.k.s0 + t * P.k.s1 + h * P.k.s2 + lane * 8, P.vec, x);
-    load8<F32>(P.v.p, b * P.v.s0 + t * P.v.s1 + h * P.v.s2 + lane * 8, P.vec, y);
+  const uint32_t r0 = blockIdx.x * (RPC * U) + threadIdx.x / LPR;
+  if (blockIdx.x * static_cast<uint64_t>(RPC * U) >= P.total) return;  // a CTA for status only
+  Raw<F32> k[U], v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t r = r0 + u * RPC;
+    if (r < P.total && on) {
+      const uint32_t h = r % w.Hkv, bt = r / w.Hkv, t = bt % w.N, b = bt / w.N;
+      load8<F32>(P.k.p, b * P.k.s0 + t * P.k.s1 + h * P.k.s2 + lane * 8, P.vec, k[u]);
+      load8<F32>(P.v.p, b * P.v.s0 + t * P.v.s1 + h * P.v.s2 + lane * 8, P.vec, v[u]);
+    }
   }
-  int own = 0, n = 0;
-  if (live) kv::row_shape(w, b, own, n);
-  live = live && t < static_cast<uint32_t>(n);
-  int page = -1;
-  if (live) page = w.table[b * w.tstride + ((own + static_cast<int>(t)) >> w.ps_log2)];
-  live = live && static_cast<uint32_t>(page) < static_cast<uint32_t>(w.n_pages);
-  const int slot = (own + static_cast<int>(t)) & ((1 << w.ps_log2) - 1);
-  const int64_t at = (static_cast<int64_t>(h) << w.ps_log2) + slot;  // row within the page
-  if constexpr (E4M3) {
-    const int ek = row_exp(row_max<LPR>(x, on)), ev = row_exp(row_max<LPR>(y, on));
-    if (!live) return;
-    if (on) {
-      const float sk = kv::pow2i(-ek), sv = kv::pow2i(-ev);
-      uint2 a, c;
-      a.x = kv::stored2(x[0] * sk, x[1] * sk) | kv::stored2(x[2] * sk, x[3] * sk) << 16;
-      a.y = kv::stored2(x[4] * sk, x[5] * sk) | kv::stored2(x[6] * sk, x[7] * sk) << 16;
-      c.x = kv::stored2(y[0] * sv, y[1] * sv) | kv::stored2(y[2] * sv, y[3] * sv) << 16;
-      c.y = kv::stored2(y[4] * sv, y[5] * sv) | kv::stored2(y[6] * sv, y[7] * sv) << 16;
-      *reinterpret_cast<uint2 *>(P.kp + page * w.kps + at * D + lane * 8) = a;
-      *reinterpret_cast<uint2 *>(P.vp + page * w.vps + at * D + lane * 8) = c;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t r = r0 + u * RPC, h = r % w.Hkv, bt = r / w.Hkv, t = bt % w.N, b = bt / w.N;
+    bool live = r < P.total;
+    int own = 0, n = 0, page = -1;
+    if (live) kv::row_shape(w, b, own, n);
+    live = live && t < static_cast<uint32_t>(n);
+    if (live) page = w.table[b * w.tstride + ((own + static_cast<int>(t)) >> w.ps_log2)];
+    live = live && static_cast<uint32_t>(page) < static_cast<uint32_t>(w.n_pages);
+    const int slot = (own + static_cast<int>(t)) & ((1 << w.ps_log2) - 1);
+    const int64_t at = (static_cast<int64_t>(h) << w.ps_log2) + slot;  // row within the page
+    float x[8], y[8];
+    values<F32>(k[u], x);
+    values<F32>(v[u], y);
+    if constexpr (E4M3) {
+      const int ek = row_exp(row_max<LPR>(x, live && on)), ev = row_exp(row_max<LPR>(y, live && on));
+      if (!live) continue;
+      if (on) {
+        const float sk = kv::pow2i(-ek), sv = kv::pow2i(-ev);
+        uint2 a, c;
+        a.x = kv::stored2(x[0] * sk, x[1] * sk) | kv::stored2(x[2] * sk, x[3] * sk) << 16;
+        a.y = kv::stored2(x[4] * sk, x[5] * sk) | kv::stored2(x[6] * sk, x[7] * sk) << 16;
+        c.x = kv::stored2(y[0] * sv, y[1] * sv) | kv::stored2(y[2] * sv, y[3] * sv) << 16;
+        c.y = kv::stored2(y[4] * sv, y[5] * sv) | kv::stored2(y[6] * sv, y[7] * sv) << 16;
+        *reinterpret_cast<uint2 *>(P.kp + page * w.kps + at * D + lane * 8) = a;
+        *reinterpret_cast<uint2 *>(P.vp + page * w.vps + at * D + lane * 8) = c;
+      }
+      if (lane == 0) {
+        const int64_t s = ((static_cast<int64_t>(page) * w.Hkv) << w.ps_log2) + at;
+        P.ke[s] = static_cast<int8_t>(ek);
+        P.ve[s] = static_cast<int8_t>(ev);
+      }
+    } else {
+      if (!live || !on) continue;
+      *reinterpret_cast<uint4 *>(P.kp + page * w.kps + (at * D + lane * 8) * 2) =
+          make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+      *reinterpret_cast<uint4 *>(P.vp + page * w.vps + (at * D + lane * 8) * 2) =
+          make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
     }
-    if (lane == 0) {
-      const int64_t s = ((static_cast<int64_t>(page) * w.Hkv) << w.ps_log2) + at;
-      P.ke[s] = static_cast<int8_t>(ek);
-      P.ve[s] = static_cast<int8_t>(ev);
-    }
-  } else {
-    if (!live || !on) return;
-    const uint4 a = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                     pack_bf16(x[6], x[7])};
-    const uint4 c = {pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                     pack_bf16(y[6], y[7])};
-    *reinterpret_cast<uint4 *>(P.kp + page * w.kps + (at * D + lane * 8) * 2) = a;
-    *reinterpret_cast<uint4 *>(P.vp + page * w.vps + (at * D + lane * 8) * 2) = c;
   }
 }
 
@@ -287,8 +309,13 @@ void by_head(int D, F f) {
   else f(std::integral_constant<int, 128>());
 }
 
-unsigned grid_of(uint32_t rows, int D, int B, bool status) {
-  const uint32_t rpc = NT / (D == 64 ? 8 : 16);
+// Rows per group of lanes: several once the call fills the machine twice over.
+int rows_per_group(uint32_t rows, int D, int most) {
+  return rows >= 2u * 152 * 8 * (NT / (D == 64 ? 8 : 16)) ? most : 1;
+}
+
+unsigned grid_of(uint32_t rows, int D, int B, bool status, int u) {
+  const uint32_t rpc = NT / (D == 64 ? 8 : 16) * u;
   const uint32_t g = (rows + rpc - 1) / rpc, s = status ? (B + NT - 1) / NT : 0;
   return g > s ? g : s;
 }
@@ -323,15 +350,16 @@ extern "C" spec_status spec_kv_append(const spec_kv_cache *cache, const spec_kv_
   P.ve = cache->v_exp;
   P.status = row_status;
   P.total = static_cast<uint32_t>(rows);
-  const unsigned grid = grid_of(P.total, cache->head_dim, P.w.B, row_status != nullptr);
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool q = cache->format == SPEC_KV_E4M3, f = dtype == SPEC_F32;
+  const int u = rows_per_group(P.total, cache->head_dim, f ? 2 : 4);
+  const unsigned grid = grid_of(P.total, cache->head_dim, P.w.B, row_status != nullptr, u);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   by_head(cache->head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (q && f) append_kernel<D, true, true><<<grid, NT, 0, s>>>(P);
-    else if (q) append_kernel<D, true, false><<<grid, NT, 0, s>>>(P);
-    else if (f) append_kernel<D, false, true><<<grid, NT, 0, s>>>(P);
-    else append_kernel<D, false, false><<<grid, NT, 0, s>>>(P);
+    if (q && f) u > 1 ? append_kernel<D, true, true, 2><<<grid, NT, 0, s>>>(P) : append_kernel<D, true, true, 1><<<grid, NT, 0, s>>>(P);
+    else if (q) u > 1 ? append_kernel<D, true, false, 4><<<grid, NT, 0, s>>>(P) : append_kernel<D, true, false, 1><<<grid, NT, 0, s>>>(P);
+    else if (f) u > 1 ? append_kernel<D, false, true, 2><<<grid, NT, 0, s>>>(P) : append_kernel<D, false, true, 1><<<grid, NT, 0, s>>>(P);
+    else u > 1 ? append_kernel<D, false, false, 4><<<grid, NT, 0, s>>>(P) : append_kernel<D, false, false, 1><<<grid, NT, 0, s>>>(P);
   });
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
@@ -358,7 +386,7 @@ extern "C" spec_status spec_kv_read(const spec_kv_cache *cache, const spec_kv_ba
   P.total = static_cast<uint32_t>(rows);
   P.begin = begin;
   P.n = n;
-  const unsigned grid = grid_of(P.total, cache->head_dim, P.w.B, row_status != nullptr);
+  const unsigned grid = grid_of(P.total, cache->head_dim, P.w.B, row_status != nullptr, 1);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool q = cache->format == SPEC_KV_E4M3, f = dtype == SPEC_F32;
   by_head(cache->head_dim, [&](auto d) {

@@ -127,6 +127,8 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
   uint32_t *cum0 = reinterpret_cast<uint32_t *>(sm + C::FIXED);  // B + 1: tiles or rows before b
   uint32_t *cum1 = cum0 + P.w.B + 1;                             // B + 1: items before b (own)
 
+  // the merge kernel may be set up meanwhile; it waits for this grid's end
+  cudaTriggerProgrammaticLaunchCompletion();
   const View &w = P.w;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wr = warp / WT, wt = warp % WT;
