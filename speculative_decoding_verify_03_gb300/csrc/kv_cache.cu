@@ -79,17 +79,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&t);
 }
 
-// Largest finite magnitude of the row as bits (the order of non-negative
-// floats is that of their bits); lanes of a group of LPR hold 8 elements each.
-template <int LPR>
-__device__ __forceinline__ uint32_t row_max(const float (&x)[8], bool on) {
+// Largest magnitude of the lane's eight elements as float bits (the order of
+// non-negative floats is that of their bits); `finite`: of the finite ones.
+template <bool F32>
+__device__ __forceinline__ uint32_t most8(const Raw<F32> &r, bool finite) {
   uint32_t m = 0;
+  auto take = [&](uint32_t a) { m = max(m, finite && a >= 0x7f800000u ? 0u : a); };
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t a = __float_as_uint(x[i]) & 0x7fffffffu;
-    m = max(m, a < 0x7f800000u ? a : 0u);
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    const uint32_t u[4] = {r.q[i].x, r.q[i].y, r.q[i].z, r.q[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (F32) {
+        take(u[k] & 0x7fffffffu);
+      } else {
+        take(u[k] & 0x7fff0000u);
+        take(u[k] << 16 & 0x7fff0000u);
+      }
+    }
   }
-  if (!on) m = 0;
+  return m;
+}
+template <int LPR>
+__device__ __forceinline__ uint32_t group_max(uint32_t m) {
 #pragma unroll
   for (int o = LPR / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
@@ -107,12 +119,22 @@ struct AP {
   uint8_t *kp, *vp;
   int8_t *ke, *ve;
   int32_t *status;
-  uint32_t total;  // rows: B * N * Hkv
+  uint32_t total;  // rows of a sequence: N * Hkv
   bool vec;
 };
 
-// U rows per group of lanes, whose loads come first: one where the call is
-// small (latency), four (two of float32) where it streams.
+// Eight elements times s as e4m3; `odd`: there may be infinities.
+__device__ __forceinline__ uint2 store8(const float (&x)[8], float s, bool odd) {
+  uint32_t t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    t[i] = odd ? kv::stored2(x[2 * i] * s, x[2 * i + 1] * s) : kv::finite2(x[2 * i] * s, x[2 * i + 1] * s);
+  return make_uint2(t[0] | t[1] << 16, t[2] | t[3] << 16);
+}
+
+// Grid: rows (t, h) of a sequence, by sequences.  U rows per group of lanes,
+// whose loads come first: one where the call is small (latency), four (two of
+// float32) where it streams.
 template <int D, bool E4M3, bool F32, int U>
 __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ AP P) {
   constexpr int LPR = D == 64 ? 8 : 16;   // lanes per row
@@ -120,68 +142,62 @@ __global__ void __launch_bounds__(NT) append_kernel(const __grid_constant__ AP P
   const View &w = P.w;
   const int lane = threadIdx.x % LPR;
   const bool on = lane * 8 < D;
-  if (P.status) {  // one thread per sequence reports
-    const uint32_t b = blockIdx.x * NT + threadIdx.x;
-    if (b < static_cast<uint32_t>(w.B)) {
-      int own, n;
-      int st = kv::row_shape(w, b, own, n);
-      const int32_t *t = w.table + b * w.tstride;
-      if (n > 0)
-        for (int p = own >> w.ps_log2; p <= (own + n - 1) >> w.ps_log2; ++p)
-          if (static_cast<uint32_t>(t[p]) >= static_cast<uint32_t>(w.n_pages))
-            st |= SPEC_ROW_BAD_PAGE;
-      P.status[b] = st;
-    }
-  }
+  const uint32_t b = blockIdx.y;
   const uint32_t r0 = blockIdx.x * (RPC * U) + threadIdx.x / LPR;
-  if (blockIdx.x * static_cast<uint64_t>(RPC * U) >= P.total) return;  // a CTA for status only
-  Raw<F32> k[U], v[U];
+  Raw<F32> k[U] = {}, v[U] = {};
+  uint32_t tok[U], head[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const uint32_t r = r0 + u * RPC;
+    tok[u] = r / w.Hkv;
+    head[u] = r - tok[u] * w.Hkv;
     if (r < P.total && on) {
-      const uint32_t h = r % w.Hkv, bt = r / w.Hkv, t = bt % w.N, b = bt / w.N;
-      load8<F32>(P.k.p, b * P.k.s0 + t * P.k.s1 + h * P.k.s2 + lane * 8, P.vec, k[u]);
-      load8<F32>(P.v.p, b * P.v.s0 + t * P.v.s1 + h * P.v.s2 + lane * 8, P.vec, v[u]);
+      load8<F32>(P.k.p, b * P.k.s0 + tok[u] * P.k.s1 + head[u] * P.k.s2 + lane * 8, P.vec, k[u]);
+      load8<F32>(P.v.p, b * P.v.s0 + tok[u] * P.v.s1 + head[u] * P.v.s2 + lane * 8, P.vec, v[u]);
     }
+  }
+  int own, n;
+  int st = kv::row_shape(w, b, own, n);
+  const int32_t *ids = w.table + b * w.tstride;
+  if (P.status && blockIdx.x == 0 && threadIdx.x == 0) {
+    if (n > 0)
+      for (int p = own >> w.ps_log2; p <= (own + n - 1) >> w.ps_log2; ++p)
+        if (static_cast<uint32_t>(ids[p]) >= static_cast<uint32_t>(w.n_pages)) st |= SPEC_ROW_BAD_PAGE;
+    P.status[b] = st;
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t r = r0 + u * RPC, h = r % w.Hkv, bt = r / w.Hkv, t = bt % w.N, b = bt / w.N;
-    bool live = r < P.total;
-    int own = 0, n = 0, page = -1;
-    if (live) kv::row_shape(w, b, own, n);
-    live = live && t < static_cast<uint32_t>(n);
-    if (live) page = w.table[b * w.tstride + ((own + static_cast<int>(t)) >> w.ps_log2)];
-    live = live && static_cast<uint32_t>(page) < static_cast<uint32_t>(w.n_pages);
-    const int slot = (own + static_cast<int>(t)) & ((1 << w.ps_log2) - 1);
-    const int64_t at = (static_cast<int64_t>(h) << w.ps_log2) + slot;  // row within the page
+    const int t = static_cast<int>(tok[u]);
+    const bool live = r0 + u * RPC < P.total && t < n;
+    const int id = live ? __ldg(ids + ((own + t) >> w.ps_log2)) : -1;
+    const bool put = static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages);
+    const uint32_t at = (head[u] << w.ps_log2) + ((own + t) & ((1 << w.ps_log2) - 1));  // row within the page
     float x[8], y[8];
     values<F32>(k[u], x);
     values<F32>(v[u], y);
     if constexpr (E4M3) {
-      const int ek = row_exp(row_max<LPR>(x, live && on)), ev = row_exp(row_max<LPR>(y, live && on));
-      if (!live) continue;
+      uint32_t mk = group_max<LPR>(most8<F32>(k[u], false)), mv = group_max<LPR>(most8<F32>(v[u], false));
+      const bool odd = __any_sync(0xffffffffu, max(mk, mv) >= 0x7f800000u);
+      if (odd) {  // rare: NaN or infinities among the warp's rows
+        mk = group_max<LPR>(most8<F32>(k[u], true));
+        mv = group_max<LPR>(most8<F32>(v[u], true));
+      }
+      const int ek = row_exp(mk), ev = row_exp(mv);
+      if (!put) continue;
       if (on) {
-        const float sk = kv::pow2i(-ek), sv = kv::pow2i(-ev);
-        uint2 a, c;
-        a.x = kv::stored2(x[0] * sk, x[1] * sk) | kv::stored2(x[2] * sk, x[3] * sk) << 16;
-        a.y = kv::stored2(x[4] * sk, x[5] * sk) | kv::stored2(x[6] * sk, x[7] * sk) << 16;
-        c.x = kv::stored2(y[0] * sv, y[1] * sv) | kv::stored2(y[2] * sv, y[3] * sv) << 16;
-        c.y = kv::stored2(y[4] * sv, y[5] * sv) | kv::stored2(y[6] * sv, y[7] * sv) << 16;
-        *reinterpret_cast<uint2 *>(P.kp + page * w.kps + at * D + lane * 8) = a;
-        *reinterpret_cast<uint2 *>(P.vp + page * w.vps + at * D + lane * 8) = c;
+        *reinterpret_cast<uint2 *>(P.kp + id * w.kps + at * D + lane * 8) = store8(x, kv::pow2i(-ek), odd);
+        *reinterpret_cast<uint2 *>(P.vp + id * w.vps + at * D + lane * 8) = store8(y, kv::pow2i(-ev), odd);
       }
       if (lane == 0) {
-        const int64_t s = ((static_cast<int64_t>(page) * w.Hkv) << w.ps_log2) + at;
+        const int64_t s = ((static_cast<int64_t>(id) * w.Hkv) << w.ps_log2) + at;
         P.ke[s] = static_cast<int8_t>(ek);
         P.ve[s] = static_cast<int8_t>(ev);
       }
     } else {
-      if (!live || !on) continue;
-      *reinterpret_cast<uint4 *>(P.kp + page * w.kps + (at * D + lane * 8) * 2) =
+      if (!put || !on) continue;
+      *reinterpret_cast<uint4 *>(P.kp + id * w.kps + (at * D + lane * 8) * 2) =
           make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-      *reinterpret_cast<uint4 *>(P.vp + page * w.vps + (at * D + lane * 8) * 2) =
+      *reinterpret_cast<uint4 *>(P.vp + id * w.vps + (at * D + lane * 8) * 2) =
           make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
     }
   }
@@ -309,13 +325,8 @@ void by_head(int D, F f) {
   else f(std::integral_constant<int, 128>());
 }
 
-// Rows per group of lanes: several once the call fills the machine twice over.
-int rows_per_group(uint32_t rows, int D, int most) {
-  return rows >= 2u * 152 * 8 * (NT / (D == 64 ? 8 : 16)) ? most : 1;
-}
-
-unsigned grid_of(uint32_t rows, int D, int B, bool status, int u) {
-  const uint32_t rpc = NT / (D == 64 ? 8 : 16) * u;
+unsigned grid_of(uint32_t rows, int D, int B, bool status) {
+  const uint32_t rpc = NT / (D == 64 ? 8 : 16);
   const uint32_t g = (rows + rpc - 1) / rpc, s = status ? (B + NT - 1) / NT : 0;
   return g > s ? g : s;
 }
@@ -337,8 +348,8 @@ extern "C" spec_status spec_kv_append(const spec_kv_cache *cache, const spec_kv_
   const uintptr_t es = dtype == SPEC_F32 ? 4 : 2;
   if (!k || !v || reinterpret_cast<uintptr_t>(k) % es || reinterpret_cast<uintptr_t>(v) % es)
     return SPEC_ERR_INVALID_ARG;
-  const int64_t rows = static_cast<int64_t>(P.w.B) * P.w.N * P.w.Hkv;
-  if (rows >= INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+  const int64_t rows = static_cast<int64_t>(P.w.N) * P.w.Hkv;
+  if (rows >= INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
   uintptr_t bits = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v);
   for (int i = 0; i < 3; ++i) bits |= static_cast<uintptr_t>(k_strides[i] | v_strides[i]) * es;
   P.vec = bits % 16 == 0;
@@ -351,8 +362,10 @@ extern "C" spec_status spec_kv_append(const spec_kv_cache *cache, const spec_kv_
   P.status = row_status;
   P.total = static_cast<uint32_t>(rows);
   const bool q = cache->format == SPEC_KV_E4M3, f = dtype == SPEC_F32;
-  const int u = rows_per_group(P.total, cache->head_dim, f ? 2 : 4);
-  const unsigned grid = grid_of(P.total, cache->head_dim, P.w.B, row_status != nullptr, u);
+  // Several rows per group of lanes once the call fills the machine twice over.
+  const uint32_t rpc = NT / (cache->head_dim == 64 ? 8 : 16);
+  const uint32_t u = rows * P.w.B >= 2ll * 152 * 8 * rpc ? (f ? 2 : 4) : 1;
+  const dim3 grid((P.total + rpc * u - 1) / (rpc * u), P.w.B);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   by_head(cache->head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
@@ -386,7 +399,7 @@ extern "C" spec_status spec_kv_read(const spec_kv_cache *cache, const spec_kv_ba
   P.total = static_cast<uint32_t>(rows);
   P.begin = begin;
   P.n = n;
-  const unsigned grid = grid_of(P.total, cache->head_dim, P.w.B, row_status != nullptr, 1);
+  const unsigned grid = grid_of(P.total, cache->head_dim, P.w.B, row_status != nullptr);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool q = cache->format == SPEC_KV_E4M3, f = dtype == SPEC_F32;
   by_head(cache->head_dim, [&](auto d) {

@@ -119,15 +119,16 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two floats as e4m3, to nearest even, saturating, an infinity (which e4m3 does
-// not have) to NaN.
-__device__ __forceinline__ uint32_t stored2(float lo, float hi) {
-  const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
-  if (fabsf(lo) == inf) lo = nan;
-  if (fabsf(hi) == inf) hi = nan;
+// Two floats as e4m3, to nearest even, saturating; stored2: an infinity (which
+// e4m3 does not have) to NaN.
+__device__ __forceinline__ uint32_t finite2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ uint32_t stored2(float lo, float hi) {
+  const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
+  return finite2(fabsf(lo) == inf ? nan : lo, fabsf(hi) == inf ? nan : hi);
 }
 // 2^e as a float, e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }

@@ -38,7 +38,7 @@ constexpr int DN_FETCH = 256;  // of them loading
 constexpr int DN_TILE = 128;   // key tokens per tile
 constexpr int DN_RING = 8;     // tiles whose exponents are kept
 // Registers per thread: at launch (5 warpgroups), softmax (2), loading (2), the rest.
-constexpr int DN_REGS = 96, DN_SOFT = 112, DN_LOAD = 104, DN_REST = 48;
+constexpr int DN_REGS = 96, DN_SOFT = 136, DN_LOAD = 80, DN_REST = 48;
 static_assert(2 * DN_SOFT + 2 * DN_LOAD + DN_REST <= 5 * DN_REGS, "registers");
 
 template <int D>
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   };
 
   if (warp < 8) {
-    regs_up<DN_SOFT>();
+    regs_to<DN_SOFT, DN_REGS>();
     // ================================================= softmax and output
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 TMEM lanes a warp
@@ -231,32 +231,50 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       bar_wait(s32(&S.sfull[half]), t & 1, dead);
       tc_after();
       const int n = w.prefix - tt * DN_TILE;  // tokens of the tile
-      // 32 scores at a time, the next ones on their way
+      // 16 scores at a time, the next ones on their way
       auto over_scores = [&](auto f) {
-        float s[2][32];
-        tmem_ld32(sc, s[0]);
+        float s[2][16];
+        tmem_ld16(sc, s[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld(s[c & 1], 32);
-          if (c < 3) tmem_ld32(sc + 32 * (c + 1), s[c + 1 & 1]);
+        for (int c = 0; c < 8; ++c) {
+          tmem_wait_ld(s[c & 1], 16);
+          if (c < 7) tmem_ld16(sc + 16 * (c + 1), s[c + 1 & 1]);
           if (n < DN_TILE) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= n) s[c & 1][i] = -INFINITY;
+            for (int i = 0; i < 16; ++i)
+              if (16 * c + i >= n) s[c & 1][i] = -INFINITY;
           }
           f(c, s[c & 1]);
         }
       };
-      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      over_scores([&](int, const float (&s)[32]) {
+      if (fresh) {  // the first tile's exact maximum
+        float m = -INFINITY;
+        over_scores([&](int, const float (&s)[16]) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
+          for (int i = 0; i < 16; ++i) m = fmaxf(m, s[i]);
+        });
+        M = fmaxf(kNone, fmaf(m, kt, F));
+      }
+      // the weights with the maximum so far; only where a score passes it by more
+      // than the slack, again with the new one (the scores are still there)
+      uint32_t p[64];
+      float2 acc[2];
+      for (bool again = false;; again = true) {
+        const float2 k2 = {kt, kt}, b2 = {F - M + BIAS, F - M + BIAS};
+        acc[0] = acc[1] = make_float2(0.0f, 0.0f);
+        float far = -INFINITY;
+        over_scores([&](int c, const float (&s)[16]) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(fmaxf(m4[k], s[i + k]), s[i + 4 + k]);
-      });
-      const float m = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kt, F);
-      if (__any_sync(~0u, fresh || m > M + SLACK)) {
-        const float nm = fmaxf(M, m), f = ex2(M - nm);
+          for (int i = 0; i < 8; ++i) {
+            float2 z = fma2(make_float2(s[2 * i], s[2 * i + 1]), k2, b2);
+            far = fmaxf(fmaxf(far, z.x), z.y);
+            z.x = ex2(z.x), z.y = ex2(z.y);
+            acc[i & 1] = add2(acc[i & 1], z);
+            p[8 * c + i] = pack<E4M3>(z.x, z.y);
+          }
+        });
+        if (again || !__any_sync(~0u, far > BIAS + SLACK)) break;
+        const float nm = far > BIAS + SLACK ? M + (far - BIAS) : M, f = ex2(M - nm);
         M = nm;
         l *= f;
         if (!fresh) {
@@ -264,28 +282,18 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           tc_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
+            float o[16];
             tmem_ld16(oc + c, o);
+            tmem_wait_ld(o, 16);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st16(oc + c, o);
+            for (int i = 0; i < 16; ++i) o[i] *= f;
+            tmem_st16(oc + c, reinterpret_cast<const uint32_t *>(o));
           }
           tmem_wait_st();
         }
       }
-      const float2 k2 = {kt, kt}, b2 = {F - M + BIAS, F - M + BIAS};
-      float2 acc[2] = {{0, 0}, {0, 0}};
-      over_scores([&](int c, const float (&s)[32]) {
-        uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 z = fma2(make_float2(s[2 * i], s[2 * i + 1]), k2, b2);
-          z.x = ex2(z.x), z.y = ex2(z.y);
-          acc[i & 1] = add2(acc[i & 1], z);
-          p[i] = pack<E4M3>(z.x, z.y);
-        }
-        tmem_st16(sc + 16 * c, p);  // over scores that are read
-      });
+      for (int c = 0; c < 4; ++c) tmem_st16(sc + 16 * c, p + 16 * c);  // over the scores
       acc[0] = add2(acc[0], acc[1]);
       l = fmaf(acc[0].x + acc[0].y, invF, l);
       tmem_wait_st();
@@ -304,14 +312,13 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         float *dst = P.po + at * D;
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
-          uint32_t o[16];
+          float o[16];
           tmem_ld16(oc + c, o);
+          tmem_wait_ld(o, 16);
           if (there) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4 *>(dst + c + 4 * i) =
-                  make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
-                              __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<float4 *>(dst + c + i) = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
           }
         }
         tc_before();
@@ -320,7 +327,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       if (++tt == nt) tt = 0, ++item;
     }
   } else if (warp < 16) {
-    regs_up<DN_LOAD>();
+    regs_to<DN_LOAD, DN_REGS>();
     // ============================================ queries, keys and values
     const int p = tid - 256;
     const int lg = w.ps_log2, pm = (1 << lg) - 1;
@@ -328,10 +335,6 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     if constexpr (E4M3) {
       constexpr int CPR = D / 16, ALL = DN_TILE * CPR;      // 16-byte chunks of a row, of a tile
       constexpr int PASS = (ALL + DN_FETCH - 1) / DN_FETCH;  // chunks per thread
-      struct Set {
-        uint4 k[PASS], v[PASS];
-        uint32_t ek, ev;  // exponents of the lane's four tokens; -128 where there is none
-      };
       int id[PASS], ide = -1;  // page ids of the tile to be fetched next
       auto pages = [&](int tile) {
         const int t0 = tile * DN_TILE;
@@ -342,31 +345,29 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         }
         ide = t0 + 4 * lane < w.prefix ? ldg_now(w.ptable + (t0 + 4 * lane >> lg)) : -1;
       };
-      auto fetch = [&](Set &s, int it, int tile) {
-        const uint32_t head = it / nj, row0 = head << lg;
+      auto fetch = [&](uint4 (&q)[PASS], const uint8_t *src, int64_t stride, int it, int tile) {
+        const uint32_t row0 = static_cast<uint32_t>(it / nj) << lg;
         const int t0 = tile * DN_TILE;
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
           const int x = p + i * DN_FETCH, row = x / CPR;
-          s.k[i] = s.v[i] = make_uint4(0, 0, 0, 0);
-          if (static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(w.n_pages)) {
-            const uint32_t at = (row0 + (t0 + row & pm)) * D + (x - row * CPR) * 16;
-            s.k[i] = ldg_now16(w.k + id[i] * w.kps + at);
-            s.v[i] = ldg_now16(w.v + id[i] * w.vps + at);
-          }
+          q[i] = make_uint4(0, 0, 0, 0);
+          if (static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(w.n_pages))
+            q[i] = ldg_now16(src + id[i] * stride + (row0 + (t0 + row & pm)) * D + (x - row * CPR) * 16);
         }
-        const int tok = t0 + 4 * lane, n = w.prefix - tok;
-        s.ek = s.ev = 0x80808080u;
+      };
+      // exponents of the lane's four tokens; -128 where there is none
+      auto exps = [&](const int8_t *src, int it, int tile) {
+        const int tok = tile * DN_TILE + 4 * lane, n = w.prefix - tok;
+        uint32_t v = 0x80808080u;
         if (static_cast<uint32_t>(ide) < static_cast<uint32_t>(w.n_pages)) {
-          const int64_t at = ((static_cast<int64_t>(ide) * w.Hkv + head) << lg) + (tok & pm);
-          s.ek = ldg_now32(w.ke + at);
-          s.ev = ldg_now32(w.ve + at);
+          v = ldg_now32(src + ((static_cast<int64_t>(ide) * w.Hkv + it / nj) << lg) + (tok & pm));
           if (n < 4) {
             const uint32_t in = (1u << 8 * n) - 1;
-            s.ek = (s.ek & in) | (0x80808080u & ~in);
-            s.ev = (s.ev & in) | (0x80808080u & ~in);
+            v = (v & in) | (0x80808080u & ~in);
           }
         }
+        return v;
       };
       auto top = [&](uint32_t v) {  // seven below the tile's largest
         int m = -128;
@@ -402,39 +403,41 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       auto next = [&](int &it, int &tile) {
         if (++tile == nt) tile = 0, ++it;
       };
-      // tile t from `now`, the loads of tile t + 1 into `then`
-      int ni = item, nx = tt;
-      auto turn = [&](int t, Set &now, Set &then) {
-        const int st = t & 1;
-        next(ni, nx);
-        if (t + 1 < tiles) {
-          fetch(then, ni, nx);
-          pages(nx + 1 == nt ? 0 : nx + 1);
-        }
-        const int E = top(now.ek), F = top(now.ev);
+      // the loads of a tile's keys are issued when the keys before are stored, and
+      // so the values': a tile ahead
+      uint4 k[PASS], v[PASS];
+      uint32_t ek = 0, ev = 0;
+      if (tiles > 0) {
+        pages(tt);
+        fetch(k, w.k, w.kps, item, tt);
+        ek = exps(w.ke, item, tt);
+        fetch(v, w.v, w.vps, item, tt);
+        ev = exps(w.ve, item, tt);
+      }
+      for (int t = 0; t < tiles; ++t) {
+        const int st = t & 1, E = top(ek), F = top(ev);
+        next(item, tt);
+        if (t + 1 < tiles) pages(tt);
         if (t >= 2) bar_wait(s32(&S.kempty[st]), (t >> 1) - 1 & 1, dead);
-        store(base + C::K + st * C::OP, now.k, now.ek, E);
+        store(base + C::K + st * C::OP, k, ek, E);
         if (p == 0) S.exps[t % DN_RING] = make_int2(E, F);
         fence_async();
         __syncwarp();
         if (lane == 0) bar_arrive(s32(&S.kfull[st]));
         if (p == 0) bar_arrive(s32(&S.consts[t % DN_RING]));
+        if (t + 1 < tiles) {
+          fetch(k, w.k, w.kps, item, tt);
+          ek = exps(w.ke, item, tt);
+        }
         if (t >= 2) bar_wait(s32(&S.vempty[st]), (t >> 1) - 1 & 1, dead);
-        store(base + C::V + st * C::OP, now.v, now.ev, F);
+        store(base + C::V + st * C::OP, v, ev, F);
         fence_async();
         __syncwarp();
         if (lane == 0) bar_arrive(s32(&S.vfull[st]));
-        next(item, tt);
-      };
-      Set sa, sb;
-      if (tiles > 0) {
-        pages(tt);
-        fetch(sa, item, tt);
-        pages(tt + 1 == nt ? 0 : tt + 1);
-      }
-      for (int t = 0; t < tiles; t += 2) {
-        turn(t, sa, sb);
-        if (t + 1 < tiles) turn(t + 1, sb, sa);
+        if (t + 1 < tiles) {
+          fetch(v, w.v, w.vps, item, tt);
+          ev = exps(w.ve, item, tt);
+        }
       }
     } else {
       constexpr int CPR = D / 8;
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       cp_wait<0>();
     }
   } else {
-    regs_down<DN_REST>();
+    regs_to<DN_REST, DN_REGS>();
     // =========================================================== products
     if (warp < 18) {
     const int half = warp - 16;
