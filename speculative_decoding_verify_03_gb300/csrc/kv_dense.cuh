@@ -14,10 +14,11 @@
 // Bound: the tensor cores, and next to them the exponentials (16384 for each
 // 128 x 128 tile beside 2 x 512 cycles of products).  A CTA takes 256 query
 // rows of one key/value head, as two tiles of 128 rows that share each key and
-// value tile and take turns on the tensor cores: one's products run beside the
-// other's softmax.  Scores and outputs are in TMEM (4 x 128 columns); a softmax
-// thread has a row of its own, so nothing is reduced across lanes; the weights
-// go back to TMEM over the scores, as the left operand of P V.
+// value tile.  A key tile is taken in two halves of 64 tokens with a score buffer
+// each, so that a row tile's next scores are formed beside its softmax, and the
+// other row tile's products beside both.  Scores (2 x 2 x 64 columns) and outputs
+// are in TMEM; a softmax thread has a row of its own, so nothing is reduced across
+// lanes; the weights go back to TMEM over the scores, as the left operand of P V.
 //
 // Roles: warps 0-3 and 4-7 queries, softmax and output of a row tile each; warps
 // 8-15 bring keys and values into shared memory (e4m3 through registers as
@@ -50,7 +51,8 @@ struct DenseCfg {
 
 struct DenseShared {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-  uint64_t sfull[2], pfull[2], odone[2], drain[2];  // per row tile
+  uint64_t sfull[2][2], pfull[2][2];         // per row tile and score buffer
+  uint64_t odone[2], ofull[2], drain[2];     // per row tile
   uint64_t consts[DN_RING], qfull[2];
   int2 exps[DN_RING];        // E, F
   uint32_t qmax[DN_ROWS];    // largest finite magnitude of a row, as bfloat16 bits
@@ -78,8 +80,8 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     for (int i = 0; i < 2; ++i) {
       bar_init(s32(&S.kfull[i]), E4M3 ? DN_FETCH / 32 : DN_FETCH), bar_init(s32(&S.kempty[i]), 2);
       bar_init(s32(&S.vfull[i]), E4M3 ? DN_FETCH / 32 : DN_FETCH), bar_init(s32(&S.vempty[i]), 2);
-      bar_init(s32(&S.sfull[i]), 1), bar_init(s32(&S.pfull[i]), 4);
-      bar_init(s32(&S.odone[i]), 1), bar_init(s32(&S.drain[i]), 1);
+      for (int k = 0; k < 2; ++k) bar_init(s32(&S.sfull[i][k]), 1), bar_init(s32(&S.pfull[i][k]), 4);
+      bar_init(s32(&S.odone[i]), 1), bar_init(s32(&S.ofull[i]), 1), bar_init(s32(&S.drain[i]), 1);
     }
     for (int i = 0; i < DN_RING; ++i) bar_init(s32(&S.consts[i]), 1);
     bar_init(s32(&S.qfull[0]), 4), bar_init(s32(&S.qfull[1]), 4);
@@ -144,12 +146,14 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     // ================================================= softmax and output
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 TMEM lanes a warp
-    const uint32_t sc = tmem + lanes + half * 128, oc = tmem + lanes + 256 + half * 128;
+    const uint32_t oc = tmem + lanes + 256 + half * 128;
     const int r = tid;  // row of the item
     int item = item0, tt = first0;
     float M = kNone, l = 0.0f, qc = 0.0f;
     bool fresh = true;
-    for (int t = 0; t < tiles; ++t) {
+    int g = 0;  // items
+    for (int u = 0; u < 2 * tiles; ++u) {
+      const int t = u >> 1;  // half u & 1 of tile t
       if (fresh) {  // the row's query; the products with the item before are done
         const uint32_t row = item % nj * DN_ROWS + r;
         int64_t off = -1;
@@ -228,57 +232,31 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         F = static_cast<float>(x.y);
         invF = pow2i(-x.y);
       }
-      bar_wait(s32(&S.sfull[half]), t & 1, dead);
+      const uint32_t sc = tmem + lanes + half * 128 + (u & 1) * 64;
+      bar_wait(s32(&S.sfull[half][u & 1]), t & 1, dead);
       tc_after();
-      const int n = w.prefix - tt * DN_TILE;  // tokens of the tile
-      // 16 scores at a time, the next ones on their way
-      auto over_scores = [&](auto f) {
-        float s[2][16];
-        tmem_ld16(sc, s[0]);
+      float s[64];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          tmem_wait_ld(s[c & 1], 16);
-          if (c < 7) tmem_ld16(sc + 16 * (c + 1), s[c + 1 & 1]);
-          if (n < DN_TILE) {
+      for (int c = 0; c < 64; c += 16) tmem_ld16(sc + c, s + c);
+      tmem_wait_ld(s, 64);
+      const int n = w.prefix - tt * DN_TILE - (u & 1) * 64;  // tokens from here on
+      if (n < 64) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (16 * c + i >= n) s[c & 1][i] = -INFINITY;
-          }
-          f(c, s[c & 1]);
-        }
-      };
-      if (fresh) {  // the first tile's exact maximum
-        float m = -INFINITY;
-        over_scores([&](int, const float (&s)[16]) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) m = fmaxf(m, s[i]);
-        });
-        M = fmaxf(kNone, fmaf(m, kt, F));
+        for (int c = 0; c < 64; ++c)
+          if (c >= n) s[c] = -INFINITY;
       }
-      // the weights with the maximum so far; only where a score passes it by more
-      // than the slack, again with the new one (the scores are still there)
-      uint32_t p[64];
-      float2 acc[2];
-      for (bool again = false;; again = true) {
-        const float2 k2 = {kt, kt}, b2 = {F - M + BIAS, F - M + BIAS};
-        acc[0] = acc[1] = make_float2(0.0f, 0.0f);
-        float far = -INFINITY;
-        over_scores([&](int c, const float (&s)[16]) {
+      float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float2 z = fma2(make_float2(s[2 * i], s[2 * i + 1]), k2, b2);
-            far = fmaxf(fmaxf(far, z.x), z.y);
-            z.x = ex2(z.x), z.y = ex2(z.y);
-            acc[i & 1] = add2(acc[i & 1], z);
-            p[8 * c + i] = pack<E4M3>(z.x, z.y);
-          }
-        });
-        if (again || !__any_sync(~0u, far > BIAS + SLACK)) break;
-        const float nm = far > BIAS + SLACK ? M + (far - BIAS) : M, f = ex2(M - nm);
+      for (int c = 4; c < 64; c += 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], s[c + i]);
+      const float m = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kt, F);
+      if (__any_sync(~0u, fresh || m > M + SLACK)) {
+        const float nm = fmaxf(M, m), f = ex2(M - nm);
         M = nm;
         l *= f;
         if (!fresh) {
-          bar_wait(s32(&S.odone[half]), t - 1 & 1, dead);  // products up to tile t - 1
+          bar_wait(s32(&S.odone[half]), u - 1 & 1, dead);  // products up to the half tile before
           tc_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -292,22 +270,34 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           tmem_wait_st();
         }
       }
+      const float2 k2 = {kt, kt}, b2 = {F - M + BIAS, F - M + BIAS};
+      float2 acc[2] = {{0, 0}, {0, 0}};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_st16(sc + 16 * c, p + 16 * c);  // over the scores
+      for (int c = 0; c < 2; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float2 z = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), k2, b2);
+          z.x = ex2(z.x), z.y = ex2(z.y);
+          acc[i & 1] = add2(acc[i & 1], z);
+          p[i] = pack<E4M3>(z.x, z.y);
+        }
+        tmem_st16(sc + 16 * c, p);  // over scores that are read
+      }
       acc[0] = add2(acc[0], acc[1]);
       l = fmaf(acc[0].x + acc[0].y, invF, l);
       tmem_wait_st();
       tc_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(s32(&S.pfull[half]));
+      if (lane == 0) bar_arrive(s32(&S.pfull[half][u & 1]));
 
-      const bool last = tt + 1 == nt || t + 1 == tiles;
+      const bool last = (u & 1) && (tt + 1 == nt || t + 1 == tiles);
       if (last) {
         const int64_t at = static_cast<int64_t>(item + blockIdx.x) * DN_ROWS + r;
         const bool there = static_cast<uint32_t>(item % nj * DN_ROWS + r) < rows;
         const float f = l == 0.0f ? 0.0f : 1.0f / l;
         if (there) P.pl[at] = l == 0.0f ? -INFINITY : M - BIAS + log2f(l);
-        bar_wait(s32(&S.odone[half]), t & 1, dead);
+        bar_wait(s32(&S.ofull[half]), g++ & 1, dead);
         tc_after();
         float *dst = P.po + at * D;
 #pragma unroll 1
@@ -324,7 +314,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         tc_before();
       }
       fresh = last;
-      if (++tt == nt) tt = 0, ++item;
+      if ((u & 1) && ++tt == nt) tt = 0, ++item;
     }
   } else if (warp < 16) {
     regs_to<DN_LOAD, DN_REGS>();
@@ -470,46 +460,67 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     // =========================================================== products
     if (warp < 18) {
     const int half = warp - 16;
-    constexpr uint32_t sdesc = mma_desc(E4M3, 128, DN_TILE, false, false);
+    constexpr uint32_t sdesc = mma_desc(E4M3, 128, 64, false, false);
     constexpr uint32_t odesc = mma_desc(E4M3, 128, D, false, true);
     const uint64_t qd = smem_desc(base + C::Q + half * C::OP, 16, 1024), kd = smem_desc(base + C::K, 16, 1024);
     const uint64_t vd = smem_desc(base + C::V, DN_TILE * 128, 1024);
     const uint32_t sc = tmem + half * 128, oc = tmem + 256 + half * 128;
-    int tt = first0, g = 0;
-    bool fresh = true;
-    for (int t = 0; t < tiles; ++t) {
-      const int st = t & 1;
-      if (fresh) bar_wait(s32(&S.qfull[half]), g++ & 1, dead);
-      if (t > 0) bar_wait(s32(&S.odone[half]), t - 1 & 1, dead);  // P of tile t - 1 is read
-      bar_wait(s32(&S.kfull[st]), t >> 1 & 1, dead);
+    int g = 0;
+    // Half tile u, tile tt of its item: scores into buffer u & 1 ...
+    auto scores = [&](int u, int tt) {
+      const int t = u >> 1, st = t & 1;
+      if (!(u & 1) && (t == 0 || tt == 0)) bar_wait(s32(&S.qfull[half]), g++ & 1, dead);
+      // the weights of half tile u - 2 are read; behind an item, all of it is done
+      const bool behind = u > 0 && !(u & 1) && tt == 0;
+      if (u >= 2) bar_wait(s32(&S.odone[half]), behind ? u - 1 & 1 : u & 1, dead);
+      if (!(u & 1)) bar_wait(s32(&S.kfull[st]), t >> 1 & 1, dead);
       if (!E4M3) fence_async();  // the copies' writes, before the products' reads
       tc_after();
       if (lane == 0 && !*dead) {
-        const uint64_t kk = kd + st * (C::OP >> 4);
+        const uint64_t kk = kd + st * (C::OP >> 4) + (u & 1) * (64 * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const int off = (k >> 2) * (DN_TILE * 128) + (k & 3) * 32 >> 4;
-          mma_ss(sc, qd + off, kk + off, sdesc, k > 0);
+          mma_ss(sc + (u & 1) * 64, qd + off, kk + off, sdesc, k > 0);
         }
-        mma_commit(s32(&S.sfull[half]));
-        mma_commit(s32(&S.kempty[st]));
+        mma_commit(s32(&S.sfull[half][u & 1]));
+        if (u & 1) mma_commit(s32(&S.kempty[st]));
       }
       __syncwarp();
-      bar_wait(s32(&S.vfull[st]), t >> 1 & 1, dead);
+    };
+    // ... and its weighted values.
+    auto values = [&](int u, int tt) {
+      const int t = u >> 1, st = t & 1;
+      const bool last = (u & 1) && (tt + 1 == nt || t + 1 == tiles);
+      // (parities tell one phase from the next only: no phase is skipped)
+      if (last) bar_wait(s32(&S.odone[half]), u - 1 & 1, dead);
+      if (!(u & 1)) bar_wait(s32(&S.vfull[st]), t >> 1 & 1, dead);
       if (!E4M3) fence_async();
-      bar_wait(s32(&S.pfull[half]), t & 1, dead);
+      bar_wait(s32(&S.pfull[half][u & 1]), t & 1, dead);
       tc_after();
       if (lane == 0 && !*dead) {
-        const uint64_t vv = vd + st * (C::OP >> 4);
+        const uint64_t vv = vd + st * (C::OP >> 4) + (u & 1) * (64 * 128 >> 4);
+        const bool fresh = !(u & 1) && (t == 0 || tt == 0);
 #pragma unroll
-        for (int k = 0; k < DN_TILE / 16; ++k)
-          mma_ts(oc, sc + 8 * k, vv + (k * 2048 >> 4), odesc, !fresh || k > 0);
+        for (int k = 0; k < 4; ++k)
+          mma_ts(oc, sc + (u & 1) * 64 + 8 * k, vv + (k * 2048 >> 4), odesc, !fresh || k > 0);
         mma_commit(s32(&S.odone[half]));
-        mma_commit(s32(&S.vempty[st]));
+        if (u & 1) mma_commit(s32(&S.vempty[st]));
+        if (last) mma_commit(s32(&S.ofull[half]));
       }
       __syncwarp();
-      fresh = ++tt == nt;
-      if (fresh) tt = 0;
+    };
+    int tt = first0;
+    for (int t = 0; t < tiles; ++t) {
+      // the next half tile's scores before these weights, except behind an item's
+      // last, whose output has to be out before the next item's queries are in
+      const bool last = tt + 1 == nt || t + 1 == tiles;
+      if (t == 0 || tt == 0) scores(2 * t, tt);
+      scores(2 * t + 1, tt);
+      values(2 * t, tt);
+      if (!last) scores(2 * t + 2, tt + 1);
+      values(2 * t + 1, tt);
+      if (++tt == nt) tt = 0;
     }
     if (lane == 0) drained(half);
     __syncwarp();

@@ -66,7 +66,7 @@ __device__ __forceinline__ void tc_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // 16 columns of this warp's 32 lanes: lane i of the warp gets lane i's row.
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&r)[16]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float *r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
