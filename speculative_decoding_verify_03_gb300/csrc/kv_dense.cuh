@@ -21,7 +21,7 @@
 // lanes; the weights go back to TMEM over the scores, as the left operand of P V.
 //
 // Roles: warps 0-3 and 4-7 queries, softmax and output of a row tile each; warps
-// 8-15 bring keys and values into shared memory (e4m3 through registers as
+// 8-11 bring keys, 12-15 values into shared memory (e4m3 through registers as
 // float16, a tile ahead, bfloat16 by asynchronous copies); warps 16 and 17
 // issue the products of a row tile each, as soon as its operands are there.
 // Two stages of keys and of values.
@@ -35,11 +35,11 @@
 namespace kv {
 
 constexpr int DN_NT = 640;     // threads
-constexpr int DN_FETCH = 256;  // of them loading
+constexpr int DN_FETCH = 128;  // of them loading keys; as many load values
 constexpr int DN_TILE = 128;   // key tokens per tile
 constexpr int DN_RING = 8;     // tiles whose exponents are kept
 // Registers per thread: at launch (5 warpgroups), softmax (2), loading (2), the rest.
-constexpr int DN_REGS = 96, DN_SOFT = 136, DN_LOAD = 80, DN_REST = 48;
+constexpr int DN_REGS = 96, DN_SOFT = 120, DN_LOAD = 96, DN_REST = 48;
 static_assert(2 * DN_SOFT + 2 * DN_LOAD + DN_REST <= 5 * DN_REGS, "registers");
 
 template <int D>
@@ -54,8 +54,7 @@ struct DenseShared {
   uint64_t sfull[2][2], pfull[2][2];         // per row tile and score buffer
   uint64_t odone[2], ofull[2], drain[2];     // per row tile
   uint64_t consts[DN_RING], qfull[2];
-  int2 exps[DN_RING];        // E, F
-  uint32_t qmax[DN_ROWS];    // largest finite magnitude of a row, as bfloat16 bits
+  int exps[2][DN_RING];      // E, F
   uint32_t tmem, dead;
   uint32_t sum[DN_NT / 32];
 };
@@ -83,7 +82,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       for (int k = 0; k < 2; ++k) bar_init(s32(&S.sfull[i][k]), 1), bar_init(s32(&S.pfull[i][k]), 4);
       bar_init(s32(&S.odone[i]), 1), bar_init(s32(&S.ofull[i]), 1), bar_init(s32(&S.drain[i]), 1);
     }
-    for (int i = 0; i < DN_RING; ++i) bar_init(s32(&S.consts[i]), 1);
+    for (int i = 0; i < DN_RING; ++i) bar_init(s32(&S.consts[i]), 2);
     bar_init(s32(&S.qfull[0]), 4), bar_init(s32(&S.qfull[1]), 4);
     S.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -147,9 +146,11 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 TMEM lanes a warp
     const uint32_t oc = tmem + lanes + 256 + half * 128;
+    const uint32_t wb = base + C::Q + half * C::OP + (warp & 3) * 32 * 128;  // the warp's query rows
     const int r = tid;  // row of the item
     int item = item0, tt = first0;
     float M = kNone, l = 0.0f, qc = 0.0f;
+    float kt = 0.0f, F = 0.0f, invF = 1.0f;  // of the tile
     bool fresh = true;
     int g = 0;  // items
     for (int u = 0; u < 2 * tiles; ++u) {
@@ -167,11 +168,13 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           const int y = row - cum[b], i = y / G;
           off = b * P.qs0 + i * P.qs1 + (item / nj * G + y - i * G) * P.qs2;
         }
-        // the warp's 32 rows together: neighbouring lanes, neighbouring chunks
+        // into shared memory by the warp's 32 rows together, neighbouring lanes
+        // neighbouring chunks; then a row by its own thread
         constexpr int CH = D / 8;
         uint4 v[CH];
-        if constexpr (E4M3) S.qmax[r] = 0;
-        __syncwarp();
+        auto at = [&](int y, int c) {
+          return wb + (c >> 3) * (DN_TILE * 128) + y * 128 + (((c ^ y) & 7) << 4);
+        };
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
           const int x = lane + 32 * k, y = x / CH;
@@ -187,50 +190,50 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
             }
           }
         }
-        qc = P.c;
-        if constexpr (E4M3) {
-          // bring each row's largest finite magnitude to [2^10, 2^11): exact in
-          // float16 for all elements above 2^-28 of it
-#pragma unroll
-          for (int k = 0; k < CH; ++k) {
-            uint32_t m = 0;
-            auto most = [&](uint32_t u) {
-              const uint32_t a = u & 0x7fffu, b = u >> 16 & 0x7fffu;
-              m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
-            };
-            most(v[k].x), most(v[k].y), most(v[k].z), most(v[k].w);
-            atomicMax(&S.qmax[warp * 32 + (lane + 32 * k) / CH], m);
-          }
-          __syncwarp();
-          const int eq = max(static_cast<int>(S.qmax[r] >> 7) - 127 - 10, -100);
-          qc = P.c * pow2i(eq);
-#pragma unroll
-          for (int k = 0; k < CH; ++k) {
-            const float f = pow2i(-__shfl_sync(~0u, eq, (lane + 32 * k) / CH));
-            auto two = [&](uint32_t u) {
-              return pack<true>(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
-            };
-            v[k] = make_uint4(two(v[k].x), two(v[k].y), two(v[k].z), two(v[k].w));
-          }
-        }
-        const uint32_t qb = base + C::Q + half * C::OP + (warp & 3) * 32 * 128;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-          const int x = lane + 32 * k, y = x / CH, c = x - y * CH;
-          sts128(qb + (c >> 3) * (DN_TILE * 128) + y * 128 + (((c ^ y) & 7) << 4), v[k]);
+          const int x = lane + 32 * k, y = x / CH;
+          sts128(at(y, x - y * CH), v[k]);
+        }
+        qc = P.c;
+        if constexpr (E4M3) {
+          // bring the row's largest finite magnitude to [2^10, 2^11): exact in
+          // float16 for all elements above 2^-28 of it
+          __syncwarp();
+          uint32_t m = 0;
+          auto most = [&](uint32_t u) {
+            const uint32_t a = u & 0x7fffu, b = u >> 16 & 0x7fffu;
+            m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+          };
+#pragma unroll
+          for (int k = 0; k < CH; ++k) {
+            v[k] = lds128(at(lane, k));
+            most(v[k].x), most(v[k].y), most(v[k].z), most(v[k].w);
+          }
+          const int eq = max(static_cast<int>(m >> 7) - 127 - 10, -100);
+          qc = P.c * pow2i(eq);
+          const float f = pow2i(-eq);
+          auto two = [&](uint32_t u) {
+            return pack<true>(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
+          };
+#pragma unroll
+          for (int k = 0; k < CH; ++k)
+            sts128(at(lane, k), make_uint4(two(v[k].x), two(v[k].y), two(v[k].z), two(v[k].w)));
         }
         fence_async();
         __syncwarp();
         if (lane == 0) bar_arrive(s32(&S.qfull[half]));
         M = kNone, l = 0.0f;
       }
-      float kt = qc, F = 0.0f, invF = 1.0f;
-      if constexpr (E4M3) {
-        bar_wait(s32(&S.consts[t % DN_RING]), t / DN_RING & 1, dead);
-        const int2 x = S.exps[t % DN_RING];
-        kt = qc * pow2i(x.x);
-        F = static_cast<float>(x.y);
-        invF = pow2i(-x.y);
+      if (!(u & 1)) {
+        kt = qc;
+        if constexpr (E4M3) {
+          bar_wait(s32(&S.consts[t % DN_RING]), t / DN_RING & 1, dead);
+          const int fe = S.exps[1][t % DN_RING];
+          kt = qc * pow2i(S.exps[0][t % DN_RING]);
+          F = static_cast<float>(fe);
+          invF = pow2i(-fe);
+        }
       }
       const uint32_t sc = tmem + lanes + half * 128 + (u & 1) * 64;
       bar_wait(s32(&S.sfull[half][u & 1]), t & 1, dead);
@@ -245,12 +248,10 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         for (int c = 0; c < 64; ++c)
           if (c >= n) s[c] = -INFINITY;
       }
-      float m4[4] = {s[0], s[1], s[2], s[3]};
+      float m2[2] = {s[0], s[1]};
 #pragma unroll
-      for (int c = 4; c < 64; c += 4)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], s[c + i]);
-      const float m = fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), kt, F);
+      for (int c = 2; c < 62; c += 4) m2[0] = max3(m2[0], s[c], s[c + 1]), m2[1] = max3(m2[1], s[c + 2], s[c + 3]);
+      const float m = fmaf(max3(fmaxf(m2[0], m2[1]), s[62], s[63]), kt, F);
       if (__any_sync(~0u, fresh || m > M + SLACK)) {
         const float nm = fmaxf(M, m), f = ex2(M - nm);
         M = nm;
@@ -299,18 +300,30 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         if (there) P.pl[at] = l == 0.0f ? -INFINITY : M - BIAS + log2f(l);
         bar_wait(s32(&S.ofull[half]), g++ & 1, dead);
         tc_after();
-        float *dst = P.po + at * D;
+        // rows leave through the shared memory of the item's queries, 16 columns
+        // at a time in two buffers, so that a store covers whole sectors
+        float *dst = P.po + (at - lane) * D + (lane & 3) * 4;
+        const uint32_t there32 = __ballot_sync(~0u, there);
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
+          const uint32_t buf = wb + (c & 16) * 128;
           float o[16];
           tmem_ld16(oc + c, o);
           tmem_wait_ld(o, 16);
-          if (there) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4 *>(dst + c + i) = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
+          for (int i = 0; i < 4; ++i)
+            sts128(buf + lane * 64 + ((i ^ lane >> 1) & 3) * 16,
+                   make_uint4(__float_as_uint(o[4 * i] * f), __float_as_uint(o[4 * i + 1] * f),
+                              __float_as_uint(o[4 * i + 2] * f), __float_as_uint(o[4 * i + 3] * f)));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int y = 8 * i + (lane >> 2);
+            const uint4 x = lds128(buf + y * 64 + ((lane ^ y >> 1) & 3) * 16);
+            if (there32 >> y & 1) *reinterpret_cast<uint4 *>(dst + y * D + c) = x;
           }
         }
+        __syncwarp();
         tc_before();
       }
       fresh = last;
@@ -318,71 +331,64 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     }
   } else if (warp < 16) {
     regs_to<DN_LOAD, DN_REGS>();
-    // ============================================ queries, keys and values
-    const int p = tid - 256;
+    // ===================================== keys (four warps), values (four)
+    const bool vs = warp >= 12;
+    const int p = tid & DN_FETCH - 1;
+    const uint8_t *src = vs ? w.v : w.k;
+    const int64_t stride = vs ? w.vps : w.kps;
+    const uint32_t dst0 = base + (vs ? C::V : C::K);
+    uint64_t *full = vs ? S.vfull : S.kfull, *empty = vs ? S.vempty : S.kempty;
     const int lg = w.ps_log2, pm = (1 << lg) - 1;
     int item = item0, tt = first0;
     if constexpr (E4M3) {
-      constexpr int CPR = D / 16, ALL = DN_TILE * CPR;      // 16-byte chunks of a row, of a tile
-      constexpr int PASS = (ALL + DN_FETCH - 1) / DN_FETCH;  // chunks per thread
+      constexpr int CPR = D / 16;                     // 16-byte chunks of a row
+      constexpr int PASS = DN_TILE * CPR / DN_FETCH;  // of a tile, per thread
+      static_assert(DN_TILE * CPR % DN_FETCH == 0, "chunks");
       int id[PASS], ide = -1;  // page ids of the tile to be fetched next
       auto pages = [&](int tile) {
         const int t0 = tile * DN_TILE;
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
-          const int x = p + i * DN_FETCH, tok = t0 + x / CPR;
-          id[i] = (ALL % DN_FETCH == 0 || x < ALL) && tok < w.prefix ? ldg_now(w.ptable + (tok >> lg)) : -1;
+          const int tok = t0 + (p + i * DN_FETCH) / CPR;
+          id[i] = tok < w.prefix ? ldg_now(w.ptable + (tok >> lg)) : -1;
         }
         ide = t0 + 4 * lane < w.prefix ? ldg_now(w.ptable + (t0 + 4 * lane >> lg)) : -1;
       };
-      auto fetch = [&](uint4 (&q)[PASS], const uint8_t *src, int64_t stride, int it, int tile) {
+      uint4 q[PASS] = {};
+      uint32_t ex = 0;  // exponents of the lane's four tokens, the first `live` of them there
+      int live = 0;
+      // A chunk without a page is read from page 0 and put to zero in store(): the
+      // loads stand in a row without branches.
+      auto fetch = [&](int it, int tile) {
+        if (w.n_pages == 0) return;
         const uint32_t row0 = static_cast<uint32_t>(it / nj) << lg;
         const int t0 = tile * DN_TILE;
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
           const int x = p + i * DN_FETCH, row = x / CPR;
-          q[i] = make_uint4(0, 0, 0, 0);
-          if (static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(w.n_pages))
-            q[i] = ldg_now16(src + id[i] * stride + (row0 + (t0 + row & pm)) * D + (x - row * CPR) * 16);
+          const uint32_t pg = static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(w.n_pages) ? id[i] : 0;
+          q[i] = ldg_now16(src + pg * stride + (row0 + (t0 + row & pm)) * D + (x - row * CPR) * 16);
         }
+        // (masked when it is used: nothing here waits for a load)
+        live = static_cast<uint32_t>(ide) < static_cast<uint32_t>(w.n_pages) ? min(max(w.prefix - t0 - 4 * lane, 0), 4) : 0;
+        ex = ldg_now32((vs ? w.ve : w.ke) + ((static_cast<int64_t>(live ? ide : 0) * w.Hkv + it / nj) << lg) +
+                       (t0 + 4 * lane & pm));
       };
-      // exponents of the lane's four tokens; -128 where there is none
-      auto exps = [&](const int8_t *src, int it, int tile) {
-        const int tok = tile * DN_TILE + 4 * lane, n = w.prefix - tok;
-        uint32_t v = 0x80808080u;
-        if (static_cast<uint32_t>(ide) < static_cast<uint32_t>(w.n_pages)) {
-          v = ldg_now32(src + ((static_cast<int64_t>(ide) * w.Hkv + it / nj) << lg) + (tok & pm));
-          if (n < 4) {
-            const uint32_t in = (1u << 8 * n) - 1;
-            v = (v & in) | (0x80808080u & ~in);
-          }
-        }
-        return v;
-      };
-      auto top = [&](uint32_t v) {  // seven below the tile's largest
-        int m = -128;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, static_cast<int>(static_cast<int8_t>(v >> 8 * i)));
-        return max(__reduce_max_sync(~0u, m), kExpMin) - 7;
-      };
-      auto store = [&](uint32_t dst, const uint4 (&q)[PASS], uint32_t v, int E) {
+      auto store = [&](uint32_t dst, int E) {
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
           const int x = p + i * DN_FETCH, row = x / CPR, f = 2 * (x - row * CPR);
-          const uint32_t word = __shfl_sync(~0u, v, row >> 2);
-          if (ALL % DN_FETCH && x >= ALL) break;
-          const int d = static_cast<int8_t>(word >> 8 * (row & 3)) - E;  // <= 7
-          const float one = pow2i(max(d, -126));
-          const uint32_t two = pack<true>(one, one);
+          const int e = static_cast<int8_t>(__shfl_sync(~0u, ex, row >> 2) >> 8 * (row & 3));
+          const float one = pow2i(max(e - E, -126));  // e - E <= 7
+          const uint32_t two = pack<true>(one, one), is = e == -128 ? 0u : ~0u;
           const __half2 sc = *reinterpret_cast<const __half2 *>(&two);
           auto scaled = [&](uint32_t h) {
             const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), sc);
             return *reinterpret_cast<const uint32_t *>(&y);
           };
-          const uint4 lo4 = make_uint4(scaled(cvt_lo(q[i].x)), scaled(cvt_hi(q[i].x)), scaled(cvt_lo(q[i].y)),
-                                       scaled(cvt_hi(q[i].y)));
-          const uint4 hi4 = make_uint4(scaled(cvt_lo(q[i].z)), scaled(cvt_hi(q[i].z)), scaled(cvt_lo(q[i].w)),
-                                       scaled(cvt_hi(q[i].w)));
+          const uint4 b = make_uint4(q[i].x & is, q[i].y & is, q[i].z & is, q[i].w & is);
+          const uint4 lo4 = make_uint4(scaled(cvt_lo(b.x)), scaled(cvt_hi(b.x)), scaled(cvt_lo(b.y)), scaled(cvt_hi(b.y)));
+          const uint4 hi4 = make_uint4(scaled(cvt_lo(b.z)), scaled(cvt_hi(b.z)), scaled(cvt_lo(b.w)), scaled(cvt_hi(b.w)));
           const uint32_t to = dst + (f >> 3) * (DN_TILE * 128) + row * 128;
           const uint32_t c0 = ((f ^ row) & 7) << 4, c1 = ((f + 1 ^ row) & 7) << 4;
           const bool swap = f & 8;  // lanes of one row: all eight chunk positions at once
@@ -390,52 +396,38 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           sts128(to + (swap ? c0 : c1), swap ? lo4 : hi4);
         }
       };
-      auto next = [&](int &it, int &tile) {
-        if (++tile == nt) tile = 0, ++it;
-      };
-      // the loads of a tile's keys are issued when the keys before are stored, and
-      // so the values': a tile ahead
-      uint4 k[PASS], v[PASS];
-      uint32_t ek = 0, ev = 0;
-      if (tiles > 0) {
-        pages(tt);
-        fetch(k, w.k, w.kps, item, tt);
-        ek = exps(w.ke, item, tt);
-        fetch(v, w.v, w.vps, item, tt);
-        ev = exps(w.ve, item, tt);
-      }
+      // the loads of a tile are issued when the tile before is stored
+      if (tiles > 0) pages(tt), fetch(item, tt);
       for (int t = 0; t < tiles; ++t) {
-        const int st = t & 1, E = top(ek), F = top(ev);
-        next(item, tt);
+        if (live < 4) {  // -128 where there is no token
+          const uint32_t in = (1u << 8 * live) - 1;
+          ex = (ex & in) | (0x80808080u & ~in);
+        }
+        int E = -128;  // seven below the tile's largest exponent
+#pragma unroll
+        for (int i = 0; i < 4; ++i) E = max(E, static_cast<int>(static_cast<int8_t>(ex >> 8 * i)));
+        E = max(__reduce_max_sync(~0u, E), kExpMin) - 7;
+        if (p == 0) {
+          S.exps[vs][t % DN_RING] = E;
+          bar_arrive(s32(&S.consts[t % DN_RING]));
+        }
+        if (++tt == nt) tt = 0, ++item;
         if (t + 1 < tiles) pages(tt);
-        if (t >= 2) bar_wait(s32(&S.kempty[st]), (t >> 1) - 1 & 1, dead);
-        store(base + C::K + st * C::OP, k, ek, E);
-        if (p == 0) S.exps[t % DN_RING] = make_int2(E, F);
+        if (t >= 2) bar_wait(s32(empty + (t & 1)), (t >> 1) - 1 & 1, dead);
+        store(dst0 + (t & 1) * C::OP, E);
         fence_async();
         __syncwarp();
-        if (lane == 0) bar_arrive(s32(&S.kfull[st]));
-        if (p == 0) bar_arrive(s32(&S.consts[t % DN_RING]));
-        if (t + 1 < tiles) {
-          fetch(k, w.k, w.kps, item, tt);
-          ek = exps(w.ke, item, tt);
-        }
-        if (t >= 2) bar_wait(s32(&S.vempty[st]), (t >> 1) - 1 & 1, dead);
-        store(base + C::V + st * C::OP, v, ev, F);
-        fence_async();
-        __syncwarp();
-        if (lane == 0) bar_arrive(s32(&S.vfull[st]));
-        if (t + 1 < tiles) {
-          fetch(v, w.v, w.vps, item, tt);
-          ev = exps(w.ve, item, tt);
-        }
+        if (lane == 0) bar_arrive(s32(full + (t & 1)));
+        if (t + 1 < tiles) fetch(item, tt);
       }
     } else {
       constexpr int CPR = D / 8;
-      auto copy = [&](uint32_t dst, const uint8_t *src, int64_t stride, int it, int tile, uint64_t *bar) {
-        const uint32_t row0 = static_cast<uint32_t>(it / nj) << lg;
+      for (int t = 0; t < tiles; ++t) {
+        if (t >= 2) bar_wait(s32(empty + (t & 1)), (t >> 1) - 1 & 1, dead);
+        const uint32_t row0 = static_cast<uint32_t>(item / nj) << lg, dst = dst0 + (t & 1) * C::OP;
 #pragma unroll
-        for (int i = 0; i < CPR / 2; ++i) {
-          const int x = p + i * DN_FETCH, row = x / CPR, f = x - row * CPR, tok = tile * DN_TILE + row;
+        for (int i = 0; i < CPR; ++i) {
+          const int x = p + i * DN_FETCH, row = x / CPR, f = x - row * CPR, tok = tt * DN_TILE + row;
           const int id = tok < w.prefix ? __ldg(w.ptable + (tok >> lg)) : -1;
           const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages);
           const uint32_t at = ((row0 + (tok & pm)) * D + f * 8) * 2;
@@ -443,14 +435,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
                ok ? src + id * stride + at : src, ok);
         }
         // arrives when this thread's copies are in
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s32(bar)) : "memory");
-      };
-      for (int t = 0; t < tiles; ++t) {
-        const int st = t & 1;
-        if (t >= 2) bar_wait(s32(&S.kempty[st]), (t >> 1) - 1 & 1, dead);
-        copy(base + C::K + st * C::OP, w.k, w.kps, item, tt, &S.kfull[st]);
-        if (t >= 2) bar_wait(s32(&S.vempty[st]), (t >> 1) - 1 & 1, dead);
-        copy(base + C::V + st * C::OP, w.v, w.vps, item, tt, &S.vfull[st]);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s32(full + (t & 1))) : "memory");
         if (++tt == nt) tt = 0, ++item;
       }
       cp_wait<0>();
@@ -459,7 +444,12 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     regs_to<DN_REST, DN_REGS>();
     // =========================================================== products
     if (warp < 18) {
-    const int half = warp - 16;
+    // one lane issues, chosen by elect.sync, and all that its products are
+    // described by is the warp's: kept in uniform registers, where they are wanted
+    const int half = __shfl_sync(~0u, warp, 0) - 16;
+    const uint32_t base = __shfl_sync(~0u, s32(sm), 0), tmem = __shfl_sync(~0u, S.tmem, 0);
+    const int tiles = __shfl_sync(~0u, static_cast<int>(hi - lo), 0);
+    const int nt = __shfl_sync(~0u, (w.prefix + DN_TILE - 1) / DN_TILE, 0);
     constexpr uint32_t sdesc = mma_desc(E4M3, 128, 64, false, false);
     constexpr uint32_t odesc = mma_desc(E4M3, 128, D, false, true);
     const uint64_t qd = smem_desc(base + C::Q + half * C::OP, 16, 1024), kd = smem_desc(base + C::K, 16, 1024);
@@ -476,7 +466,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       if (!(u & 1)) bar_wait(s32(&S.kfull[st]), t >> 1 & 1, dead);
       if (!E4M3) fence_async();  // the copies' writes, before the products' reads
       tc_after();
-      if (lane == 0 && !*dead) {
+      if (elected() && !*dead) {
         const uint64_t kk = kd + st * (C::OP >> 4) + (u & 1) * (64 * 128 >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -498,7 +488,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       if (!E4M3) fence_async();
       bar_wait(s32(&S.pfull[half][u & 1]), t & 1, dead);
       tc_after();
-      if (lane == 0 && !*dead) {
+      if (elected() && !*dead) {
         const uint64_t vv = vd + st * (C::OP >> 4) + (u & 1) * (64 * 128 >> 4);
         const bool fresh = !(u & 1) && (t == 0 || tt == 0);
 #pragma unroll
@@ -510,7 +500,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       }
       __syncwarp();
     };
-    int tt = first0;
+    int tt = __shfl_sync(~0u, first0, 0);
     for (int t = 0; t < tiles; ++t) {
       // the next half tile's scores before these weights, except behind an item's
       // last, whose output has to be out before the next item's queries are in
@@ -522,7 +512,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       values(2 * t + 1, tt);
       if (++tt == nt) tt = 0;
     }
-    if (lane == 0) drained(half);
+    if (elected()) drained(half);
     __syncwarp();
     }
   }

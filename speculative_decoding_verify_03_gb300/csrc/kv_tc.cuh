@@ -93,6 +93,12 @@ __device__ __forceinline__ void tmem_wait_st() {
 }
 
 // --------------------------------------------------------------- products
+// True in one lane of the warp, always the same one.
+__device__ __forceinline__ bool elected() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
 // Shared-memory operand descriptor, 128-byte swizzle.  lead: bytes between
 // 64-element chunks of an operand whose rows (not k) are contiguous; step:
 // bytes between groups of 8 rows (k contiguous) or of 8 k (rows contiguous).
@@ -148,6 +154,16 @@ __device__ __forceinline__ uint4 ldg_now16(const void *p) {
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // Two single-precision operations at once.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
