@@ -213,19 +213,20 @@ def test_read_errors_give_nan(sv):
 
 
 # ------------------------------------------------------------------- attend
-def check_attend(got, ref, fmt, gammas):
+def check_attend(got, ref, fmt, gammas, least=0.0):
     """out: one rounding to bfloat16 (8 bits: 2^-8 of the result), one of each
     weight (2^-8 of sum w|v| in bfloat16, 2^-11 in float16), and single
     precision: scores summed in at most 32 steps of 2^-23 of
     size = max scale sum|q k| (2^-18 of it), which move a weight and the sum
     by as much each, and 2^-18 for exponentials, sums and the merge.  lse: the
-    scores' error and 2^-20 for the exponential and the logarithm."""
+    scores' error and 2^-20 for the exponential and the logarithm.  least: what
+    weights in float16's subnormal range are off by in all, where that shows."""
     out, lse = (x.float().cpu().numpy().astype(np.float64) for x in got[:2])
     want, wl, weight, size = ref
     for b, g in enumerate(gammas):
         assert (out[b, g + 1:] == 0).all() and np.isneginf(lse[b, g + 1:]).all()
         o, w, a, z = out[b, : g + 1], want[b, : g + 1], weight[b, : g + 1], size[b, : g + 1, :, None]
-        tol = 2.0 ** -8 * np.abs(w) + a * ((2.0 ** -8 if fmt == "bf16" else 2.0 ** -11) + 2.0 ** -17 * z + 2.0 ** -18)
+        tol = least + 2.0 ** -8 * np.abs(w) + a * ((2.0 ** -8 if fmt == "bf16" else 2.0 ** -11) + 2.0 ** -17 * z + 2.0 ** -18)
         assert (np.abs(o - w) <= tol * 1.01).all(), (b, (np.abs(o - w) / tol).max())
         z = z[..., 0]
         assert (np.abs(lse[b, : g + 1] - wl[b, : g + 1]) <= 2.0 ** -18 * z + 2.0 ** -20 * (1 + np.abs(wl[b, : g + 1]))).all()
@@ -546,3 +547,151 @@ def test_append_then_attend_follows_the_step(sv):
                             pt, 9, np.full(B, N - 1), S, D ** -0.5)
         check_attend(got, ref, "bf16", np.full(B, N - 1))
         lens = lens + np.array([1, 3, 2])  # accepted drafts and the new token
+
+
+# ------------------------------------------- prefixes with many query rows
+MANY = [  # B, N, Hq, Hkv, D, S, prefix: more than 64 query rows of a key/value head
+    (13, 5, 2, 2, 128, 16, 1),       # 65 rows, one token
+    (9, 9, 4, 4, 64, 64, 128),       # 81 rows, a tile's end
+    (22, 3, 8, 2, 80, 16, 129),      # 264 rows: more than a row tile; one token past a tile
+    (16, 4, 16, 4, 96, 32, 63),      # 256 rows, half a tile less one token
+    (30, 9, 4, 2, 128, 128, 700),    # 540 rows
+    (70, 1, 6, 3, 64, 16, 2000),     # single tokens
+]
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("case", MANY, ids=[f"B{c[0]}N{c[1]}q{c[2]}k{c[3]}D{c[4]}S{c[5]}p{c[6]}" for c in MANY])
+def test_attend_shared_prefix(sv, fmt, case, ragged):
+    B, N, Hq, Hkv, D, S, prefix = case
+    rng = np.random.default_rng(31)
+    gam = rng.integers(0, N, B) if ragged else None
+    got, ref, g = attend_case(sv, 32, fmt, B, N, Hq, Hkv, D, S, prefix, rng.integers(0, 20, B), gammas=gam)
+    check_attend(got, ref, fmt, g)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("q_scale", [0.0, 1e-30, 40.0, 1e6])
+def test_attend_shared_prefix_query_sizes(sv, fmt, q_scale):
+    """Weights far below a row's largest: float16 has steps of 2^-24 there, the
+    largest weight is 2^11 or more, so each is off by up to 2^-36 of it, times
+    the largest value (448 * 2^-7), for 300 tokens of the prefix."""
+    got, ref, g = attend_case(sv, 33, fmt, 20, 4, 4, 1, 64, 16, 300, np.arange(20), q_scale=q_scale)
+    check_attend(got, ref, fmt, g, least=300 * 2.0 ** -36 * 3.5 if fmt == "e4m3" else 0.0)
+
+
+def many(sv, fmt, prefix=333, B=24, **kw):
+    return build_batch(sv, fmt, prefix=prefix, lens=tuple(np.arange(B) % 7), **kw)  # 24 * 4 * 4 rows a head
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+def test_attend_shared_prefix_garbage_past_the_end(sv, fmt):
+    """NaN and infinities behind the prefix in its last page, exponents included."""
+    s = many(sv, fmt, prefix=333, S=64)
+    want = reference(s)
+    for sl in range(333 % 64, 64):
+        for w in "kv":
+            for h in range(2):
+                put(s, w, s["pt"][-1], h, sl, slice(None), 0x7F if fmt == "e4m3" else 0x7F80 if sl % 2 else 0x7FC1)
+                if fmt == "e4m3":
+                    getattr(s["cache"], w + "_exp")[s["pt"][-1], h, sl] = -128 if sl % 2 else 127
+    check_attend(call(sv, s), want, fmt, np.full(24, 3))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("p", [0, 200, 332])
+def test_attend_shared_prefix_nan(sv, fmt, which, p):
+    """A NaN of the prefix reaches its own head's queries, a value's only its element."""
+    s = many(sv, fmt)
+    want = reference(s)
+    put(s, which, s["pt"][p // 16], 1, p % 16, 5, 0x7F if fmt == "e4m3" else 0x7FC0)
+    out, lse, st = (x.float().cpu().numpy() for x in call(sv, s))
+    hit = np.zeros(out.shape, bool)
+    hit[:, :, 4:, 5 if which == "v" else slice(None)] = True
+    assert np.isnan(out[hit]).all() and np.isfinite(out[~hit]).all() and (st == 0).all()
+    assert np.isnan(lse[:, :, 4:]).all() == (which == "k") and np.isfinite(lse[:, :, :4]).all()
+    assert np.abs(out - want[0])[~hit].max() < 0.05 * (1 + np.abs(want[0]).max())
+
+
+def test_attend_shared_prefix_exponents(sv):
+    """Tokens whose entries differ in size by up to 2^18, and entries of zeros."""
+    s = many(sv, "e4m3", prefix=500, D=128)
+    rng = np.random.default_rng(34)
+    for w in "kv":
+        e = getattr(s["cache"], w + "_exp")
+        new = rng.integers(-24, -5, e.shape).astype(np.int8)
+        zero = rng.random(e.shape) < 0.1
+        new[zero] = -100
+        s[w][zero] = 0
+        s[w + "e"][...] = new
+        e.copy_(__import__("torch").from_numpy(new))
+        pages = getattr(s["cache"], w + "_pages")
+        pages.view(__import__("torch").uint8).copy_(__import__("torch").from_numpy(s[w]))
+    check_attend(call(sv, s), reference(s), "e4m3", np.full(24, 3))
+
+
+def test_attend_shared_prefix_errors(sv):
+    """Rows in error among many, and a bad page of the prefix."""
+    import torch
+    s = many(sv, "e4m3")
+    want = reference(s)
+    s["table"][3, 0] = -1
+    s["lens"][7] = s["prefix"] - 1
+    got = call(sv, s)
+    st = got[2].cpu().numpy()
+    bad = [3, 7]
+    good = [b for b in range(24) if b not in bad]
+    assert list(st[bad]) == [sv.ROW_BAD_PAGE, sv.ROW_BAD_LENGTH] and (st[good] == 0).all()
+    assert torch.isnan(got[0][bad]).all() and torch.isnan(got[1][bad]).all()
+    check_attend([x[good] for x in got[:2]], [x[good] for x in want], "e4m3", np.full(22, 3))
+    s["pt"][2] = s["cache"].n_pages
+    got = call(sv, s)
+    assert torch.isnan(got[0]).all() and (got[2].cpu().numpy()[good] == sv.ROW_BAD_PAGE).all()
+
+
+@pytest.mark.parametrize("off", [0, 1, 8])
+def test_attend_shared_prefix_query_strides(sv, off):
+    import torch
+    s = many(sv, "bf16", D=80)
+    q = bf16(s["q"])
+    B, N, H, D = q.shape
+    raw = torch.full((B, H, N, D + 16), float("nan"), dtype=torch.bfloat16, device="cuda")
+    view = raw[..., off:off + D].transpose(1, 2)
+    view.copy_(q)
+    args = (s["cache"], i32(s["table"]), i32(s["lens"]))
+    kw = dict(prefix_table=i32(s["pt"]), prefix_len=s["prefix"])
+    a, b = sv.spec_attend(view, *args, **kw), sv.spec_attend(q, *args, **kw)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_attend_workspace_is_reusable(sv):
+    """One workspace, not cleared, for calls of other shapes in turn: the same bits."""
+    import torch
+    runs = [many(sv, "e4m3"), build_batch(sv, "e4m3"), many(sv, "e4m3", prefix=40, D=128)]
+    want = [call(sv, s) for s in runs]
+    ws = torch.full((1 << 28,), 0xFF, dtype=torch.uint8, device="cuda")
+    for k in (0, 1, 2, 1, 0):
+        got = call(sv, runs[k], workspace=ws)
+        assert all(torch.equal(x, y) for x, y in zip(got, want[k]))
+
+
+def test_append_and_read_on_another_stream(sv):
+    """Ordered on the stream that is given: what is read is what was appended there."""
+    import torch
+    rng = np.random.default_rng(35)
+    H, D, S = 4, 128, 16
+    cache = sv.KVCache.empty(40, H, S, D)
+    x, y = (torch.from_numpy(rng.standard_normal((2, 300, H, D)).astype(np.float32)).cuda() for _ in range(2))
+    table, zero, n = i32(np.arange(40).reshape(2, 20)), i32([0, 0]), i32([300, 300])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    sv.spec_kv_append(cache, x, y, table, zero, stream=side)
+    k, v = sv.spec_kv_read(cache, table, n, 300, stream=side)
+    side.synchronize()
+    # half a step of e4m3: 2^-4 of an element, below its least normal 2^-10 2^e; 224 2^e is less than the largest
+    for a, b in ((k, x), (v, y)):
+        a, b = a.float().cpu().numpy(), b.cpu().numpy()
+        most = np.abs(b).max(-1, keepdims=True)
+        assert (np.abs(a - b) <= np.abs(b) * 2.0 ** -4 + most * 2.0 ** -10 / 224).all()
