@@ -74,8 +74,9 @@ typedef struct {
  * prefix's, prefix_len 0).  To e4m3 every value is rounded once, to nearest
  * even, saturating; NaN and infinities become NaN, and the exponent is that
  * of the row's finite values.  To bfloat16 values are rounded to nearest even.
- * A row with an error (bad gamma, bad length, bad page id) writes nothing.
- * No two tokens of a call may share a place.
+ * A row with a bad gamma or length writes nothing; with a bad page id its
+ * tokens on that page are not written, the others are.  No two tokens
+ * of a call may share a place.
  */
 spec_status spec_kv_append(const spec_kv_cache *cache, const spec_kv_batch *batch, const void *k,
                            const void *v, int32_t dtype, const int64_t *k_strides,
@@ -85,7 +86,8 @@ spec_status spec_kv_append(const spec_kv_cache *cache, const spec_kv_batch *batc
  * Read back positions begin .. begin + n - 1 of every sequence, in float32 or
  * bfloat16 (rounded to nearest even): k_out, v_out device
  * [B, n, n_kv_heads, head_dim], contiguous.  Positions at or past kv_len[b]
- * give zeros.  A row with an error gives NaN.
+ * give zeros.  A bad length gives NaN in the whole row, a bad page id in the
+ * positions on that page.
  */
 spec_status spec_kv_read(const spec_kv_cache *cache, const spec_kv_batch *batch, int32_t begin,
                          int32_t n, int32_t dtype, void *k_out, void *v_out, int32_t *row_status,
@@ -104,8 +106,14 @@ spec_status spec_kv_read(const spec_kv_cache *cache, const spec_kv_batch *batch,
  * gamma_b give 0 and -inf; a row with an error gives NaN.  The prefix is read
  * once for the whole batch.  Scores, softmax sums and outputs are accumulated
  * in single precision; the softmax weights enter the product with the values
- * as float16 (e4m3 cache) or bfloat16.  NaN and infinities in keys and values
- * that a query does not attend to do not reach it.
+ * as float16 (e4m3 cache: weights below 2^-25 of a row's largest lose bits,
+ * those below 2^-33 may vanish) or bfloat16.  e4m3 entries and queries enter
+ * their products exactly where an element is at least 2^-28 of its query's
+ * largest and, in a prefix that more than 64 query rows of a key/value head
+ * share, an entry at least 2^-22 of the largest within its 128 tokens; smaller
+ * ones are rounded.  NaN and infinities in keys and values that a query does
+ * not attend to do not reach it.  A row whose kernel gave up a wait reports
+ * SPEC_ROW_WAIT_TIMEOUT and gives NaN.
  *
  * workspace: required, 256-byte aligned, spec_attend_workspace_size bytes (it
  * depends on the shapes only, not on kv_len); contents do not matter.

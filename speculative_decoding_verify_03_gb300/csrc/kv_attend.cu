@@ -6,7 +6,9 @@
 //   out = sum_s 2^(lse2_s - m) o_s / sum_s 2^(lse2_s - m),
 //   lse = ln 2 (m + log2 sum_s 2^(lse2_s - m)),  m = max_s lse2_s,
 // in the order of the slots (reproducible).  The partial results were written
-// just before and are read from L2.
+// just before and are read from L2.  Measured: 256 x 9 x 32
+// rows of 128, two results and more each, 56 us (the bytes alone from HBM: 14 us):
+// the chain from a row's slots to its loads.
 #include "kv_span.h"
 
 namespace {

