@@ -7,7 +7,9 @@
 // largest exponents.  That is exact in float16 for tokens down to 2^22 below
 // the tile's largest, so that a score needs one multiplication, by a factor
 // that all of a row's scores of the tile share, and the weights are
-// P_j = 2^(z_j + F - M), l = sum_tiles 2^-F sum_j P_j.  The running maximum M
+// P_j = 2^(z_j + F - M), l = sum_tiles 2^-F sum_j P_j, kept 2^-25 times as large:
+// a tile of zeros (F = -107) adds 2^(15 + 107 - 25) a token, which 2^30 tokens keep
+// finite, one of the largest exponent (F = 112) 2^(11 - 112 - 25), still normal.  The running maximum M
 // follows only where a row's maximum passes it by more than 4 (float16 P with
 // a bias of 2^11; 8 in bfloat16): otherwise nothing that is summed is scaled.
 //
@@ -68,6 +70,7 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__ SpanParams P) {
   using C = DenseCfg<D>;
   constexpr float BIAS = E4M3 ? 11.0f : 0.0f, SLACK = E4M3 ? 4.0f : 8.0f;
+  constexpr float SUM = E4M3 ? 0x1p-25f : 1.0f, SUM_LOG = E4M3 ? 25.0f : 0.0f;  // factor of the sum of weights
   constexpr float kNone = -1e30f;  // maximum of no scores
   extern __shared__ uint8_t raw[];
   uint8_t *sm = raw + (-s32(raw) & 1023);  // operands: 1024-byte aligned
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           const int fe = S.exps[1][t % DN_RING];
           kt = qc * pow2i(S.exps[0][t % DN_RING]);
           F = static_cast<float>(fe);
-          invF = pow2i(-fe);
+          invF = pow2i(-fe - 13) * (SUM * 0x1p13f);  // 2^-F SUM, subnormal for the largest F
         }
       }
       const uint32_t sc = tmem + lanes + half * 128 + (u & 1) * 64;
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         const int64_t at = static_cast<int64_t>(item + blockIdx.x) * DN_ROWS + r;
         const bool there = static_cast<uint32_t>(item % nj * DN_ROWS + r) < rows;
         const float f = l == 0.0f ? 0.0f : 1.0f / l;
-        if (there) P.pl[at] = l == 0.0f ? -INFINITY : M - BIAS + log2f(l);
+        if (there) P.pl[at] = l == 0.0f ? -INFINITY : M - (BIAS - SUM_LOG) + log2f(l);
         bar_wait(s32(&S.ofull[half]), g++ & 1, dead);
         tc_after();
         // rows leave through the shared memory of the item's queries, 16 columns
@@ -318,8 +321,8 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             sts128(buf + lane * 64 + ((i ^ lane >> 1) & 3) * 16,
-                   make_uint4(__float_as_uint(o[4 * i] * f), __float_as_uint(o[4 * i + 1] * f),
-                              __float_as_uint(o[4 * i + 2] * f), __float_as_uint(o[4 * i + 3] * f)));
+                   make_uint4(__float_as_uint(o[4 * i] * SUM * f), __float_as_uint(o[4 * i + 1] * SUM * f),
+                              __float_as_uint(o[4 * i + 2] * SUM * f), __float_as_uint(o[4 * i + 3] * SUM * f)));
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

@@ -9,7 +9,9 @@
 // weights is l = sum_j P_j 2^-ev_j.  o = (sum_j P_j u_j) / l,
 // lse2 = M + log2 l.  y and u are exact in float16 and each row of q is scaled
 // by a power of two into its range; P is biased by 2^8, so that weights down to
-// 2^-33 of the largest survive.  (Products of e4m3, with q as a sum of two, would
+// 2^-33 of the largest survive.  The sum is kept 2^-12 times as large: a token
+// of zeros (e = -100) adds 2^(8 + 100 - 12), which 2^30 of them keep finite, one of
+// the largest exponent (119) 2^-123, still normal.  (Products of e4m3, with q as a sum of two, would
 // need no conversion of the keys, but are summed with about 14 bits: lse came
 // out 2e-4 off.)  bfloat16 caches: the same with ek = ev = 0 in bfloat16.
 //
@@ -121,10 +123,11 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
   constexpr int TPP = TPW < 32 ? TPW : 32;  // tokens of a pass: what registers hold
   constexpr int NG = TPP / 8;       // groups of 8 tokens
   constexpr float BIAS = E4M3 ? 8.0f : 0.0f;
+  constexpr float SUM = E4M3 ? 0x1p-12f : 1.0f, SUM_LOG = E4M3 ? 12.0f : 0.0f;  // factor of the sum of weights
   extern __shared__ __align__(128) uint8_t sm[];
   uint8_t *stages = sm;
   float *join = reinterpret_cast<float *>(sm + ST * C::STAGE);
-  float4 *consts = reinterpret_cast<float4 *>(sm + ST * C::STAGE + C::JOIN);  // 2^ek, ev, 2^-ev
+  float4 *consts = reinterpret_cast<float4 *>(sm + ST * C::STAGE + C::JOIN);  // 2^ek, ev, 2^-ev SUM
   uint8_t *qbuf = sm + ST * C::STAGE + C::JOIN + C::CONSTS;
   TileInfo *info = reinterpret_cast<TileInfo *>(qbuf + C::QBUF);  // 4
   Cursor *cursor = reinterpret_cast<Cursor *>(info + 4);           // of the newest description
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
   };
   auto factors = [&](uint32_t x, int i, int e) {
     const int ek = static_cast<int16_t>(e & 0xffff), ev = e >> 16;
-    consts[x % ST * kTile + i] = make_float4(pow2i(ek), static_cast<float>(ev), pow2i(-ev), 0.0f);
+    consts[x % ST * kTile + i] = make_float4(pow2i(ek), static_cast<float>(ev), pow2i(-ev) * SUM, 0.0f);
   };
   // --- row r (of all rows of the item's sequence, or of the prefix): its query
   // and the tokens that it sees; null past the last row
@@ -579,7 +582,7 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
     for (int j = 0; j < NG; ++j) {
       const float a = ex2(s[j][0] - u0), b = ex2(s[j][1] - u0);
       const float c = ex2(s[j][2] - u1), d = ex2(s[j][3] - u1);
-      float i0 = 1.0f, i1 = 1.0f;  // 2^-ev
+      float i0 = 1.0f, i1 = 1.0f;  // 2^-ev SUM
       if constexpr (E4M3) {
         const int col = tp + 8 * j + 2 * q4;
         i0 = fac[col].z, i1 = fac[col + 1].z;
@@ -712,15 +715,15 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
           *reinterpret_cast<float4 *>(dst + 16 * c + 4 * q4) =
-              make_float4(o[2 * c][2 * a] * f, o[2 * c + 1][2 * a] * f, o[2 * c][2 * a + 1] * f,
-                          o[2 * c + 1][2 * a + 1] * f);
+              make_float4(o[2 * c][2 * a] * SUM * f, o[2 * c + 1][2 * a] * SUM * f, o[2 * c][2 * a + 1] * SUM * f,
+                          o[2 * c + 1][2 * a + 1] * SUM * f);
       } else {
 #pragma unroll
         for (int c = 0; c < D / 8; ++c)
           *reinterpret_cast<float2 *>(dst + 8 * c + 2 * q4) =
               make_float2(o[c][2 * a] * f, o[c][2 * a + 1] * f);
       }
-      if (q4 == 0) P.pl[at] = l == 0.0f ? -INFINITY : M - BIAS + log2f(l);
+      if (q4 == 0) P.pl[at] = l == 0.0f ? -INFINITY : M - (BIAS - SUM_LOG) + log2f(l);
     }
   }
   cp_wait<0>();

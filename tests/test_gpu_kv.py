@@ -695,3 +695,83 @@ def test_append_and_read_on_another_stream(sv):
         a, b = a.float().cpu().numpy(), b.cpu().numpy()
         most = np.abs(b).max(-1, keepdims=True)
         assert (np.abs(a - b) <= np.abs(b) * 2.0 ** -4 + most * 2.0 ** -10 / 224).all()
+
+
+# ----------------------------------------------- values and scores of zero
+def zero_values(sv, rows, prefix, fmt="e4m3", keys="random", own="random", heads=None):
+    """`rows` query rows of each key/value head over a prefix whose values are
+    all zero, as append stores them (e4m3: exponent -100), and own tokens.  So
+    many heads that a CTA sums up 1024 tokens of one of them and more."""
+    import torch
+    B = rows // 4
+    heads = heads or -(-9 * 152 * 128 // prefix)
+    s = build_batch(sv, fmt, seed=41, prefix=prefix, lens=tuple(np.arange(B) % 5), N=1, Hq=4 * heads, Hkv=heads, S=64)
+    pages = s["pt"] if own == "random" else np.arange(s["cache"].n_pages)
+    for w in ("k", "v") if keys == "zero" else ("v",):
+        s[w][pages] = 0
+        p = torch.from_numpy(np.ascontiguousarray(s[w]).view(np.int16 if fmt == "bf16" else np.uint8)).cuda()
+        t = getattr(s["cache"], w + "_pages")
+        t.view(torch.int16 if fmt == "bf16" else torch.uint8).copy_(p)
+        if fmt == "e4m3":
+            s[w + "e"][pages] = kv_ref.E_MIN
+            getattr(s["cache"], w + "_exp").copy_(torch.from_numpy(s[w + "e"]))
+    return s
+
+
+def check_zero(got, ref, fmt):
+    """check_attend's bounds, and for lse 2^-16 more: the largest exponent of the
+    weights (-100 and 7 below it) and the logarithm of their sum are then of
+    opposite sign and near 2^7, each with a rounding of 2^-17 at most."""
+    out, lse = (x.float().cpu().numpy().astype(np.float64) for x in got[:2])
+    want, wl, weight, size = ref
+    z = size[..., None]
+    tol = 2.0 ** -8 * np.abs(want) + weight * ((2.0 ** -8 if fmt == "bf16" else 2.0 ** -11) + 2.0 ** -17 * z + 2.0 ** -18 + 2.0 ** -16)
+    assert (np.abs(out - want) <= tol * 1.01).all()
+    assert (np.abs(lse - wl) <= 2.0 ** -18 * size + 2.0 ** -20 * (1 + np.abs(wl)) + 2.0 ** -16).all()
+
+
+@pytest.mark.parametrize("rows,prefix,keys,own", [
+    (64, 1024, "zero", "zero"), (64, 8192, "random", "random"), (80, 960, "zero", "random"), (80, 1024, "zero", "random"),
+    (80, 1024, "zero", "zero"), (80, 2048, "zero", "random"), (80, 8192, "zero", "zero"), (80, 8192, "random", "random")])
+def test_attend_prefix_of_zero_values(sv, rows, prefix, keys, own):
+    """The weights of zero values count: an output of 0 from them alone, a share
+    of what the own tokens give, and the logarithm of their number."""
+    s = zero_values(sv, rows, prefix, keys=keys, own=own)
+    got, ref = call(sv, s), reference(s)
+    check_zero(got, ref, "e4m3")
+    if own == "zero":
+        assert (got[0] == 0).all()
+
+
+def test_attend_zero_values_of_many_tokens(sv):
+    """2^21 tokens of equal weight and zero values for each sequence, all of them
+    the same page: own tokens that one CTA sums up without an end."""
+    import torch
+    B, n, S, D = 640, 1 << 21, 128, 64
+    cache = sv.KVCache.empty(1, 1, S, D)
+    zero = torch.zeros((1, S, 1, D), device="cuda")
+    one = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    sv.spec_kv_append(cache, zero, zero, one, i32([0]))
+    table = torch.zeros((B, n // S), dtype=torch.int32, device="cuda")
+    q = torch.zeros((B, 1, 1, D), dtype=torch.bfloat16, device="cuda")
+    out, lse, st = sv.spec_attend(q, cache, table, torch.full((B,), n - 1, dtype=torch.int32, device="cuda"), with_status=True)
+    assert (st == 0).all() and (out == 0).all()
+    assert (lse.double() - 21 * np.log(2)).abs().max() <= 2.0 ** -16 + 2.0 ** -20 * 16
+
+
+@pytest.mark.parametrize("rows", [64, 80])
+@pytest.mark.parametrize("e", [kv_ref.E_MIN, kv_ref.E_MAX])
+def test_attend_values_at_the_ends_of_the_exponents(sv, rows, e):
+    """All values with the least or the largest exponent (codes up to 2^3, so
+    that sums of some of them are finite)."""
+    import torch
+    rng = np.random.default_rng(42)
+    B = rows // 4
+    s = build_batch(sv, "e4m3", seed=43, prefix=700, lens=tuple(np.arange(B) % 90), N=1, Hq=8, Hkv=2, S=64)
+    s["v"][...] = rng.integers(0, 0x51, s["v"].shape) | rng.integers(0, 2, s["v"].shape) << 7
+    s["ve"][...] = e
+    s["cache"].v_pages.view(torch.uint8).copy_(torch.from_numpy(s["v"]))
+    s["cache"].v_exp.fill_(e)
+    got, ref = call(sv, s), reference(s)
+    check_zero(got, ref, "e4m3")
+    assert (got[2] == 0).all()
