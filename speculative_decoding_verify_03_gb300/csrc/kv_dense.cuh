@@ -251,15 +251,16 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       for (int c = 0; c < 64; c += 16) tmem_ld16(sc + c, s + c);
       tmem_wait_ld(s, 64);
       const int n = w.prefix - tt * DN_TILE - (u & 1) * 64;  // tokens from here on
-      if (n < 64) {
+      float ks = kt;  // still to be multiplied by
+      if (n < 64) {   // masked behind the multiplication: a factor of 0 would make NaN of -inf
+        ks = 1.0f;
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (c >= n) s[c] = -INFINITY;
+        for (int c = 0; c < 64; ++c) s[c] = c >= n ? -INFINITY : s[c] * kt;
       }
       float m2[2] = {s[0], s[1]};
 #pragma unroll
       for (int c = 2; c < 62; c += 4) m2[0] = max3(m2[0], s[c], s[c + 1]), m2[1] = max3(m2[1], s[c + 2], s[c + 3]);
-      const float m = fmaf(max3(fmaxf(m2[0], m2[1]), s[62], s[63]), kt, F);
+      const float m = fmaf(max3(fmaxf(m2[0], m2[1]), s[62], s[63]), ks, F);
       if (__any_sync(~0u, fresh || m > M + SLACK)) {
         const float nm = fmaxf(M, m), f = ex2(M - nm);
         M = nm;
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           tmem_wait_st();
         }
       }
-      const float2 k2 = {kt, kt}, b2 = {F - M + BIAS, F - M + BIAS};
+      const float2 k2 = {ks, ks}, b2 = {F - M + BIAS, F - M + BIAS};
       float2 acc[2] = {{0, 0}, {0, 0}};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {

@@ -775,3 +775,27 @@ def test_attend_values_at_the_ends_of_the_exponents(sv, rows, e):
     got, ref = call(sv, s), reference(s)
     check_zero(got, ref, "e4m3")
     assert (got[2] == 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("rows", [64, 80])
+@pytest.mark.parametrize("prefix", [100, 128, 192])
+@pytest.mark.parametrize("what", ["scale", "zeros"])
+def test_attend_no_scores(sv, fmt, rows, prefix, what):
+    """scale = 0, and zero queries on zero keys: every token weighs the same, and
+    what lies behind the prefix's end still weighs nothing."""
+    import torch
+    B = rows // 4
+    s = build_batch(sv, fmt, seed=44, prefix=prefix, lens=tuple(np.arange(B) % 9), N=1, Hq=8, Hkv=2, S=32)
+    if what == "zeros":
+        s["q"][...] = 0
+        s["k"][...] = 0
+        s["cache"].k_pages.view(torch.uint8).zero_()
+        if fmt == "e4m3":
+            s["ke"][...] = kv_ref.E_MIN
+            s["cache"].k_exp.fill_(kv_ref.E_MIN)
+    scale = 0.0 if what == "scale" else s["D"] ** -0.5
+    got = call(sv, s, scale=scale)
+    ref = kv_ref.attend(kv_ref.bf16_value(s["q"]), kv_ref.cache_value(s["k"], s["ke"]), kv_ref.cache_value(s["v"], s["ve"]),
+                        s["table"], s["lens"], s["pt"], prefix, np.zeros(B, int), s["S"], scale)
+    check_attend(got, ref, fmt, np.zeros(B, int))
