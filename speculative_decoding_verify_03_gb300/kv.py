@@ -3,7 +3,6 @@ the binding of include/spec_kv.h."""
 from __future__ import annotations
 
 import ctypes
-import threading
 
 import torch
 
@@ -147,11 +146,17 @@ def _check(code):
         check(code)
 
 
-def _stream(stream, device):
-    """Address of the stream to launch on: the given one or the device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return _raw_stream(device.index)
+def _on(stream, device, call, *args):
+    """call(*args) with the stream current, so that what it allocates is the stream's.
+    What it returns may be freed by its caller while the caller's own stream still
+    uses it: the allocator is told."""
+    with torch.cuda.stream(stream):
+        got = call(*args)
+    here = torch.cuda.current_stream(device)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            t.record_stream(here)
+    return got
 
 
 def _status(with_status, B, device):
@@ -169,7 +174,9 @@ def spec_kv_append(cache, k, v, page_table, kv_len, gamma_per_row=None, prefix_l
     bfloat16 (any strides, contiguous head_dim), token t of sequence b to
     position kv_len[b] + t; with gamma_per_row [B] int32, sequence b has
     gamma_b + 1 tokens.  page_table [B, max_pages] int32 holds the sequences'
-    own pages, whose first position is prefix_len.  Updates the cache in
+    own pages, whose first position is prefix_len.  stream: as a call within
+    torch.cuda.stream(stream); what it returns may be used on the caller's
+    stream as well, once that waits for it.  Updates the cache in
     place; returns row_status [B] when with_status, else None."""
     dev = cache.device
     shape, dtype = k.shape, k.dtype
@@ -185,6 +192,8 @@ def spec_kv_append(cache, k, v, page_table, kv_len, gamma_per_row=None, prefix_l
     ks, vs = k.stride(), v.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("the head_dim axis must be contiguous")
+    if stream is not None:
+        return _on(stream, dev, spec_kv_append, cache, k, v, page_table, kv_len, gamma_per_row, prefix_len, with_status)
     b = _batch(cache, page_table, kv_len, n - 1, None, 0, gamma_per_row)
     if prefix_len:
         b.prefix_len = int(prefix_len)
@@ -192,7 +201,7 @@ def spec_kv_append(cache, k, v, page_table, kv_len, gamma_per_row=None, prefix_l
     st = _status(with_status, B, dev)
     code = _lib().spec_kv_append(cache.ref, _byref(b), k.data_ptr(), v.data_ptr(), 0 if dtype is _f32 else 1,
                                  _byref(_Strides(*ks[:3])), _byref(_Strides(*vs[:3])), _ptr(st),
-                                 _stream(stream, dev))
+                                 _raw_stream(dev.index))
     if code:
         _check(code)
     return st
@@ -203,13 +212,18 @@ def spec_kv_read(cache, page_table, kv_len, n, begin=0, prefix_table=None, prefi
     """Read positions begin .. begin + n - 1 of every sequence back (see
     spec_kv_read in include/spec_kv.h): returns (k, v) [B, n, n_kv_heads,
     head_dim] in dtype (bfloat16 by default, or float32), zeros from kv_len[b]
-    on, and row_status [B] when with_status."""
+    on, and row_status [B] when with_status.  stream: as a call within
+    torch.cuda.stream(stream); what it returns may be used on the caller's
+    stream as well, once that waits for it."""
     dev = cache.device
     dtype = dtype or _bf16
     if dtype is not _bf16 and dtype is not _f32:
         raise TypeError("dtype must be bfloat16 or float32")
     if n < 0 or begin < 0:
         raise ValueError("begin and n must not be negative")
+    if stream is not None:
+        return _on(stream, dev, spec_kv_read, cache, page_table, kv_len, n, begin, prefix_table, prefix_len, dtype,
+                   with_status)
     b = _batch(cache, page_table, kv_len, 0, prefix_table, prefix_len, None)
     n, begin = int(n), int(begin)
     shape = (b.B, n, cache.n_kv_heads, cache.head_dim)
@@ -217,31 +231,15 @@ def spec_kv_read(cache, page_table, kv_len, n, begin=0, prefix_table=None, prefi
     v = torch.empty(shape, dtype=dtype, device=dev)
     st = _status(with_status, b.B, dev)
     code = _lib().spec_kv_read(cache.ref, _byref(b), begin, n, 0 if dtype is _f32 else 1, k.data_ptr(), v.data_ptr(),
-                               _ptr(st), _stream(stream, dev))
+                               _ptr(st), _raw_stream(dev.index))
     if code:
         _check(code)
     return (k, v, st) if with_status else (k, v)
 
 
-_ws_lock = threading.Lock()
-_ws = {}
-
-
 def attend_workspace_bytes(cache, batch, n_heads) -> int:
     """Workspace bytes of spec_attend for these shapes (a SpecKvBatch)."""
     return _lib().spec_attend_workspace_size(cache.ref, _byref(batch), n_heads)
-
-
-def _attend_workspace(cache, batch, n_heads, stream_ptr):
-    """A workspace cached per device and stream (calls on one stream run in order)."""
-    need = attend_workspace_bytes(cache, batch, n_heads)
-    key = (cache.device.index, stream_ptr)
-    with _ws_lock:
-        buf = _ws.get(key)
-        if buf is None or buf.numel() < need:
-            buf = torch.empty(max(need, 4096), dtype=torch.uint8, device=cache.device)
-            _ws[key] = buf
-    return buf
 
 
 def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, gamma_per_row=None,
@@ -252,8 +250,12 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     the first prefix_len of them in the shared pages prefix_table, the others
     in the sequence's own pages page_table[b].  The step's keys and values are
     in the cache already.  scale defaults to head_dim ** -0.5.  workspace:
-    "auto" (cached per device and stream) or a uint8 CUDA tensor.  out: a pair
-    of contiguous tensors for the results, or None.  Returns (out [B,
+    "auto" (the call's own, from torch's allocator: calls from several threads
+    and in captured graphs do not share it) or a uint8 CUDA tensor, which no
+    other call may use meanwhile.  out: a pair of contiguous tensors for the
+    results, or None.  stream: as a call within torch.cuda.stream(stream); what
+    it returns may be used on the caller's stream as well, once that waits for
+    it.  Returns (out [B,
     gamma_max + 1, n_heads, head_dim] bfloat16, lse [B, gamma_max + 1, n_heads]
     float32), and row_status [B] when with_status."""
     dev = cache.device
@@ -270,12 +272,14 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     B, N, Hq, D = shape
     if Hq < 1 or Hq % cache.n_kv_heads:
         raise ValueError("n_heads must be a multiple of the cache's n_kv_heads")
+    if stream is not None:
+        return _on(stream, dev, spec_attend, q, cache, page_table, kv_len, prefix_table, prefix_len, gamma_per_row,
+                   scale, workspace, out, with_status)
     b = _batch(cache, page_table, kv_len, N - 1, prefix_table, prefix_len, gamma_per_row)
-    s = _stream(stream, dev)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")
-        workspace = _attend_workspace(cache, b, Hq, s)
+        workspace = torch.empty(attend_workspace_bytes(cache, b, Hq), dtype=torch.uint8, device=dev)
     if out is None:
         o = torch.empty(shape, dtype=_bf16, device=dev)
         lse = torch.empty(shape[:3], dtype=_f32, device=dev)
@@ -287,7 +291,7 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     st = _status(with_status, B, dev)
     code = _lib().spec_attend(cache.ref, _byref(b), q.data_ptr(), Hq, _byref(_Strides(*qs[:3])),
                               D ** -0.5 if scale is None else float(scale), o.data_ptr(), lse.data_ptr(), _ptr(st),
-                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), s)
+                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
     if code:
         _check(code)
     return (o, lse, st) if with_status else (o, lse)

@@ -799,3 +799,71 @@ def test_attend_no_scores(sv, fmt, rows, prefix, what):
     ref = kv_ref.attend(kv_ref.bf16_value(s["q"]), kv_ref.cache_value(s["k"], s["ke"]), kv_ref.cache_value(s["v"], s["ve"]),
                         s["table"], s["lens"], s["pt"], prefix, np.zeros(B, int), s["S"], scale)
     check_attend(got, ref, fmt, np.zeros(B, int))
+
+
+# ------------------------------------------------- streams, graphs and workspaces
+def test_attend_graph_keeps_its_workspace(sv):
+    """A graph captured with the workspace left to the call, replayed behind
+    larger calls on the same stream and with the freed memory in use."""
+    import torch
+    s = build_batch(sv, "e4m3", prefix=64, lens=(20, 63, 5))
+    large = many(sv, "e4m3")
+    q, table, lens, pt = bf16(s["q"]), i32(s["table"]), i32(s["lens"]), i32(s["pt"])
+    kw = dict(prefix_table=pt, prefix_len=64)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        want = sv.spec_attend(q, s["cache"], table, lens, **kw)
+        side.synchronize()
+        with torch.cuda.graph(g, stream=side):
+            out = sv.spec_attend(q, s["cache"], table, lens, **kw)
+        for _ in range(3):
+            call(sv, large)
+            junk = [torch.full((1 << k,), 0x7F, dtype=torch.uint8, device="cuda") for k in range(12, 26)]
+            g.replay()
+            side.synchronize()
+            assert all((j == 0x7F).all() for j in junk)
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_attend_on_a_stream_while_the_callers_allocates(sv):
+    """Calls of growing size on a given stream, the caller's stream filling what
+    it gets from the allocator between them."""
+    import torch
+    runs = [build_batch(sv, "e4m3"), many(sv, "e4m3"), many(sv, "e4m3", prefix=1000, D=128)]
+    args = [((bf16(s["q"]), s["cache"], i32(s["table"]), i32(s["lens"])), dict(prefix_table=i32(s["pt"]), prefix_len=s["prefix"]))
+            for s in runs]
+    want = [sv.spec_attend(*a, **kw) for a, kw in args]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(10):
+        for a, kw in args:
+            got.append(sv.spec_attend(*a, stream=side, **kw))
+            for k in (16, 20, 24, 26):
+                torch.full((1 << k,), 0x7F, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for k, g in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(g, want[k % 3])), k
+
+
+def test_attend_from_threads_on_one_stream(sv):
+    """Calls of several threads whose launches may come between one another's."""
+    import threading
+
+    import torch
+    runs = [build_batch(sv, "e4m3", seed=50 + k, prefix=40 + k) for k in range(4)]
+    want = [call(sv, s) for s in runs]
+    wrong = []
+
+    def work(k):
+        for _ in range(50):
+            got = call(sv, runs[k])
+            if not all(torch.equal(x, y) for x, y in zip(got, want[k])):
+                wrong.append(k)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

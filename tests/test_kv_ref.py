@@ -1,5 +1,6 @@
 """The cache reference against identities, and the binding's and the C ABI's
 refusals, without a GPU."""
+import contextlib
 import ctypes
 
 import numpy as np
@@ -203,3 +204,115 @@ def test_binding_takes_pages_of_one_head():
     """A size of one leaves its stride open: only the order of what is there counts."""
     t = torch.zeros((4, 16, 1, 64), dtype=torch.bfloat16).transpose(1, 2)
     assert sv.KVCache(t, t).n_kv_heads == 1
+
+
+# --------------------------------------- streams, devices and workspaces, on the CPU
+class OnGpu:
+    """A CPU tensor that says it lies on a GPU."""
+
+    def __init__(self, t, device="cuda:0", stream=None):
+        self.t, self.device, self.stream, self.used_on = t, torch.device(device), stream, []
+
+    def record_stream(self, stream):
+        self.used_on.append(stream.cuda_stream)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def __getitem__(self, i):
+        return self.t[i]
+
+
+class FakeGpu:
+    """The library and torch's current stream and device, none of them real: what
+    is allocated and launched is noted with the stream and device of the moment."""
+
+    def __init__(self, monkeypatch):
+        self.device, self.streams, self.made, self.calls, self.hook = 0, {}, [], [], None
+        empty = torch.empty
+
+        def new(*size, dtype=None, device=None):
+            t = OnGpu(empty(*size, dtype=dtype), device, self.streams.get(torch.device(device).index, 0))
+            self.made.append(t)
+            return t
+        monkeypatch.setattr(torch, "empty", new)
+        monkeypatch.setattr(torch.cuda, "stream", self.on_stream)
+        monkeypatch.setattr(torch.cuda, "device", self.on_device)
+        monkeypatch.setattr(torch.cuda, "current_stream",
+                            lambda device=None: Stream(self.streams.get(torch.device(device).index, 0), device))
+        monkeypatch.setattr(kv, "_device", lambda: self.device, raising=False)
+        monkeypatch.setattr(kv, "_raw_stream", lambda index: self.streams.get(index, 0))
+        monkeypatch.setattr(kv, "_library", self)
+
+    @contextlib.contextmanager
+    def on_device(self, device):
+        before, self.device = self.device, torch.device(device).index
+        yield
+        self.device = before
+
+    @contextlib.contextmanager
+    def on_stream(self, stream):
+        with self.on_device(stream.device):
+            before = self.streams.get(self.device, 0)
+            self.streams[self.device] = stream.cuda_stream
+            yield
+            self.streams[self.device] = before
+
+    def _called(self, *args):
+        self.calls.append((self.device, *args))
+        hook, self.hook = self.hook, None
+        if hook:
+            hook()
+        return 0
+
+    spec_kv_append = spec_kv_read = spec_attend = _called
+
+    def spec_attend_workspace_size(self, cache, batch, n_heads):
+        return batch._obj.B << 20
+
+
+class Stream:
+    def __init__(self, address, device="cuda:0"):
+        self.cuda_stream, self.device = address, torch.device(device)
+
+
+def step_on(device="cuda:0", B=2):
+    """Arguments of the three operators, all on one device."""
+    z = lambda *s, dt=torch.bfloat16: OnGpu(torch.zeros(s, dtype=dt), device)  # noqa: E731
+    cache = sv.KVCache(z(3, 2, 16, 64), z(3, 2, 16, 64))
+    t, n = z(B, 4, dt=torch.int32), z(B, dt=torch.int32)
+    return {"append": lambda **kw: sv.spec_kv_append(cache, z(B, 1, 2, 64), z(B, 1, 2, 64), t, n, with_status=True, **kw),
+            "read": lambda **kw: sv.spec_kv_read(cache, t, n, 5, with_status=True, **kw),
+            "attend": lambda **kw: sv.spec_attend(z(B, 1, 4, 64), cache, t, n, with_status=True, **kw)}
+
+
+def test_calls_that_overlap_do_not_share_a_workspace(monkeypatch):
+    """The launches of a call from another thread may come between two of a call's own."""
+    gpu = FakeGpu(monkeypatch)
+    gpu.hook = step_on()["attend"]
+    step_on()["attend"]()
+    outer, inner = (c[-3] for c in gpu.calls)
+    assert outer and inner and outer != inner
+
+
+@pytest.mark.parametrize("op", ["append", "read", "attend"])
+def test_a_given_stream_is_the_one_of_all_tensors(monkeypatch, op):
+    """What a call allocates goes back to the stream that its kernels run on, and
+    what it returns not before the caller's stream is done with it."""
+    gpu = FakeGpu(monkeypatch)
+    got = step_on()[op](stream=Stream(77))
+    assert gpu.calls[0][-1] == 77
+    assert gpu.made and all(t.stream == 77 for t in gpu.made)
+    assert all(t.used_on == [0] for t in (got if isinstance(got, tuple) else (got,)))
+    step_on()[op]()
+    assert gpu.calls[1][-1] == 0 and gpu.made[-1].stream == 0
+
+
+def test_workspaces_do_not_outlive_the_call(monkeypatch):
+    """A workspace is the call's own: within a graph's capture it is the graph's."""
+    gpu = FakeGpu(monkeypatch)
+    for B in (1, 3, 2):
+        step_on(B=B)["attend"]()
+        work = [t for t in gpu.made if t.dtype == torch.uint8]
+        assert [t.numel() for t in work] == [B << 20]
+        gpu.made.clear()
