@@ -17,8 +17,9 @@ def _raw_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
-# torch's own short way to the same address, where it has it (2 us a call less)
+# torch's own short ways to the same address and number, where it has them (2 us a call less)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class SpecKvCache(ctypes.Structure):
@@ -146,10 +147,24 @@ def _check(code):
         check(code)
 
 
+def _elsewhere(stream, device):
+    """Whether a call has to go to another stream or device than the current ones."""
+    return stream is not None or device.type != "cuda" or device.index != _device()
+
+
 def _on(stream, device, call, *args):
-    """call(*args) with the stream current, so that what it allocates is the stream's.
-    What it returns may be freed by its caller while the caller's own stream still
-    uses it: the allocator is told."""
+    """call(*args) with the device and the stream (if given) current: kernels run on
+    the current device, and what the call allocates is to be the stream's.  What it
+    returns may be freed by its caller while the caller's own stream still uses
+    it: the allocator is told."""
+    if device.type != "cuda":
+        from . import SpecError
+        raise SpecError(f"the cache is on {device}: this library has no CPU path")
+    if stream is None:
+        with torch.cuda.device(device):
+            return call(*args)
+    if stream.device != device:
+        raise ValueError(f"the stream must be on {device}")
     with torch.cuda.stream(stream):
         got = call(*args)
     here = torch.cuda.current_stream(device)
@@ -192,9 +207,9 @@ def spec_kv_append(cache, k, v, page_table, kv_len, gamma_per_row=None, prefix_l
     ks, vs = k.stride(), v.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("the head_dim axis must be contiguous")
-    if stream is not None:
-        return _on(stream, dev, spec_kv_append, cache, k, v, page_table, kv_len, gamma_per_row, prefix_len, with_status)
     b = _batch(cache, page_table, kv_len, n - 1, None, 0, gamma_per_row)
+    if _elsewhere(stream, dev):
+        return _on(stream, dev, spec_kv_append, cache, k, v, page_table, kv_len, gamma_per_row, prefix_len, with_status)
     if prefix_len:
         b.prefix_len = int(prefix_len)
         b.prefix_table = b.page_table  # not read: the step is past the prefix
@@ -221,10 +236,10 @@ def spec_kv_read(cache, page_table, kv_len, n, begin=0, prefix_table=None, prefi
         raise TypeError("dtype must be bfloat16 or float32")
     if n < 0 or begin < 0:
         raise ValueError("begin and n must not be negative")
-    if stream is not None:
+    b = _batch(cache, page_table, kv_len, 0, prefix_table, prefix_len, None)
+    if _elsewhere(stream, dev):
         return _on(stream, dev, spec_kv_read, cache, page_table, kv_len, n, begin, prefix_table, prefix_len, dtype,
                    with_status)
-    b = _batch(cache, page_table, kv_len, 0, prefix_table, prefix_len, None)
     n, begin = int(n), int(begin)
     shape = (b.B, n, cache.n_kv_heads, cache.head_dim)
     k = torch.empty(shape, dtype=dtype, device=dev)
@@ -272,10 +287,10 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     B, N, Hq, D = shape
     if Hq < 1 or Hq % cache.n_kv_heads:
         raise ValueError("n_heads must be a multiple of the cache's n_kv_heads")
-    if stream is not None:
+    b = _batch(cache, page_table, kv_len, N - 1, prefix_table, prefix_len, gamma_per_row)
+    if _elsewhere(stream, dev):
         return _on(stream, dev, spec_attend, q, cache, page_table, kv_len, prefix_table, prefix_len, gamma_per_row,
                    scale, workspace, out, with_status)
-    b = _batch(cache, page_table, kv_len, N - 1, prefix_table, prefix_len, gamma_per_row)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")

@@ -316,3 +316,25 @@ def test_workspaces_do_not_outlive_the_call(monkeypatch):
         work = [t for t in gpu.made if t.dtype == torch.uint8]
         assert [t.numel() for t in work] == [B << 20]
         gpu.made.clear()
+
+
+@pytest.mark.parametrize("op", ["append", "read", "attend"])
+def test_the_launch_is_on_the_caches_device(monkeypatch, op):
+    gpu = FakeGpu(monkeypatch)
+    for device, stream in ((1, None), (0, None), (1, Stream(5, "cuda:1"))):
+        gpu.calls.clear()
+        step_on(f"cuda:{device}")[op](stream=stream)
+        assert gpu.calls[0][0] == device and gpu.calls[0][-1] == (stream.cuda_stream if stream else 0)
+        assert gpu.device == 0
+
+
+@pytest.mark.parametrize("op", ["append", "read", "attend"])
+def test_streams_of_other_devices_and_host_tensors_are_refused(monkeypatch, op):
+    gpu = FakeGpu(monkeypatch)
+    with pytest.raises(ValueError):
+        step_on("cuda:1")[op](stream=Stream(5, "cuda:0"))
+    with pytest.raises(sv.SpecError):
+        step_on("cpu")[op]()
+    with pytest.raises(sv.SpecError):
+        step_on("cpu")[op](stream=Stream(5, "cuda:0"))
+    assert not gpu.calls
