@@ -524,8 +524,8 @@ def spec_cascade_verify(levels, draft_tokens, uniforms, temperature, top_k=0, to
     return out_tok, out_len, stage_acc, status
 
 
-_KV = ("KVCache", "ROW_BAD_LENGTH", "ROW_BAD_PAGE", "attend_workspace_bytes", "spec_attend", "spec_kv_append",
-       "spec_kv_read")
+_KV = ("KVCache", "ROW_BAD_LENGTH", "ROW_BAD_PAGE", "SpecKvBatch", "attend_workspace_bytes", "spec_attend",
+       "spec_kv_append", "spec_kv_read")
 
 
 def __getattr__(name):

@@ -253,8 +253,10 @@ def spec_kv_read(cache, page_table, kv_len, n, begin=0, prefix_table=None, prefi
 
 
 def attend_workspace_bytes(cache, batch, n_heads) -> int:
-    """Workspace bytes of spec_attend for these shapes (a SpecKvBatch)."""
-    return _lib().spec_attend_workspace_size(cache.ref, _byref(batch), n_heads)
+    """Workspace bytes of spec_attend for these shapes: of the SpecKvBatch, B,
+    gamma_max, max_pages (the page table's columns) and prefix_len count."""
+    shapes = SpecKvBatch(batch.B, batch.gamma_max, batch.max_pages, batch.prefix_len, batch.max_pages)
+    return _lib().spec_attend_workspace_size(cache.ref, _byref(shapes), n_heads)
 
 
 def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, gamma_per_row=None,
@@ -266,13 +268,13 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     in the sequence's own pages page_table[b].  The step's keys and values are
     in the cache already.  scale defaults to head_dim ** -0.5.  workspace:
     "auto" (the call's own, from torch's allocator: calls from several threads
-    and in captured graphs do not share it) or a uint8 CUDA tensor, which no
-    other call may use meanwhile.  out: a pair of contiguous tensors for the
-    results, or None.  stream: as a call within torch.cuda.stream(stream); what
-    it returns may be used on the caller's stream as well, once that waits for
-    it.  Returns (out [B,
-    gamma_max + 1, n_heads, head_dim] bfloat16, lse [B, gamma_max + 1, n_heads]
-    float32), and row_status [B] when with_status."""
+    and in captured graphs do not share it) or a uint8 CUDA tensor of
+    attend_workspace_bytes, which no other call may use meanwhile.  out: a pair
+    of contiguous tensors for the results, or None.  stream: as a call within
+    torch.cuda.stream(stream); what it returns may be used on the caller's
+    stream as well, once that waits for it.  Returns (out [B, gamma_max + 1,
+    n_heads, head_dim] bfloat16, lse [B, gamma_max + 1, n_heads] float32), and
+    row_status [B] when with_status."""
     dev = cache.device
     shape = q.shape
     if q.dtype is not _bf16:
@@ -294,7 +296,9 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")
-        workspace = torch.empty(attend_workspace_bytes(cache, b, Hq), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_lib().spec_attend_workspace_size(cache.ref, _byref(b), Hq), dtype=torch.uint8, device=dev)
+    elif workspace is None or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be 'auto' or a contiguous tensor on {dev}")
     if out is None:
         o = torch.empty(shape, dtype=_bf16, device=dev)
         lse = torch.empty(shape[:3], dtype=_f32, device=dev)

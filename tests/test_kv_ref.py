@@ -338,3 +338,28 @@ def test_streams_of_other_devices_and_host_tensors_are_refused(monkeypatch, op):
     with pytest.raises(sv.SpecError):
         step_on("cpu")[op](stream=Stream(5, "cuda:0"))
     assert not gpu.calls
+
+
+def test_a_given_workspace_is_checked(monkeypatch):
+    gpu = FakeGpu(monkeypatch)
+    ok = OnGpu(torch.zeros(4096, dtype=torch.uint8))
+    step_on()["attend"](workspace=ok)
+    assert gpu.calls[0][-3:-1] == (ok.data_ptr(), 4096)
+    for bad in (None, torch.zeros(4096, dtype=torch.uint8), OnGpu(torch.zeros(4096, dtype=torch.uint8), "cuda:1"),
+                OnGpu(torch.zeros((64, 128), dtype=torch.uint8)[:, ::2])):
+        with pytest.raises(ValueError):
+            step_on()["attend"](workspace=bad)
+    assert len(gpu.calls) == 1
+
+
+def test_workspace_bytes_by_shapes():
+    """What a caller that keeps a workspace needs: the package's names alone."""
+    sv.build()
+    t = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
+    cache = sv.KVCache(t, t)
+    size = lambda **kw: sv.attend_workspace_bytes(cache, sv.SpecKvBatch(**kw), 16)  # noqa: E731
+    want = dict(B=3, gamma_max=4, max_pages=7, prefix_len=100)
+    made = kv._batch(cache, torch.zeros((3, 7), dtype=torch.int32), torch.zeros(3, dtype=torch.int32), 4,
+                     torch.zeros(7, dtype=torch.int32), 100, None)
+    assert size(**want) == sv.attend_workspace_bytes(cache, made, 16) > 0
+    assert size(**dict(want, B=300)) > size(**want)
