@@ -105,9 +105,14 @@ spec_status spec_kv_read(const spec_kv_cache *cache, const spec_kv_batch *batch,
  * device float32 [B, gamma_max+1, n_heads]; both contiguous.  Queries past
  * gamma_b give 0 and -inf; a row with an error gives NaN.  The prefix is read
  * once for the whole batch.  Scores, softmax sums and outputs are accumulated
- * in single precision; the softmax weights enter the product with the values
- * as float16 (e4m3 cache: weights below 2^-25 of a row's largest lose bits,
- * those below 2^-33 may vanish) or bfloat16.  e4m3 entries and queries enter
+ * in single precision.  The softmax weights enter the product with the values
+ * in 16 bits, as the values do: over a bfloat16 cache as bfloat16 (2^-8 of
+ * each), over an e4m3 cache as float16 and times 2^e, e the exponent of the
+ * token's values (in a prefix that more than 64 query rows of a key/value head
+ * share, the largest one of its 128 tokens).  Such a product loses bits below
+ * 2^-22 of the row's largest (in such a prefix 2^-25) and may vanish below
+ * 2^-33 (2^-36), also for an element that is 0 in the token of the largest;
+ * below 2^-134 the weight may be missing from lse.  e4m3 entries and queries enter
  * their products exactly where an element is at least 2^-28 of its query's
  * largest and, in a prefix that more than 64 query rows of a key/value head
  * share, an entry at least 2^-22 of the largest within its 128 tokens; smaller

@@ -867,3 +867,43 @@ def test_attend_from_threads_on_one_stream(sv):
     for t in threads:
         t.join()
     assert not wrong
+
+
+@pytest.mark.parametrize("rows", [0, 64, 80])
+@pytest.mark.parametrize("far", [10, 25, 30, 60])
+def test_attend_value_exponents_far_apart(sv, rows, far):
+    """One token whose values are 2^far times as large as the others', but for an
+    element of 0, all tokens of equal weight w.  Over an e4m3 cache a weight
+    times 2^e is a float16 number (e the token's exponent), the row's largest
+    at 2^8 or above and its last place 2^-24: off by 2^-33 of the largest at
+    most, beside 2^-11 of itself.  From 65 rows on e is the tile's largest, the
+    row's largest at 2^11 or above (2^-36), and a value u 2^e is a float16
+    number times 2^(e - 7) (2^-32 of 2^e at most).  rows = 0: own tokens only."""
+    import torch
+    B = max(rows, 8) // 4
+    prefix = 300 if rows else 0
+    s = build_batch(sv, "e4m3", seed=45, prefix=prefix, lens=(150,) * B, N=1, Hq=8, Hkv=2, S=64)
+    s["q"][...] = 0
+    pg, sl = (s["pt"][2], 5) if rows else (s["table"][1, 1], 5)
+    s["ve"][pg, :, sl] = -8 + far
+    s["v"][pg, :, sl, 7] = 0
+    s["cache"].v_exp.copy_(torch.from_numpy(s["ve"]))
+    s["cache"].v_pages.view(torch.uint8).copy_(torch.from_numpy(s["v"]))
+    out, lse, st = (x.float().cpu().numpy().astype(np.float64) for x in call(sv, s))
+    want, wl, weight, _ = reference(s)
+    assert (st == 0).all() and (np.abs(lse - wl) <= 2.0 ** -20 * (1 + np.abs(wl))).all()
+    n = prefix + 151
+    val = kv_ref.cache_value(s["v"], s["ve"])
+    for b in range(B):
+        tok = kv_ref.tokens_of(val, s["table"], s["pt"], prefix, 64, b, n)
+        e = kv_ref.tokens_of(s["ve"][..., None].astype(np.float64), s["table"], s["pt"], prefix, 64, b, n)[..., 0]
+        off, rough = 2.0 ** -33, np.zeros((n, 2))  # the own tokens' bound, which covers a prefix's too
+        if rows > 64:
+            for t in range(0, prefix, 128):
+                e[t:min(t + 128, prefix)] = e[t:min(t + 128, prefix)].max(0)
+            rough[:prefix] = 2.0 ** (e[:prefix] - 32)
+        for h in range(8):
+            u = np.abs(tok[:, h // 4]) * 2.0 ** -e[:, h // 4, None]
+            tol = off * (2.0 ** e[:, h // 4].max() / n) * u.sum(0) + rough[:, h // 4].mean()
+            tol = tol + 2.0 ** -8 * np.abs(want[b, 0, h]) + weight[b, 0, h] * (2.0 ** -11 + 2.0 ** -18)
+            assert (np.abs(out[b, 0, h] - want[b, 0, h]) <= tol * 1.01).all(), (b, h)
