@@ -174,7 +174,7 @@ bool lay_out(const View &w, int D, int G, Layout &L) {
   if (io > INT32_MAX / 2 || ip > INT32_MAX / 2 || L.tiles_o > INT32_MAX || L.tiles_p > INT32_MAX)
     return false;
   const size_t so = static_cast<size_t>(io + kMaxGrid) * 16 * L.wo;
-  const size_t sp = ip ? static_cast<size_t>(ip + kMaxGrid) * L.rp : 0;
+  const size_t sp = ip ? static_cast<size_t>(ip + (L.dense ? kMaxDense : kMaxGrid)) * L.rp : 0;
   L.plan = 0;
   L.po = up(sizeof(uint32_t) * (3 * (w.B + 1) + kMaxGrid));
   L.pl = up(L.po + so * D * 4);

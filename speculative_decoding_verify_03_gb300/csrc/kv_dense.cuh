@@ -542,7 +542,7 @@ cudaError_t dense_go(const SpanParams &p, int64_t tiles, int *grid, cudaStream_t
   constexpr int smem = fixed + 4 * (kMaxB + 1);
   const cudaError_t e = slots.get(reinterpret_cast<const void *>(f), DN_NT, smem, smem, &sms, &occ);
   if (e != cudaSuccess) return e;
-  int64_t n = sms < kMaxGrid ? sms : kMaxGrid;
+  int64_t n = sms < kMaxDense ? sms : kMaxDense;
   if (n > tiles) n = tiles;
   if (n < 1) n = 1;
   *grid = static_cast<int>(n);

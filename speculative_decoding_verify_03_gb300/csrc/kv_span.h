@@ -81,6 +81,8 @@ cudaError_t span_bf16_128(const SpanParams &, int, int64_t, int *, cudaStream_t)
 
 // The dense kernel: prefix items of DN_ROWS rows, tiles of 128 tokens.
 constexpr int DN_ROWS = 256;
+constexpr int kMaxDense = 152;  // CTAs of the dense kernel at most: one on each multiprocessor
+static_assert(kMaxDense <= kMaxGrid, "plan");
 cudaError_t dense_e4m3(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
 cudaError_t dense_bf16(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
 

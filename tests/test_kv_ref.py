@@ -363,3 +363,14 @@ def test_workspace_bytes_by_shapes():
                      torch.zeros(7, dtype=torch.int32), 100, None)
     assert size(**want) == sv.attend_workspace_bytes(cache, made, 16) > 0
     assert size(**dict(want, B=300)) > size(**want)
+
+
+def test_workspace_of_a_shared_prefix(L):
+    """Its partial results are those of one CTA per multiprocessor (152) and one
+    more for each item of 256 query rows: outputs and a logarithm in float32."""
+    cache = _cache(head_dim=128, k_page_stride=8 * 16 * 128, v_page_stride=8 * 16 * 128)
+    size = lambda **kw: L.spec_attend_workspace_size(ctypes.byref(cache), ctypes.byref(_batch(**kw)), 32)  # noqa: E731
+    for B in (17, 64, 300):  # 4 * 4 query rows of each of 8 heads for a sequence
+        items = -(-B * 16 // 256) * 8
+        more = size(B=B, prefix_len=1000) - size(B=B)
+        assert 0 < more <= (items + 152) * 256 * (128 + 1) * 4 + 1024
