@@ -436,7 +436,7 @@ def sample_leg(args, w, sv, torch, dev):
     ms = a.elapsed_time(b_)
     peak, kind = measured_peak()
     achieved = n * V * es / (ms / K * 1e-3) / 1e9
-    # the kernel the library selects with its cached workspace (a row is a
+    # the kernel the library selects with a workspace (a row is a
     # sequence with no drafts)
     filt = 0 < w.top_k < V or w.top_p < 1
     if V <= 1024 and (T == 0 or not filt):

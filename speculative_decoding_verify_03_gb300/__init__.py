@@ -215,23 +215,16 @@ def make_params(target, draft, temperature, top_k=0, top_p=1.0, gamma_per_row=No
         cluster_size=int(cluster_size), list_capacity=int(list_capacity))
 
 
-_ws_lock = threading.Lock()
-_ws_cache = {}
-
-
 def auto_workspace(params: SpecParams, device, stream=None):
-    """A workspace of the size the call needs, cached per device and stream
-    (calls on one stream run in order, so they may share it)."""
+    """A workspace of the size the call needs, from torch's allocator, which
+    orders its reuse by the stream (the given or the current one) and keeps a
+    captured graph's for the graph."""
     torch = _torch()
-    need = int(lib().spec_verify_workspace_size(ctypes.byref(params)))
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    key = (torch.device(device).index, s.cuda_stream)
-    with _ws_lock:
-        buf = _ws_cache.get(key)
-        if buf is None or buf.numel() < need:
-            buf = torch.zeros(max(need, 4096), dtype=torch.uint8, device=device)
-            _ws_cache[key] = buf
-    return buf
+    need = max(int(lib().spec_verify_workspace_size(ctypes.byref(params))), 4096)
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def spec_verify(target, draft, draft_tokens, uniforms, temperature, top_k=0, top_p=1.0,
@@ -242,7 +235,7 @@ def spec_verify(target, draft, draft_tokens, uniforms, temperature, top_k=0, top
     target [B, G+1, V] and draft [B, G, V] (float32 or bfloat16, CUDA, any
     row / position strides, contiguous vocabulary axis); draft_tokens [B, G]
     int32; uniforms [B, G+1, 2] float32; gamma_per_row [B] int32 or None.
-    workspace: "auto" (a cached buffer of the size the call needs, which
+    workspace: "auto" (a buffer of the size the call needs, which
     enables the strip-parallel kernel for greedy and top-k problems), a
     uint8 CUDA tensor, or None (no workspace: the cluster-per-row kernel).
     Vocabularies of at most 1024 with greedy or unfiltered sampling run on
@@ -342,7 +335,7 @@ def spec_sample(logits, u, temperature, top_k=0, top_p=1.0, cluster_size=0, list
                 stream=None, with_status=False, workspace="auto"):
     """One draw per row of logits [n, V] (CUDA, float32/bfloat16) with
     uniforms u [n] float32: the filtered tempered law's inverse CDF.
-    workspace: "auto" (a cached buffer of the size the call can use: the
+    workspace: "auto" (a buffer of the size the call can use: the
     strip-parallel or CTA-per-row kernels), a uint8 CUDA tensor, or None
     (the warp-per-row or cluster kernels)."""
     torch = _torch()
