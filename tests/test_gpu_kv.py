@@ -907,3 +907,12 @@ def test_attend_value_exponents_far_apart(sv, rows, far):
             tol = off * (2.0 ** e[:, h // 4].max() / n) * u.sum(0) + rough[:, h // 4].mean()
             tol = tol + 2.0 ** -8 * np.abs(want[b, 0, h]) + weight[b, 0, h] * (2.0 ** -11 + 2.0 ** -18)
             assert (np.abs(out[b, 0, h] - want[b, 0, h]) <= tol * 1.01).all(), (b, h)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("case", [(1, 500, 4, 2, 64, 16, 0, [0]), (2, 300, 2, 1, 128, 64, 70, [0, 130]),
+                                  (2, 260, 3, 1, 80, 32, 500, [1, 0])], ids=["begin", "behind", "many"])
+def test_attend_prompt(sv, fmt, case):
+    """A prompt in one call: hundreds of query tokens, each with one more to see."""
+    got, ref, g = attend_case(sv, 46, fmt, *case)
+    check_attend(got, ref, fmt, g)
