@@ -8,7 +8,8 @@
 
 namespace kv {
 
-constexpr uint32_t kPolls = 1u << 22;  // polls of a wait before it gives up
+// Polls of a wait before it gives up: a poll that fails takes 2912 clocks, so 1.5 s.
+constexpr uint32_t kPolls = 1u << 20;
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
