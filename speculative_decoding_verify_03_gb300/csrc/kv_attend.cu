@@ -8,7 +8,8 @@
 // in the order of the slots (reproducible).  The partial results were written
 // just before and are read from L2.  Measured: 256 x 9 x 32
 // rows of 128, two results and more each, 56 us (the bytes alone from HBM: 14 us):
-// the chain from a row's slots to its loads.
+// the chain from a row's slots to its loads; every CTA also checks all page ids
+// of its sequence.
 #include "kv_span.h"
 
 namespace {
@@ -143,9 +144,16 @@ int row_warps(int64_t rows) {
 
 // Query rows (of a key/value head) from which the prefix goes to the dense kernel:
 // from the 65th on the span kernel reads the keys again.  Measured, 8 heads of 128
-// in e4m3, whole calls, span and dense: prefix 4096, 64 rows 48.7 and 36.0 us, 128
-// rows 42.4 and 35.9, 320 rows 50.3 and 45.7; prefix 500, 23.3 and 26.4, 23.8 and
-// 26.9, 28.6 and 30.4: a few tiles do not fill its 256 rows' start and end.
+// in e4m3, replayed calls, span / dense kernel in us:
+//   prefix   16 rows      64 rows      80 rows      320 rows
+//      500   20.5 / 25.6  23.5 / 26.4  23.6 / 26.6  34.0 / 35.9
+//     1000   24.1 / 27.0  27.0 / 28.0  27.7 / 28.0  40.8 / 37.8
+//     2000   30.9 / 30.7  34.8 / 32.0  36.8 / 32.0  46.1 / 41.2
+//     4096   43.3 / 34.7  49.0 / 36.2  43.3 / 36.5  56.0 / 50.6
+//     8192   45.1 / 40.0  52.6 / 42.5  50.0 / 42.0  74.0 / 62.6
+// Heads of 64 and bfloat16 caches cross over between 500 and 2000 tokens too.  So the
+// prefix's length says more than the rows do: this rule costs up to 13 us below 65
+// rows and up to 3 us from 65 rows on, where the prefix is short.
 constexpr int64_t kDenseRows = 65;
 
 struct Layout {

@@ -13,9 +13,13 @@
 // reduction of 3 or 4 steps for the maximum, 8-byte stores of e4m3.  Keys and
 // values go through the same thread, so that four independent loads are in
 // flight before the first use.
-// Measured, 8 heads of 128: append 2 x 16384 tokens bfloat16 to e4m3 42.4 us
-// (4.8 TB/s, 70 % of a copy's rate), 512 x 2..9 tokens float32 7.8 us, one token
-// 1.9 us; read 16 x 8192 tokens to bfloat16 144 us (5.6 TB/s, 82 %).
+// Measured (replayed calls), 8 heads of 128: append 2 x 16384 tokens bfloat16 to
+// e4m3 42.4 us (4.8 TB/s, 70 % of a copy's rate), to a bfloat16 cache 42.5 us (6.3
+// TB/s, 93 %): as long for more bytes, so the e4m3 form is not held by them.  512 x
+// 2..9 tokens float32 7.8 us, to bfloat16 6.5 us; it loads all 9 tokens of each
+// sequence, 37.7 MB where 23.1 MB would do, from L2 when replayed.  One token
+// 2.0 us.  Read 16 x 8192 tokens to bfloat16 from e4m3 142 us (5.6 TB/s, 83 %), from
+// bfloat16 162 us (6.6 TB/s, 97 %).
 #include <cuda_fp16.h>
 
 #include <type_traits>

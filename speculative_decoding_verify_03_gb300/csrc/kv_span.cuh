@@ -13,7 +13,11 @@
 // of zeros (e = -100) adds 2^(8 + 100 - 12), which 2^30 of them keep finite, one of
 // the largest exponent (119) 2^-123, still normal.  (Products of e4m3, with q as a sum of two, would
 // need no conversion of the keys, but are summed with about 14 bits: lse came
-// out 2e-4 off.)  bfloat16 caches: the same with ek = ev = 0 in bfloat16.
+// out 2e-4 off.)  bfloat16 caches: the same with ek = ev = 0 in bfloat16: a product
+// has both operands in one 16-bit type, and float16 does not hold all values of
+// the cache, so the weights are rounded to 8 bits there (the error of 16 heads of
+// 64 over 1001 + 0..300 tokens against 64 bits 0.0022, the output's own rounding
+// 0.0017); a second product with what the rounding left would cost as much again.
 //
 // Layout: a CTA has WR x WT warps; a warp works on 16 rows and 64 / WT tokens
 // of each tile with m16n8k16 products, and keeps its own running maximum, sum
@@ -29,10 +33,15 @@
 // of a few tiles).
 //
 // Bound and measured: 8 x 5 queries of 64 heads (40 rows a key/value head of 128)
-// over 40000..65536 e4m3 tokens 339 us, 2.5 TB/s or 37 % of a copy's rate: about
-// 800 cycles of products per 64-token tile and sub-core beside the conversions on
-// the ALU pipe, where the bytes alone would take 707.  512 x 2..9 queries of 16
-// heads of 64 over 0..300 bfloat16 tokens 134 us (2.5 TB/s): what an item costs once.
+// over 40000..65536 e4m3 tokens 340 us, 2.5 TB/s or 37 % of a copy's rate: about
+// 1900 cycles per 64-token tile and SM, where the bytes alone would take 707.
+// No pipe is full (tensor 40 %, ALU 39 %, issue 44 %): three warps a
+// scheduler wait for one another's products, loads and barriers, and each of the
+// three row warps converts the whole tile for itself, about two thirds of the
+// ALU's work.  Over bfloat16 tokens, without conversions, 340 us are 5.0 TB/s (74 %).
+// 512 x 2..9 queries of 16 heads of 64 over 0..300 bfloat16 tokens 134 us (2.5
+// TB/s): what an item costs once.  A prompt of 2048 tokens at position 0, 32 heads:
+// 344 us (100 TFLOP/s of what its queries see; each row tile walks all keys).
 #pragma once
 
 #include <cuda_fp16.h>
