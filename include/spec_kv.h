@@ -40,6 +40,7 @@ typedef enum { SPEC_KV_BF16 = 0, SPEC_KV_E4M3 = 1 } spec_kv_format;
 #define SPEC_ROW_BAD_LENGTH (1 << 7) /* kv_len[b] below prefix_len, or the step's
                                         tokens pass the row's page table */
 #define SPEC_ROW_BAD_PAGE   (1 << 8) /* a page id in use outside [0, n_pages) */
+#define SPEC_ROW_NO_PAGES   (1 << 9) /* the pool has not enough free pages for the row */
 
 typedef struct {
   void *k_pages, *v_pages;
@@ -130,6 +131,106 @@ spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_batch *batch, 
                         int32_t n_heads, const int64_t *q_strides, float scale, void *out,
                         float *lse, int32_t *row_status, void *workspace, size_t workspace_bytes,
                         void *stream);
+
+/*
+ * The attention of a step whose tokens are a tree's nodes (spec_tree.h): as
+ * spec_attend, but query i of sequence b attends to the positions before the
+ * step, 0 .. kv_len[b] - 1, and to those nodes j <= gamma_b of the step
+ * (position kv_len[b] + j) whose bit is set in its mask row.  mask: device int32
+ * [B, gamma_max+1, W], contiguous, W = ceil((gamma_max+1) / 32), bit j & 31 of
+ * word j >> 5: spec_tree_mask's, or any other (a query that sees nothing gives
+ * 0 and -inf).  gamma_max < SPEC_TREE_MAX.  All else is as for spec_attend.
+ */
+size_t spec_attend_tree_workspace_size(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                                       int32_t n_heads);
+
+spec_status spec_attend_tree(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                             const int32_t *mask, const void *q, int32_t n_heads,
+                             const int64_t *q_strides, float scale, void *out, float *lse,
+                             int32_t *row_status, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * Move the entries of an accepted path together: for j = 1 .. accepted_len[b]
+ * the entry at position kv_len[b] + path[b, j] goes to position kv_len[b] + j,
+ * kv_len the lengths before the step.  path: device int32 [B, gamma_max+1],
+ * contiguous, path[b, 0] = 0, increasing (spec_tree_accept's); accepted_len:
+ * device int32 [B].  Entries elsewhere stay as they are.  One call for every
+ * cache (layer) of the model.  gamma_per_row is not read.  A row whose
+ * accepted_len is not in [0, gamma_max] or whose path is not increasing from 0
+ * within the step (SPEC_ROW_BAD_TREE, 1 << 10), or whose positions pass its
+ * table (SPEC_ROW_BAD_LENGTH), moves nothing; an entry on or for a page that
+ * is not there is not moved (SPEC_ROW_BAD_PAGE).
+ */
+spec_status spec_kv_compact(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                            const int32_t *path, const int32_t *accepted_len,
+                            int32_t *row_status, void *stream);
+
+/*
+ * Page tables over a pool of pages.  refs: device int32 [n_pages], how many
+ * table entries hold each page; a page with a count of 0 (or less) is free.
+ * Pages that the tables below do not hold (a shared prefix's, say) have their
+ * counts set by the caller.  table: device int32 [B, max_pages], row stride in
+ * elements, of the sequences' own pages; held: device int32 [B], the entries
+ * of each row in use.  What stands behind them in a row is not read, and is
+ * overwritten as the row grows.  All caches (layers) of a model share one pool,
+ * one table and these calls; page contents are per cache (spec_kv_copy).
+ */
+typedef struct {
+  int32_t B;          /* sequences, 0 .. 4096; 0 => no-op */
+  int32_t max_pages;  /* columns of table (>= 0) */
+  int32_t n_pages;    /* of the pool */
+  int32_t page_size;  /* 16, 32, 64 or 128 */
+  int32_t prefix_len; /* tokens that kv_len counts and the table does not hold */
+  int64_t table_row_stride;
+  int32_t *refs, *table, *held;
+} spec_kv_pool;
+
+/*
+ * Let row b hold kv_len[b] + n_step tokens (prefix included); kv_len[b] = -1:
+ * none.  Pages that are too many are given back (their counts fall by one);
+ * pages that are missing are the free ones of the lowest numbers, of those
+ * that are free once all rows have given back, in the order of the rows and
+ * of the positions.  A row is served if the pool has pages for it and for all
+ * rows before it; else it keeps what it has (SPEC_ROW_NO_PAGES).  A row with
+ * kv_len below -1 or, unless it is -1, with kv_len[b] + n_step < prefix_len, with
+ * more pages than columns, or held outside [0, max_pages] is left as it is
+ * (SPEC_ROW_BAD_LENGTH).  A page id outside [0, n_pages) that is to be given
+ * back is passed over (SPEC_ROW_BAD_PAGE).
+ */
+spec_status spec_kv_resize(const spec_kv_pool *pool, const int32_t *kv_len, int32_t n_step,
+                           int32_t *row_status, void *stream);
+
+/*
+ * Let rows dst[j], j < n, which hold no pages, become forks of rows src[j]: the
+ * pages that are full (kv_len[src[j]] tokens) are shared, their counts rise by
+ * one; of a last page that is not full the fork has its own, the free page of
+ * the lowest number that the forks before it leave, and copies [n, 3] (device
+ * int32) says what to copy to it in every cache: page, new page, tokens
+ * (spec_kv_copy); -1, -1, 0 where there is nothing to copy.  held and kv_len
+ * of dst[j] are set.  A fork whose page the pool does not have
+ * (SPEC_ROW_NO_PAGES) changes nothing, and so does one with a row outside
+ * [0, B), src[j] = dst[j], dst[j] holding pages or named by an earlier fork of
+ * the call (SPEC_ROW_BAD_FORK), or whose source's kv_len does not fit what it
+ * holds (SPEC_ROW_BAD_LENGTH).  A source's page id outside [0, n_pages) is
+ * copied to the fork, not counted, its contents not copied (SPEC_ROW_BAD_PAGE).
+ * fork_status: optional device int32 [n].  n in [0, 4096].
+ */
+#define SPEC_ROW_BAD_FORK (1 << 12)
+
+spec_status spec_kv_fork(const spec_kv_pool *pool, int32_t *kv_len, const int32_t *src,
+                         const int32_t *dst, int32_t n, int32_t *copies, int32_t *fork_status,
+                         void *stream);
+
+/*
+ * Copy entries between pages of a cache: for each of n triples (page, new page,
+ * tokens) of copies (device int32 [n, 3], contiguous) slots 0 .. tokens - 1
+ * (at most page_size) of all heads.  Triples with a page outside [0, n_pages)
+ * or no tokens are passed over.  No page is the target of two triples of a
+ * call, or the source of one and the target of another.  n in [0, 2^20].
+ */
+spec_status spec_kv_copy(const spec_kv_cache *cache, const int32_t *copies, int32_t n,
+                         void *stream);
 
 #ifdef __cplusplus
 }

@@ -23,12 +23,16 @@ _SOURCES = [os.path.join(_HERE, "csrc", f) for f in ("spec_verify.cu", "spec_str
                                                       "kv_span_e4m3_96_128.cu",
                                                       "kv_span_bf16_64_80.cu",
                                                       "kv_span_bf16_96_128.cu", "kv_dense_e4m3.cu",
-                                                      "kv_dense_bf16.cu")]
+                                                      "kv_dense_bf16.cu", "kv_tree_e4m3_64_80.cu",
+                                                      "kv_tree_e4m3_96_128.cu",
+                                                      "kv_tree_bf16_64_80.cu",
+                                                      "kv_tree_bf16_96_128.cu", "kv_pages.cu",
+                                                      "spec_tree.cu", "spec_adjust.cu")]
 _DEPS = _SOURCES + [os.path.join(_HERE, "csrc", f)
                     for f in ("sv_common.cuh", "sv_core.cuh", "sv_strip.h", "sv_row.h",
                               "sv_verify.h", "kv_common.cuh", "kv_span.h", "kv_span.cuh",
                               "kv_dense.cuh", "kv_tc.cuh")] + [
-    os.path.join(_ROOT, "include", h) for h in ("spec_verify.h", "spec_kv.h")]
+    os.path.join(_ROOT, "include", h) for h in ("spec_verify.h", "spec_kv.h", "spec_tree.h")]
 
 SPEC_F32, SPEC_BF16 = 0, 1
 ROW_BAD_TOKEN, ROW_BAD_LOGIT, ROW_NO_FINITE, ROW_Q_ZERO, ROW_BAD_GAMMA, ROW_BAD_UNIFORM = (
@@ -39,7 +43,10 @@ EXPORTS = ("spec_verify", "spec_sample", "spec_verify_workspace_size", "spec_sta
            "spec_read_diagnostics", "spec_verify_noalloc", "spec_commit", "spec_law",
            "spec_cascade_verify", "spec_cascade_workspace_size", "spec_law_ws",
            "spec_law_workspace_size", "spec_sample_ws", "spec_sample_workspace_size",
-           "spec_kv_append", "spec_kv_read", "spec_attend", "spec_attend_workspace_size")
+           "spec_kv_append", "spec_kv_read", "spec_attend", "spec_attend_workspace_size",
+           "spec_attend_tree", "spec_attend_tree_workspace_size", "spec_kv_compact",
+           "spec_kv_resize", "spec_kv_fork", "spec_kv_copy", "spec_tree_mask", "spec_tree_accept",
+           "spec_adjust")
 
 
 class SpecParams(ctypes.Structure):
@@ -165,6 +172,25 @@ def lib():
             L.spec_attend_workspace_size.restype = sz
             L.spec_attend.argtypes = [vp, vp, vp, i32, vp, ctypes.c_float, vp, vp, vp, vp, sz, vp]
             L.spec_attend.restype = ctypes.c_int
+            L.spec_attend_tree_workspace_size.argtypes = [vp, vp, i32]
+            L.spec_attend_tree_workspace_size.restype = sz
+            L.spec_attend_tree.argtypes = [vp, vp, vp, vp, i32, vp, ctypes.c_float, vp, vp, vp, vp, sz, vp]
+            L.spec_attend_tree.restype = ctypes.c_int
+            L.spec_kv_compact.argtypes = [vp, vp, vp, vp, vp, vp]
+            L.spec_kv_compact.restype = ctypes.c_int
+            L.spec_kv_resize.argtypes = [vp, vp, i32, vp, vp]
+            L.spec_kv_resize.restype = ctypes.c_int
+            L.spec_kv_fork.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp]
+            L.spec_kv_fork.restype = ctypes.c_int
+            L.spec_kv_copy.argtypes = [vp, vp, i32, vp]
+            L.spec_kv_copy.restype = ctypes.c_int
+            # trees and logits (tree.py)
+            L.spec_tree_mask.argtypes = [i32, i32, vp, vp, vp, vp, vp, vp]
+            L.spec_tree_mask.restype = ctypes.c_int
+            L.spec_tree_accept.argtypes = [i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+            L.spec_tree_accept.restype = ctypes.c_int
+            L.spec_adjust.argtypes = [vp, vp, vp, vp, vp]
+            L.spec_adjust.restype = ctypes.c_int
             _lib = L
     return _lib
 
@@ -517,15 +543,23 @@ def spec_cascade_verify(levels, draft_tokens, uniforms, temperature, top_k=0, to
     return out_tok, out_len, stage_acc, status
 
 
-_KV = ("KVCache", "ROW_BAD_LENGTH", "ROW_BAD_PAGE", "SpecKvBatch", "attend_workspace_bytes", "spec_attend",
-       "spec_kv_append", "spec_kv_read")
+_KV = ("KVCache", "ROW_BAD_FORK", "ROW_BAD_LENGTH", "ROW_BAD_PAGE", "ROW_NO_PAGES", "SpecKvBatch", "SpecKvPool",
+       "attend_workspace_bytes", "attend_tree_workspace_bytes", "spec_attend", "spec_attend_tree", "spec_kv_append",
+       "spec_kv_compact", "spec_kv_copy", "spec_kv_fork", "spec_kv_read", "spec_kv_resize")
+_TREE = ("ROW_BAD_PENALTY", "ROW_BAD_TREE", "SpecAdjustParams", "TREE_MAX", "spec_adjust", "spec_tree_accept",
+         "spec_tree_mask")
 
 
 def __getattr__(name):
-    """The cache operators' names, from kv.py at their first use (it needs torch)."""
+    """The names of kv.py and tree.py, from there at their first use (they need torch)."""
     if name in _KV:
         from . import kv
         for n in _KV:
             globals()[n] = getattr(kv, n)
+        return globals()[name]
+    if name in _TREE:
+        from . import tree
+        for n in _TREE:
+            globals()[n] = getattr(tree, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,4 +1,4 @@
-// kv_attend.cu -- spec_attend: the plan of the span kernels' launches and the
+// kv_attend.cu -- spec_attend and spec_attend_tree: the plan of the span kernels' launches and the
 // merge of their partial results.
 //
 // Merge: row (b, i, h) has one partial result (o_s, lse2_s) for every CTA that
@@ -11,6 +11,7 @@
 // the chain from a row's slots to its loads; every CTA also checks all page ids
 // of its sequence.
 #include "kv_span.h"
+#include "spec_tree.h"
 
 namespace {
 
@@ -192,16 +193,16 @@ bool lay_out(const View &w, int D, int G, Layout &L) {
   return true;
 }
 
-span_launch_fn span_of(int format, int D) {
+span_launch_fn span_of(int format, int D, bool tree) {
+  if (tree && format == SPEC_KV_E4M3)
+    return D == 64 ? tree_e4m3_64 : D == 80 ? tree_e4m3_80 : D == 96 ? tree_e4m3_96 : tree_e4m3_128;
+  if (tree) return D == 64 ? tree_bf16_64 : D == 80 ? tree_bf16_80 : D == 96 ? tree_bf16_96 : tree_bf16_128;
   if (format == SPEC_KV_E4M3)
     return D == 64 ? span_e4m3_64 : D == 80 ? span_e4m3_80 : D == 96 ? span_e4m3_96 : span_e4m3_128;
   return D == 64 ? span_bf16_64 : D == 80 ? span_bf16_80 : D == 96 ? span_bf16_96 : span_bf16_128;
 }
 
-}  // namespace
-
-extern "C" size_t spec_attend_workspace_size(const spec_kv_cache *cache, const spec_kv_batch *batch,
-                                             int32_t n_heads) {
+size_t workspace_of(const spec_kv_cache *cache, const spec_kv_batch *batch, int32_t n_heads, bool tree) {
   View w;
   Layout L;
   if (!cache || !batch) return 0;
@@ -211,16 +212,18 @@ extern "C" size_t spec_attend_workspace_size(const spec_kv_cache *cache, const s
   c.k_exp = c.v_exp = reinterpret_cast<int8_t *>(256);
   s.page_table = s.prefix_table = s.kv_len = reinterpret_cast<const int32_t *>(256);
   if (make_view(&c, &s, true, w) != SPEC_OK || n_heads < 1 || n_heads % w.Hkv) return 0;
+  if (tree && w.N > SPEC_TREE_MAX) return 0;
   return lay_out(w, c.head_dim, n_heads / w.Hkv, L) ? L.bytes : 0;
 }
 
-extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_batch *batch,
-                                   const void *q, int32_t n_heads, const int64_t *q_strides,
-                                   float scale, void *out, float *lse, int32_t *row_status,
-                                   void *workspace, size_t workspace_bytes, void *stream) {
+// mask: of a tree, or null.
+spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const int32_t *mask, bool tree,
+                   const void *q, int32_t n_heads, const int64_t *q_strides, float scale, void *out,
+                   float *lse, int32_t *row_status, void *workspace, size_t workspace_bytes, void *stream) {
   SpanParams P = {};
   const spec_status st = make_view(cache, batch, true, P.w);
   if (st != SPEC_OK) return st;
+  if (tree && P.w.N > SPEC_TREE_MAX) return SPEC_ERR_UNSUPPORTED;
   if (n_heads < 1 || n_heads % P.w.Hkv || !q_strides || !(scale >= 0.0f) || !(scale < INFINITY))
     return SPEC_ERR_INVALID_ARG;
   for (int i = 0; i < 3; ++i)
@@ -230,6 +233,7 @@ extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_bat
   if (!q || !out || qa % 2 || reinterpret_cast<uintptr_t>(out) % 4 ||
       reinterpret_cast<uintptr_t>(lse) % 4)
     return SPEC_ERR_INVALID_ARG;
+  if (tree && (!mask || reinterpret_cast<uintptr_t>(mask) % 4)) return SPEC_ERR_INVALID_ARG;
   const int G = n_heads / P.w.Hkv, D = cache->head_dim;
   Layout L;
   if (!lay_out(P.w, D, G, L)) return SPEC_ERR_UNSUPPORTED;
@@ -246,7 +250,7 @@ extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_bat
   const uintptr_t qbits = qa | static_cast<uintptr_t>((q_strides[0] | q_strides[1] | q_strides[2]) * 2);
   P.c = scale * 1.4426950408889634f;
   P.G = G;
-  const span_launch_fn span = span_of(cache->format, D);
+  const span_launch_fn span = span_of(cache->format, D, false), own = span_of(cache->format, D, tree);
   MP m = {};
   m.w = P.w;
   m.plan = P.plan;
@@ -266,11 +270,13 @@ extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_bat
     if (e != cudaSuccess) return SPEC_ERR_CUDA;
   }
   P.prefix = 0;
+  P.mask = mask;
+  P.mask_words = (P.w.N + 31) / 32;
   P.qvec = qbits % (L.wo == 1 ? 16 : 4) == 0;
   P.po = reinterpret_cast<float *>(ws + L.po);
   P.pl = reinterpret_cast<float *>(ws + L.pl);
   m.po = P.po, m.pl = P.pl;
-  if (span(P, L.wo, L.tiles_o, &m.co, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (own(P, L.wo, L.tiles_o, &m.co, s) != cudaSuccess) return SPEC_ERR_CUDA;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -284,4 +290,33 @@ extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_bat
   const cudaError_t e = D == 64 ? cudaLaunchKernelEx(&cfg, merge_kernel<16>, m)
                                 : cudaLaunchKernelEx(&cfg, merge_kernel<32>, m);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" size_t spec_attend_workspace_size(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                                             int32_t n_heads) {
+  return workspace_of(cache, batch, n_heads, false);
+}
+
+extern "C" spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                                   const void *q, int32_t n_heads, const int64_t *q_strides,
+                                   float scale, void *out, float *lse, int32_t *row_status,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+  return attend(cache, batch, nullptr, false, q, n_heads, q_strides, scale, out, lse, row_status, workspace,
+                workspace_bytes, stream);
+}
+
+extern "C" size_t spec_attend_tree_workspace_size(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                                                  int32_t n_heads) {
+  return workspace_of(cache, batch, n_heads, true);
+}
+
+extern "C" spec_status spec_attend_tree(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                                        const int32_t *mask, const void *q, int32_t n_heads,
+                                        const int64_t *q_strides, float scale, void *out, float *lse,
+                                        int32_t *row_status, void *workspace, size_t workspace_bytes,
+                                        void *stream) {
+  return attend(cache, batch, mask, true, q, n_heads, q_strides, scale, out, lse, row_status, workspace,
+                workspace_bytes, stream);
 }

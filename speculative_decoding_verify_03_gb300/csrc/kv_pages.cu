@@ -1,0 +1,593 @@
+// kv_pages.cu -- entries and pages of the cache on the move: an accepted path's
+// entries to consecutive positions, page tables over a pool with reference
+// counts (grow, shrink, free, fork), and copies of pages.
+//
+// Compact: a place is never behind the entry that goes to it (path[j] >= j), and
+// never that of a later one, so entries may be moved in increasing order.  A CTA
+// takes a sequence and a head, a thread 16 bytes of an entry; a pass's loads all
+// come before its stores.
+//
+// Tables: one cluster of CTAs does a whole call, so that counts, sums and
+// assignments can wait for one another.  What each row needs is summed over the
+// rows by every CTA for itself; then the counts are read, 32 a thread, and the
+// free pages numbered by sums over the warp, the CTA and the cluster, in the
+// order of the page ids: page of number k goes to the row in whose sum k falls.
+// Nothing depends on the order of atomics: they add to counts, or or bits.
+//
+// Bound: the chain of loads and cluster barriers; copies by memory.
+#include <cooperative_groups.h>
+
+#include <atomic>
+
+#include "kv_common.cuh"
+#include "spec_tree.h"
+
+namespace {
+
+namespace cg = cooperative_groups;
+using kv::View;
+
+// ------------------------------------------------------------------ compact
+constexpr int MV_NT = 256;
+
+struct MP {
+  View w;
+  uint8_t *k, *v;
+  int8_t *ke, *ve;
+  const int32_t *path, *acc;
+  int32_t *status;
+};
+
+template <bool E4M3>
+__global__ void __launch_bounds__(MV_NT) compact_kernel(const __grid_constant__ MP P, int D) {
+  const View &w = P.w;
+  const int b = blockIdx.y, head = blockIdx.x, tid = threadIdx.x;
+  const int a = P.acc[b], len = w.len[b];
+  const int32_t *path = P.path + static_cast<int64_t>(b) * w.N;
+  const int own = len - w.prefix;
+  int st = a < 0 || a >= w.N ? SPEC_ROW_BAD_TREE : 0, bad = 0;
+  if (!st)
+    for (int j = 1 + tid; j <= a; j += MV_NT) {
+      const int at = path[j], before = path[j - 1];
+      bad |= at <= before || at >= w.N || (j == 1 && before != 0);
+    }
+  if (__syncthreads_or(bad)) st = SPEC_ROW_BAD_TREE;
+  if (len < w.prefix) st |= SPEC_ROW_BAD_LENGTH;
+  else if (!st && a > 0 && own + static_cast<int64_t>(path[a]) >= static_cast<int64_t>(w.max_pages) << w.ps_log2)
+    st |= SPEC_ROW_BAD_LENGTH;
+  const bool go = !st && a > 0;  // of the whole CTA
+  const int DB = E4M3 ? D : 2 * D, CPR = DB / 16;
+  const int cols = 2 * CPR + (E4M3 ? 1 : 0);  // 16 bytes of a key or a value; both exponents
+  const int per = MV_NT / cols;               // entries of a pass
+  const int col = tid % cols, sub = tid / cols;
+  const int pm = (1 << w.ps_log2) - 1;
+  const uint32_t np = static_cast<uint32_t>(w.n_pages);
+  const int32_t *ids = w.table + b * w.tstride;
+  int lost = 0;
+  if (go)
+    for (int j0 = 1; j0 <= a; j0 += per) {
+      const int j = j0 + sub;
+      const bool mine = sub < per && j <= a;
+      int64_t to = 0;
+      bool put = false;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (mine) {
+        const int s = own + path[j], d = own + j;
+        if (s != d) {
+          const int sp = ids[s >> w.ps_log2], dp = ids[d >> w.ps_log2];
+          put = static_cast<uint32_t>(sp) < np && static_cast<uint32_t>(dp) < np;
+          lost |= !put;
+          const int64_t sr = (static_cast<int64_t>(head) << w.ps_log2) + (s & pm);
+          const int64_t dr = (static_cast<int64_t>(head) << w.ps_log2) + (d & pm);
+          if (put) {
+            if (col < CPR) {
+              to = dp * w.kps + dr * DB + col * 16;
+              x = *reinterpret_cast<const uint4 *>(P.k + sp * w.kps + sr * DB + col * 16);
+            } else if (col < 2 * CPR) {
+              to = dp * w.vps + dr * DB + (col - CPR) * 16;
+              x = *reinterpret_cast<const uint4 *>(P.v + sp * w.vps + sr * DB + (col - CPR) * 16);
+            } else if constexpr (E4M3) {
+              const int64_t page = static_cast<int64_t>(w.Hkv) << w.ps_log2;
+              to = dp * page + dr;
+              x.x = static_cast<uint8_t>(P.ke[sp * page + sr]);
+              x.y = static_cast<uint8_t>(P.ve[sp * page + sr]);
+            }
+          }
+        }
+      }
+      __syncthreads();
+      if (put) {
+        if (col < CPR) *reinterpret_cast<uint4 *>(P.k + to) = x;
+        else if (col < 2 * CPR) *reinterpret_cast<uint4 *>(P.v + to) = x;
+        else if constexpr (E4M3) P.ke[to] = static_cast<int8_t>(x.x), P.ve[to] = static_cast<int8_t>(x.y);
+      }
+      __syncthreads();
+    }
+  if (__syncthreads_or(lost)) st |= SPEC_ROW_BAD_PAGE;
+  if (P.status && head == 0 && tid == 0) P.status[b] = st;
+}
+
+// --------------------------------------------------------------------- copy
+constexpr int CY_NT = 128;
+
+struct YP {
+  uint8_t *k, *v;
+  int8_t *ke, *ve;
+  const int32_t *copies;
+  int64_t kps, vps;
+  int32_t n_pages, Hkv, page, row;  // row: bytes of an entry and head
+};
+
+// Grid: heads by triples.  The entries of a head are side by side in a page.
+__global__ void __launch_bounds__(CY_NT) copy_kernel(const __grid_constant__ YP P) {
+  const int32_t *c = P.copies + static_cast<int64_t>(blockIdx.x / P.Hkv) * 3;
+  const int head = blockIdx.x % P.Hkv;
+  const int src = c[0], dst = c[1], n = min(c[2], P.page);
+  if (static_cast<uint32_t>(src) >= static_cast<uint32_t>(P.n_pages) ||
+      static_cast<uint32_t>(dst) >= static_cast<uint32_t>(P.n_pages) || n <= 0 || src == dst)
+    return;
+  const int64_t in = static_cast<int64_t>(head) * P.page * P.row;
+  const uint4 *ks = reinterpret_cast<const uint4 *>(P.k + src * P.kps + in), *vs = reinterpret_cast<const uint4 *>(P.v + src * P.vps + in);
+  uint4 *kd = reinterpret_cast<uint4 *>(P.k + dst * P.kps + in), *vd = reinterpret_cast<uint4 *>(P.v + dst * P.vps + in);
+  const int chunks = n * P.row / 16;  // rows are multiples of 16 bytes
+  int i = threadIdx.x;
+  for (; i + 3 * CY_NT < chunks; i += 4 * CY_NT) {
+    uint4 x[4], y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) x[u] = __ldcs(ks + i + u * CY_NT), y[u] = __ldcs(vs + i + u * CY_NT);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) __stcs(kd + i + u * CY_NT, x[u]), __stcs(vd + i + u * CY_NT, y[u]);
+  }
+  for (; i < chunks; i += CY_NT) {
+    const uint4 x = __ldcs(ks + i), y = __ldcs(vs + i);
+    __stcs(kd + i, x), __stcs(vd + i, y);
+  }
+  if (P.ke) {
+    const int64_t page = static_cast<int64_t>(P.Hkv) * P.page, at = static_cast<int64_t>(head) * P.page;
+    for (int t = threadIdx.x; t < n; t += CY_NT) {
+      P.ke[dst * page + at + t] = P.ke[src * page + at + t];
+      P.ve[dst * page + at + t] = P.ve[src * page + at + t];
+    }
+  }
+}
+
+// ------------------------------------------------------------------- tables
+constexpr int TB_NT = 1024;   // threads of a CTA
+constexpr int TB_CTAS = 8;    // of the cluster
+constexpr int TB_EACH = 32;   // counts of a thread and round: 8 loads of 4
+constexpr int64_t TB_ROUND = static_cast<int64_t>(TB_CTAS) * TB_NT * TB_EACH;
+
+struct Pool {
+  int32_t *refs, *table, *held;
+  int64_t tstride;
+  int32_t B, max_pages, n_pages, prefix, ps_log2;
+  bool vec;  // refs is 16-byte aligned
+};
+
+struct TableShared {
+  uint32_t warp[TB_NT / 32];
+  uint32_t found[2];  // free pages of this CTA's part of a round, by the round's parity
+};
+
+// Exclusive sum over the CTA's threads; *all: the whole sum.  Barriers on both sides.
+__device__ uint32_t cta_sum(uint32_t x, uint32_t *warps, uint32_t *all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t e = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(~0u, e, o);
+    if (lane >= o) e += t;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = e;
+  __syncthreads();
+  const uint32_t mine = warps[lane];
+  uint32_t s = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(~0u, s, o);
+    if (lane >= o) s += t;
+  }
+  *all = __shfl_sync(~0u, s, 31);
+  return e - x + __shfl_sync(~0u, s - mine, warp);
+}
+
+// cum[0 .. n]: sums of cum[0 .. n) before each entry, by the whole CTA.
+__device__ void sum_up(uint32_t *cum, int n, uint32_t *warps) {
+  const int per = (n + TB_NT - 1) / TB_NT, i0 = min(static_cast<int>(threadIdx.x) * per, n), i1 = min(i0 + per, n);
+  uint32_t mine = 0, all;
+  for (int i = i0; i < i1; ++i) mine += cum[i];
+  uint32_t at = cta_sum(mine, warps, &all);
+  for (int i = i0; i < i1; ++i) {
+    const uint32_t x = cum[i];
+    cum[i] = at;
+    at += x;
+  }
+  if (threadIdx.x == 0) cum[n] = all;
+  __syncthreads();
+}
+
+// The largest i < n with cum[i] <= x (x < cum[n]).
+__device__ __forceinline__ int before(const uint32_t *cum, int n, uint32_t x) {
+  int l = 0, r = n;
+  while (r - l > 1) {
+    const int m = (l + r) >> 1;
+    if (cum[m] <= x) l = m;
+    else r = m;
+  }
+  return l;
+}
+
+// Of the thread's 32 counts in round `at` (the first count of the round), those
+// that are of free pages: bit 4 u + k is count at + 1024 warp + 128 u + 4 lane + k
+// (warps numbered over the cluster).
+__device__ uint32_t free_bits(const Pool &P, int64_t at, unsigned rank) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t i0 = at + (static_cast<int64_t>(rank) * (TB_NT / 32) + warp) * 1024 + 4 * lane;
+  uint32_t bits = 0;
+  if (P.vec && i0 + 7 * 128 + 4 <= P.n_pages) {
+    int4 x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) x[u] = __ldcg(reinterpret_cast<const int4 *>(P.refs + i0 + 128 * u));
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      bits |= (static_cast<uint32_t>(x[u].x <= 0) | static_cast<uint32_t>(x[u].y <= 0) << 1 |
+               static_cast<uint32_t>(x[u].z <= 0) << 2 | static_cast<uint32_t>(x[u].w <= 0) << 3) << (4 * u);
+  } else {
+#pragma unroll 1
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t i = i0 + 128 * u + k;
+        if (i < P.n_pages && __ldcg(P.refs + i) <= 0) bits |= 1u << (4 * u + k);
+      }
+  }
+  return bits;
+}
+
+// Takes the lowest free pages for the rows of cum (n + 1 sums of what they need):
+// give(row, k, page) for the k-th page of each row that is served, that is whose
+// sum is within what the pool has.  Returns the number of free pages, or any
+// number from the rows' sum on.  All CTAs of the cluster call it, after a cluster
+// barrier behind the last change of a count.
+template <class F>
+__device__ uint32_t take_pages(const Pool &P, const uint32_t *cum, int n, TableShared &S, F give) {
+  cg::cluster_group cl = cg::this_cluster();
+  const unsigned rank = cl.block_rank();
+  const uint32_t total = cum[n];
+  if (total == 0) return 0;
+  const int rounds = static_cast<int>((P.n_pages + TB_ROUND - 1) / TB_ROUND);
+  const int lane = threadIdx.x & 31;
+  uint32_t bits = 0, at0 = 0, base = 0;
+  int turn = 0;
+  // round r: the free pages of the thread, their number before the thread's warp in
+  // this CTA, and before this CTA in the round; returns that of the whole round
+  auto count = [&](int r) {
+    bits = free_bits(P, r * TB_ROUND, rank);
+    uint32_t all, here = 0;
+    at0 = __shfl_sync(~0u, cta_sum(__popc(bits), S.warp, &all), 0);
+    uint32_t *slot = &S.found[turn++ & 1];
+    if (threadIdx.x == 0) *slot = all;
+    cl.sync();
+    base = 0;
+    for (unsigned c = 0; c < TB_CTAS; ++c) {
+      const uint32_t x = *cl.map_shared_rank(slot, c);
+      if (c < rank) base += x;
+      here += x;
+    }
+    return here;
+  };
+  uint32_t found = 0;
+  for (int r = 0; r < rounds && found < total; ++r) found += count(r);
+  // rows up to the last one whose sum the pool has
+  const uint32_t limit = found >= total ? total : cum[before(cum, n, found)];
+  uint32_t sum = 0;
+  for (int r = 0; r < rounds && sum < limit; ++r) {
+    const uint32_t here = rounds == 1 ? found : count(r);  // one round: as counted
+    // a warp's pages in the order of u, lane, k: sums over the lanes for each u,
+    // four of them in a word (32 x 4 counts fit eight bits)
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      lo |= __popc(bits >> (4 * u) & 15) << (8 * u);
+      hi |= __popc(bits >> (16 + 4 * u) & 15) << (8 * u);
+    }
+    uint32_t el = lo, eh = hi;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t tl = __shfl_up_sync(~0u, el, o), th = __shfl_up_sync(~0u, eh, o);
+      if (lane >= o) el += tl, eh += th;
+    }
+    const uint32_t al = __shfl_sync(~0u, el, 31), ah = __shfl_sync(~0u, eh, 31);
+    el -= lo, eh -= hi;
+    uint32_t at = sum + base + at0;  // of the warp
+    const int64_t i0 = r * TB_ROUND + (static_cast<int64_t>(rank) * (TB_NT / 32) + (threadIdx.x >> 5)) * 1024 + 4 * lane;
+    int row = -1;
+#pragma unroll 1
+    for (int u = 0; u < 8; ++u) {
+      uint32_t k = at + ((u < 4 ? el : eh) >> (8 * (u & 3)) & 255);
+      uint32_t m = bits >> (4 * u) & 15;
+      while (m && k < limit) {
+        const int bit = __ffs(m) - 1;
+        m &= m - 1;
+        if (row < 0 || k >= cum[row + 1]) row = before(cum, n, k);
+        give(row, k - cum[row], static_cast<int32_t>(i0 + 128 * u + bit));
+        ++k;
+      }
+      at += (u < 4 ? al : ah) >> (8 * (u & 3)) & 255;
+    }
+    sum += here;
+  }
+  return found;
+}
+
+struct RP {
+  Pool p;
+  const int32_t *len;
+  int32_t *status;
+  int32_t n;
+};
+
+// Pages that a row of `held` is to hold for `len` + n tokens; -1: bad.
+__device__ __forceinline__ int wanted(const Pool &P, int len, int n, int held, int *st) {
+  const int64_t t = static_cast<int64_t>(len) + n - P.prefix;
+  const int64_t want = len == -1 ? 0 : (t + (1 << P.ps_log2) - 1) >> P.ps_log2;
+  *st = len < -1 || (len >= 0 && t < 0) || want > P.max_pages || held < 0 || held > P.max_pages ? SPEC_ROW_BAD_LENGTH : 0;
+  return *st ? -1 : static_cast<int>(want);
+}
+
+__global__ void __cluster_dims__(TB_CTAS, 1, 1) __launch_bounds__(TB_NT) resize_kernel(const __grid_constant__ RP R) {
+  extern __shared__ uint32_t cum[];  // B + 1 pages to take, B + 1 pages to give back
+  __shared__ TableShared S;
+  const Pool &P = R.p;
+  cg::cluster_group cl = cg::this_cluster();
+  const unsigned rank = cl.block_rank();
+  const int B = P.B, tid = threadIdx.x;
+  uint32_t *gone = cum + B + 1;
+  for (int b = tid; b < B; b += TB_NT) {
+    const int held = P.held[b];
+    int st;
+    const int want = wanted(P, R.len[b], R.n, held, &st);
+    cum[b] = want > held ? want - held : 0;
+    gone[b] = want >= 0 && want < held ? held - want : 0;
+    if (rank == 0 && R.status) R.status[b] = st;
+  }
+  __syncthreads();
+  sum_up(cum, B, S.warp);
+  sum_up(gone, B, S.warp);
+  if (gone[B]) {
+    cl.sync();  // the status words are written
+    const uint32_t np = static_cast<uint32_t>(P.n_pages);
+    int row = -1;
+    uint32_t end = 0;
+    for (uint32_t x = rank * TB_NT + tid; x < gone[B]; x += TB_CTAS * TB_NT) {
+      if (row < 0 || x >= end) row = before(gone, B, x), end = gone[row + 1];
+      // the last gone[row + 1] - gone[row] entries of the row
+      const int at = P.held[row] - static_cast<int>(end - x);
+      const int id = P.table[row * P.tstride + at];
+      if (static_cast<uint32_t>(id) < np) atomicSub(P.refs + id, 1);
+      else if (R.status) atomicOr(R.status + row, SPEC_ROW_BAD_PAGE);
+    }
+    __threadfence();
+  }
+  cl.sync();  // counts, status words; every CTA has read what is held
+  const uint32_t found = take_pages(P, cum, B, S, [&](int row, uint32_t k, int32_t id) {
+    P.table[row * P.tstride + P.held[row] + k] = id;
+    P.refs[id] = 1;
+  });
+  cl.sync();  // what is held is not read any more
+  for (int b = rank * TB_NT + tid; b < B; b += TB_CTAS * TB_NT) {
+    const uint32_t take = cum[b + 1] - cum[b], give = gone[b + 1] - gone[b];
+    if (take && cum[b + 1] > found) {
+      if (R.status) atomicOr(R.status + b, SPEC_ROW_NO_PAGES);
+    } else if (take | give) {
+      P.held[b] += static_cast<int>(take) - static_cast<int>(give);
+    }
+  }
+}
+
+struct FP {
+  Pool p;
+  int32_t *len;
+  const int32_t *src, *dst;
+  int32_t *copies, *status;
+  int32_t n;
+};
+
+__global__ void __cluster_dims__(TB_CTAS, 1, 1) __launch_bounds__(TB_NT) fork_kernel(const __grid_constant__ FP F) {
+  extern __shared__ uint32_t cum[];  // n + 1 pages to take, n + 1 pages to share, B first forks to each row, n flags
+  __shared__ TableShared S;
+  const Pool &P = F.p;
+  cg::cluster_group cl = cg::this_cluster();
+  const unsigned rank = cl.block_rank();
+  const int n = F.n, tid = threadIdx.x, lg = P.ps_log2;
+  const uint32_t B = static_cast<uint32_t>(P.B), np = static_cast<uint32_t>(P.n_pages);
+  uint32_t *shared = cum + n + 1, *first = shared + n + 1;
+  uint8_t *fine = reinterpret_cast<uint8_t *>(first + P.B);
+  for (int b = tid; b < P.B; b += TB_NT) first[b] = ~0u;
+  __syncthreads();
+  for (int j = tid; j < n; j += TB_NT) {
+    const uint32_t d = F.dst[j];
+    if (d < B) atomicMin(first + d, static_cast<uint32_t>(j));
+  }
+  __syncthreads();
+  for (int j = tid; j < n; j += TB_NT) {
+    const uint32_t s = F.src[j], d = F.dst[j];
+    int st = 0, need = 0, full = 0;
+    if (s >= B || d >= B || s == d || first[d] != static_cast<uint32_t>(j) || P.held[d] != 0) {
+      st = SPEC_ROW_BAD_FORK;
+    } else {
+      const int len = F.len[s], held = P.held[s];
+      const int64_t t = len == -1 ? 0 : static_cast<int64_t>(len) - P.prefix;
+      if (len < -1 || t < 0 || held < 0 || held > P.max_pages || (t + (1 << lg) - 1) >> lg > held) {
+        st = SPEC_ROW_BAD_LENGTH;
+      } else {
+        full = static_cast<int>(t >> lg);
+        need = (t & ((1 << lg) - 1)) != 0;
+      }
+    }
+    cum[j] = need;
+    shared[j] = full;
+    fine[j] = !st;
+    if (rank == 0) {
+      if (F.status) F.status[j] = st;
+      F.copies[3 * j] = F.copies[3 * j + 1] = -1, F.copies[3 * j + 2] = 0;
+    }
+  }
+  __syncthreads();
+  sum_up(cum, n, S.warp);
+  sum_up(shared, n, S.warp);
+  cl.sync();  // status words and copies
+  const uint32_t found = take_pages(P, cum, n, S, [&](int j, uint32_t, int32_t id) {
+    const int s = F.src[j], full = static_cast<int>(shared[j + 1] - shared[j]);
+    const int old = P.table[s * P.tstride + full];
+    P.table[F.dst[j] * P.tstride + full] = id;
+    P.refs[id] = 1;
+    if (static_cast<uint32_t>(old) < np) {
+      F.copies[3 * j] = old;
+      F.copies[3 * j + 1] = id;
+      F.copies[3 * j + 2] = F.len[s] - P.prefix - (full << lg);
+    } else if (F.status) {
+      atomicOr(F.status + j, SPEC_ROW_BAD_PAGE);
+    }
+  });
+  int j = -1;
+  for (uint32_t x = rank * TB_NT + tid; x < shared[n]; x += TB_CTAS * TB_NT) {
+    if (j < 0 || x >= shared[j + 1]) j = before(shared, n, x);
+    if (cum[j + 1] > cum[j] && cum[j + 1] > found) continue;
+    const int at = static_cast<int>(x - shared[j]);
+    const int id = P.table[F.src[j] * P.tstride + at];
+    P.table[F.dst[j] * P.tstride + at] = id;
+    if (static_cast<uint32_t>(id) < np) atomicAdd(P.refs + id, 1);
+    else if (F.status) atomicOr(F.status + j, SPEC_ROW_BAD_PAGE);
+  }
+  const int k = rank * TB_NT + tid;  // n is at most half as many
+  const bool mine = k < n && fine[k < n ? k : 0];
+  const uint32_t take = mine ? cum[k + 1] - cum[k] : 0;
+  const int len = mine ? F.len[F.src[k]] : 0;
+  cl.sync();  // lengths and what is held are not read any more
+  if (!mine) return;
+  if (take && cum[k + 1] > found) {
+    if (F.status) atomicOr(F.status + k, SPEC_ROW_NO_PAGES);
+    return;
+  }
+  P.held[F.dst[k]] = static_cast<int>(shared[k + 1] - shared[k] + take);
+  F.len[F.dst[k]] = len;
+}
+
+spec_status check_pool(const spec_kv_pool *p, Pool &P) {
+  if (!p || p->B < 0 || p->max_pages < 0 || p->n_pages < 0 || p->page_size < 1 || p->prefix_len < 0 ||
+      p->table_row_stride < p->max_pages)
+    return SPEC_ERR_INVALID_ARG;
+  const int lg = kv::log2_page(p->page_size);
+  if (lg < 0 || p->B > kv::kMaxB || static_cast<int64_t>(p->max_pages) * p->page_size > (1 << 30) ||
+      static_cast<int64_t>(p->max_pages) * p->B > INT32_MAX || p->prefix_len > (1 << 30))
+    return SPEC_ERR_UNSUPPORTED;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(p->refs) | reinterpret_cast<uintptr_t>(p->table) |
+                        reinterpret_cast<uintptr_t>(p->held);
+  if (all % 4) return SPEC_ERR_INVALID_ARG;
+  if (p->B > 0 && ((p->n_pages > 0 && !p->refs) || (p->max_pages > 0 && !p->table) || !p->held))
+    return SPEC_ERR_INVALID_ARG;
+  P = {p->refs, p->table, p->held, p->table_row_stride, p->B, p->max_pages, p->n_pages, p->prefix_len, lg,
+       reinterpret_cast<uintptr_t>(p->refs) % 16 == 0};
+  return SPEC_OK;
+}
+
+}  // namespace
+
+extern "C" spec_status spec_kv_compact(const spec_kv_cache *cache, const spec_kv_batch *batch,
+                                       const int32_t *path, const int32_t *accepted_len,
+                                       int32_t *row_status, void *stream) {
+  MP P = {};
+  const spec_status st = kv::make_view(cache, batch, true, P.w);
+  if (st != SPEC_OK) return st;
+  if (P.w.N > SPEC_TREE_MAX) return SPEC_ERR_UNSUPPORTED;
+  if (P.w.B == 0) return SPEC_OK;
+  if (!path || !accepted_len || reinterpret_cast<uintptr_t>(path) % 4 ||
+      reinterpret_cast<uintptr_t>(accepted_len) % 4)
+    return SPEC_ERR_INVALID_ARG;
+  P.k = static_cast<uint8_t *>(cache->k_pages);
+  P.v = static_cast<uint8_t *>(cache->v_pages);
+  P.ke = cache->k_exp;
+  P.ve = cache->v_exp;
+  P.path = path;
+  P.acc = accepted_len;
+  P.status = row_status;
+  const dim3 grid(P.w.Hkv, P.w.B);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cache->format == SPEC_KV_E4M3) compact_kernel<true><<<grid, MV_NT, 0, s>>>(P, cache->head_dim);
+  else compact_kernel<false><<<grid, MV_NT, 0, s>>>(P, cache->head_dim);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+extern "C" spec_status spec_kv_copy(const spec_kv_cache *cache, const int32_t *copies, int32_t n,
+                                    void *stream) {
+  spec_kv_batch none = {};  // the cache's own checks
+  View w;
+  spec_status st = kv::make_view(cache, &none, false, w);
+  if (st != SPEC_OK) return st;
+  if (n < 0) return SPEC_ERR_INVALID_ARG;
+  if (n > 1 << 20) return SPEC_ERR_UNSUPPORTED;
+  if (n == 0 || cache->n_pages == 0) return SPEC_OK;
+  const bool e4m3 = cache->format == SPEC_KV_E4M3;
+  if (!copies || reinterpret_cast<uintptr_t>(copies) % 4 || !cache->k_pages || !cache->v_pages ||
+      (e4m3 && (!cache->k_exp || !cache->v_exp)))
+    return SPEC_ERR_INVALID_ARG;
+  uintptr_t all = reinterpret_cast<uintptr_t>(cache->k_pages) | reinterpret_cast<uintptr_t>(cache->v_pages);
+  if (e4m3) all |= reinterpret_cast<uintptr_t>(cache->k_exp) | reinterpret_cast<uintptr_t>(cache->v_exp);
+  if (all % 16) return SPEC_ERR_INVALID_ARG;
+  YP P = {static_cast<uint8_t *>(cache->k_pages), static_cast<uint8_t *>(cache->v_pages),
+          e4m3 ? cache->k_exp : nullptr, e4m3 ? cache->v_exp : nullptr, copies, w.kps, w.vps,
+          cache->n_pages, cache->n_kv_heads, cache->page_size, cache->head_dim * (e4m3 ? 1 : 2)};
+  copy_kernel<<<static_cast<unsigned>(n) * cache->n_kv_heads, CY_NT, 0, static_cast<cudaStream_t>(stream)>>>(P);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+extern "C" spec_status spec_kv_resize(const spec_kv_pool *pool, const int32_t *kv_len, int32_t n_step,
+                                      int32_t *row_status, void *stream) {
+  RP R = {};
+  const spec_status st = check_pool(pool, R.p);
+  if (st != SPEC_OK) return st;
+  if (n_step < 0) return SPEC_ERR_INVALID_ARG;
+  if (n_step > 1 << 30) return SPEC_ERR_UNSUPPORTED;
+  if (pool->B == 0) return SPEC_OK;
+  if (!kv_len || reinterpret_cast<uintptr_t>(kv_len) % 4) return SPEC_ERR_INVALID_ARG;
+  R.len = kv_len;
+  R.n = n_step;
+  R.status = row_status;
+  const int smem = 2 * (pool->B + 1) * 4;
+  resize_kernel<<<TB_CTAS, TB_NT, smem, static_cast<cudaStream_t>(stream)>>>(R);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+extern "C" spec_status spec_kv_fork(const spec_kv_pool *pool, int32_t *kv_len, const int32_t *src,
+                                    const int32_t *dst, int32_t n, int32_t *copies, int32_t *fork_status,
+                                    void *stream) {
+  FP F = {};
+  const spec_status st = check_pool(pool, F.p);
+  if (st != SPEC_OK) return st;
+  if (n < 0) return SPEC_ERR_INVALID_ARG;
+  if (n > kv::kMaxB) return SPEC_ERR_UNSUPPORTED;
+  if (n == 0) return SPEC_OK;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(src) |
+                        reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(copies);
+  if (!src || !dst || !copies || all % 4 || (pool->B > 0 && !kv_len)) return SPEC_ERR_INVALID_ARG;
+  F.len = kv_len;
+  F.src = src;
+  F.dst = dst;
+  F.n = n;
+  F.copies = copies;
+  F.status = fork_status;
+  const int smem = (2 * (n + 1) + pool->B) * 4 + n;
+  constexpr int most = (2 * (kv::kMaxB + 1) + kv::kMaxB) * 4 + kv::kMaxB;
+  static std::atomic<bool> ready[64] = {};  // the kernel's shared memory limit, set once per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return SPEC_ERR_CUDA;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
+      return SPEC_ERR_CUDA;
+    ready[dev].store(true, std::memory_order_release);
+  }
+  fork_kernel<<<TB_CTAS, TB_NT, smem, static_cast<cudaStream_t>(stream)>>>(F);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}

@@ -123,7 +123,8 @@ struct TileInfo {
   int page[4];                // page of each 16 tokens, -1: none
 };
 
-template <int D, bool E4M3, int WR, int WT>
+// TREE: own items of a step whose queries see the nodes of their mask rows (P.mask).
+template <int D, bool E4M3, int WR, int WT, bool TREE>
 __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTAS)
     span_kernel(const __grid_constant__ SpanParams P) {
   using C = SpanCfg<D, E4M3, WR, WT>;
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
   const int wr = warp / WT, wt = warp % WT;
   const int g = lane >> 2, q4 = lane & 3;
   const int G = P.G, B = w.B;
-  const bool pre = P.prefix != 0;
+  const bool pre = !TREE && P.prefix != 0;
 
   // --- the plan: running sums over the sequences
   {
@@ -326,12 +327,14 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
   };
   // --- row r (of all rows of the item's sequence, or of the prefix): its query
   // and the tokens that it sees; null past the last row
-  auto query = [&](const TileInfo &T, int r, int &lim) -> const __nv_bfloat16 * {
-    lim = 0;
+  // (with a tree: that it sees before the step), and its place in the step
+  auto query = [&](const TileInfo &T, int r, int &lim, int &node) -> const __nv_bfloat16 * {
+    lim = 0, node = -1;
     if (r >= T.rows) return nullptr;
     const int b = pre ? before(r) : T.b, rr = pre ? r - static_cast<int>(cum0[b]) : r;
     const int i = rr / G, gg = rr - i * G;
-    lim = pre ? w.prefix : T.own + i + 1;
+    lim = pre ? w.prefix : TREE ? T.own : T.own + i + 1;
+    node = i;
     return P.q + b * P.qs0 + i * P.qs1 + (T.head * G + gg) * P.qs2;
   };
   // --- 16 rows: the queries of the item that begins with a tile, slot k of 3
@@ -339,8 +342,8 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
     constexpr int CH = D / 8;
     for (int x = tid; x < RT * CH; x += NT) {
       const int r = x / CH, ch = x - r * CH;
-      int lim;
-      const __nv_bfloat16 *src = query(T, T.row0 + r, lim);
+      int lim, node;
+      const __nv_bfloat16 *src = query(T, T.row0 + r, lim, node);
       uint8_t *dst = qbuf + (k * RT + r) * C::QLD + ch * 16;
       if (P.qvec) {
         cp16(s32(dst), src ? src + 8 * ch : P.q, src != nullptr);
@@ -388,6 +391,7 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
   float M0, M1, l0, l1;
   float cq0 = P.c, cq1 = P.c;  // score factors of rows g and g + 8: scale log2 e 2^eq
   int lim0 = 0, lim1 = 0;      // tokens that they see
+  int nd0 = -1, nd1 = -1;      // their places in the step
   int rows = 0;                // rows of the item
   int free_to = 0;             // tokens that every row sees
 
@@ -415,10 +419,10 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
 
     if (T.first) {  // a new item: its rows' queries, in registers
       rows = T.rows - T.row0;
-      free_to = pre ? w.prefix : T.own + T.row0 / G + 1;
+      free_to = pre ? w.prefix : TREE ? T.own : T.own + T.row0 / G + 1;
       const __nv_bfloat16 *src[2];
-      src[0] = query(T, T.row0 + wr * 16 + g, lim0);
-      src[1] = query(T, T.row0 + wr * 16 + g + 8, lim1);
+      src[0] = query(T, T.row0 + wr * 16 + g, lim0, nd0);
+      src[1] = query(T, T.row0 + wr * 16 + g + 8, lim1, nd1);
       const uint8_t *qs = qbuf + (slot_out * RT + g) * C::QLD;
       if (WR == 1) slot_out = slot_out == 2 ? 0 : slot_out + 1;
       auto word = [&](int a, int d) -> uint32_t {  // elements d, d + 1 of row g + 8 a
@@ -476,6 +480,12 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
     const float4 *fac = consts + x % ST * kTile;
     const int t0 = T.t0, held = T.held;
     const bool edge = t0 + kTile > free_to;
+    uint64_t see0 = 0, see1 = 0;  // with a tree: of the tile's tokens, those that the rows see
+    if (TREE && edge) {
+      const int32_t *mask = P.mask + static_cast<int64_t>(T.b) * w.N * P.mask_words;
+      see0 = nd0 < 0 ? 0 : seen_nodes(mask + nd0 * P.mask_words, P.mask_words, held - T.own, t0 - T.own);
+      see1 = nd1 < 0 ? 0 : seen_nodes(mask + nd1 * P.mask_words, P.mask_words, held - T.own, t0 - T.own);
+    }
     // Tokens that some row of the tile does not see but that are present: a
     // NaN or infinity among their values would reach every row through a zero
     // weight.  Take such elements out; add them below to the rows that see them.
@@ -565,10 +575,17 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
       }
       if (edge) {
         const int t = t0 + col;
-        if (t >= lim0) s[j][0] = -INFINITY;
-        if (t + 1 >= lim0) s[j][1] = -INFINITY;
-        if (t >= lim1) s[j][2] = -INFINITY;
-        if (t + 1 >= lim1) s[j][3] = -INFINITY;
+        if constexpr (TREE) {
+          if (!(see0 >> col & 1)) s[j][0] = -INFINITY;
+          if (!(see0 >> col & 2)) s[j][1] = -INFINITY;
+          if (!(see1 >> col & 1)) s[j][2] = -INFINITY;
+          if (!(see1 >> col & 2)) s[j][3] = -INFINITY;
+        } else {
+          if (t >= lim0) s[j][0] = -INFINITY;
+          if (t + 1 >= lim0) s[j][1] = -INFINITY;
+          if (t >= lim1) s[j][2] = -INFINITY;
+          if (t + 1 >= lim1) s[j][3] = -INFINITY;
+        }
       }
       m0 = fmaxf(m0, fmaxf(s[j][0], s[j][1]));
       m1 = fmaxf(m1, fmaxf(s[j][2], s[j][3]));
@@ -647,8 +664,8 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
               const uint16_t u = reinterpret_cast<const uint16_t *>(v)[8 * i + 2 * q4 + e];
               x = (u & 0x7f80) == 0x7f80 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : 0.0f;
             }
-            if (t < lim0) o[i][e] += x;
-            if (t < lim1) o[i][2 + e] += x;
+            if (TREE ? see0 >> row & 1 : t < lim0) o[i][e] += x;
+            if (TREE ? see1 >> row & 1 : t < lim1) o[i][2 + e] += x;
           }
       }
       __syncthreads();
@@ -738,11 +755,11 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
   cp_wait<0>();
 }
 
-template <int D, bool E4M3, int WR, int WT>
+template <int D, bool E4M3, int WR, int WT, bool TREE>
 cudaError_t span_go(const SpanParams &p, int64_t tiles, int *grid, cudaStream_t s) {
   using C = SpanCfg<D, E4M3, WR, WT>;
   const int smem = C::FIXED + 8 * (p.w.B + 1);
-  auto *f = span_kernel<D, E4M3, WR, WT>;
+  auto *f = span_kernel<D, E4M3, WR, WT, TREE>;
   static Slots slots;  // of this kernel, per device
   int sms = 0, occ = 0;
   const cudaError_t e = slots.get(reinterpret_cast<const void *>(f), C::NT, C::FIXED, C::FIXED + 8 * (kMaxB + 1),
@@ -759,13 +776,13 @@ cudaError_t span_go(const SpanParams &p, int64_t tiles, int *grid, cudaStream_t 
   return cudaGetLastError();
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool TREE = false>
 cudaError_t span_any(const SpanParams &p, int wr, int64_t tiles, int *grid, cudaStream_t s) {
   switch (wr) {
-    case 1: return span_go<D, E4M3, 1, 4>(p, tiles, grid, s);
-    case 2: return span_go<D, E4M3, 2, 2>(p, tiles, grid, s);
-    case 3: return span_go<D, E4M3, 3, 1>(p, tiles, grid, s);
-    default: return span_go<D, E4M3, 4, 1>(p, tiles, grid, s);
+    case 1: return span_go<D, E4M3, 1, 4, TREE>(p, tiles, grid, s);
+    case 2: return span_go<D, E4M3, 2, 2, TREE>(p, tiles, grid, s);
+    case 3: return span_go<D, E4M3, 3, 1, TREE>(p, tiles, grid, s);
+    default: return span_go<D, E4M3, 4, 1, TREE>(p, tiles, grid, s);
   }
 }
 

@@ -37,6 +37,8 @@ struct SpanParams {
   int32_t G;              // query heads per key/value head
   int32_t prefix;         // 1: prefix items
   bool qvec;              // q rows are 4-byte aligned; 16-byte (dense kernel, 16 rows)
+  const int32_t *mask;    // trees: [B, N, mask_words]
+  int32_t mask_words;
 };
 
 constexpr int kSmSmem = 228 * 1024;  // shared memory of an SM; 1 KB of it a CTA's own
@@ -78,6 +80,28 @@ cudaError_t span_bf16_64(const SpanParams &, int, int64_t, int *, cudaStream_t);
 cudaError_t span_bf16_80(const SpanParams &, int, int64_t, int *, cudaStream_t);
 cudaError_t span_bf16_96(const SpanParams &, int, int64_t, int *, cudaStream_t);
 cudaError_t span_bf16_128(const SpanParams &, int, int64_t, int *, cudaStream_t);
+
+// The same for trees (own items).
+cudaError_t tree_e4m3_64(const SpanParams &, int, int64_t, int *, cudaStream_t);
+cudaError_t tree_e4m3_80(const SpanParams &, int, int64_t, int *, cudaStream_t);
+cudaError_t tree_e4m3_96(const SpanParams &, int, int64_t, int *, cudaStream_t);
+cudaError_t tree_e4m3_128(const SpanParams &, int, int64_t, int *, cudaStream_t);
+cudaError_t tree_bf16_64(const SpanParams &, int, int64_t, int *, cudaStream_t);
+cudaError_t tree_bf16_80(const SpanParams &, int, int64_t, int *, cudaStream_t);
+cudaError_t tree_bf16_96(const SpanParams &, int, int64_t, int *, cudaStream_t);
+cudaError_t tree_bf16_128(const SpanParams &, int, int64_t, int *, cudaStream_t);
+
+// Of 64 tokens from place `off` of the step on (below 0: before the step), those
+// that a node sees: all before the step, and of the step's n those of its mask row.
+__device__ __forceinline__ uint64_t seen_nodes(const int32_t *row, int words, int n, int off) {
+  const int i = off >> 5;
+  uint32_t x[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) x[k] = i + k < 0 ? ~0u : i + k < words ? static_cast<uint32_t>(__ldg(row + i + k)) : 0u;
+  const uint64_t see = static_cast<uint64_t>(__funnelshift_r(x[1], x[2], off & 31)) << 32 | __funnelshift_r(x[0], x[1], off & 31);
+  const int left = n - off;
+  return left >= 64 ? see : left <= 0 ? 0 : see & ((1ull << left) - 1);
+}
 
 // The dense kernel: prefix items of DN_ROWS rows, tiles of 128 tokens.
 constexpr int DN_ROWS = 256;

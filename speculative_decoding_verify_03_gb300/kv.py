@@ -1,5 +1,5 @@
-"""The key/value cache of the verify step and the attention that reads it:
-the binding of include/spec_kv.h."""
+"""The key/value cache of the verify step, the attention that reads it and the
+page tables that it is kept in: the binding of include/spec_kv.h."""
 from __future__ import annotations
 
 import ctypes
@@ -7,7 +7,7 @@ import ctypes
 import torch
 
 SPEC_KV_BF16, SPEC_KV_E4M3 = 0, 1
-ROW_BAD_LENGTH, ROW_BAD_PAGE = 1 << 7, 1 << 8
+ROW_BAD_LENGTH, ROW_BAD_PAGE, ROW_NO_PAGES, ROW_BAD_FORK = 1 << 7, 1 << 8, 1 << 9, 1 << 12
 
 _i32, _f32, _bf16 = torch.int32, torch.float32, torch.bfloat16
 _byref = ctypes.byref
@@ -37,6 +37,13 @@ class SpecKvBatch(ctypes.Structure):
                 ("table_row_stride", ctypes.c_int64), ("page_table", ctypes.c_void_p),
                 ("prefix_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
                 ("gamma_per_row", ctypes.c_void_p)]
+
+
+class SpecKvPool(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("prefix_len", ctypes.c_int32), ("table_row_stride", ctypes.c_int64),
+                ("refs", ctypes.c_void_p), ("table", ctypes.c_void_p), ("held", ctypes.c_void_p)]
 
 
 _Strides = ctypes.c_int64 * 3
@@ -275,6 +282,12 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     stream as well, once that waits for it.  Returns (out [B, gamma_max + 1,
     n_heads, head_dim] bfloat16, lse [B, gamma_max + 1, n_heads] float32), and
     row_status [B] when with_status."""
+    return _attend(q, cache, page_table, kv_len, None, prefix_table, prefix_len, gamma_per_row, scale, workspace, out,
+                   with_status, stream)
+
+
+def _attend(q, cache, page_table, kv_len, mask, prefix_table, prefix_len, gamma_per_row, scale, workspace, out,
+            with_status, stream=None):
     dev = cache.device
     shape = q.shape
     if q.dtype is not _bf16:
@@ -290,13 +303,19 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     if Hq < 1 or Hq % cache.n_kv_heads:
         raise ValueError("n_heads must be a multiple of the cache's n_kv_heads")
     b = _batch(cache, page_table, kv_len, N - 1, prefix_table, prefix_len, gamma_per_row)
+    if mask is not None:
+        if mask.dtype is not _i32:
+            raise TypeError("mask must be int32")
+        if mask.shape != (B, N, -(-N // 32)) or mask.device != dev or not mask.is_contiguous():
+            raise ValueError(f"mask must be contiguous [{B}, {N}, {-(-N // 32)}] on {dev}")
     if _elsewhere(stream, dev):
-        return _on(stream, dev, spec_attend, q, cache, page_table, kv_len, prefix_table, prefix_len, gamma_per_row,
+        return _on(stream, dev, _attend, q, cache, page_table, kv_len, mask, prefix_table, prefix_len, gamma_per_row,
                    scale, workspace, out, with_status)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")
-        workspace = torch.empty(_lib().spec_attend_workspace_size(cache.ref, _byref(b), Hq), dtype=torch.uint8, device=dev)
+        size = _lib().spec_attend_workspace_size if mask is None else _lib().spec_attend_tree_workspace_size
+        workspace = torch.empty(size(cache.ref, _byref(b), Hq), dtype=torch.uint8, device=dev)
     elif workspace is None or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be 'auto' or a contiguous tensor on {dev}")
     if out is None:
@@ -308,9 +327,137 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
                 lse.dtype is not _f32 or not lse.is_contiguous() or o.device != dev or lse.device != dev):
             raise ValueError("out must be contiguous bfloat16 and float32 tensors of the results' shapes")
     st = _status(with_status, B, dev)
-    code = _lib().spec_attend(cache.ref, _byref(b), q.data_ptr(), Hq, _byref(_Strides(*qs[:3])),
-                              D ** -0.5 if scale is None else float(scale), o.data_ptr(), lse.data_ptr(), _ptr(st),
-                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
+    rest = (q.data_ptr(), Hq, _byref(_Strides(*qs[:3])), D ** -0.5 if scale is None else float(scale), o.data_ptr(),
+            lse.data_ptr(), _ptr(st), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _raw_stream(dev.index))
+    if mask is None:
+        code = _lib().spec_attend(cache.ref, _byref(b), *rest)
+    else:
+        code = _lib().spec_attend_tree(cache.ref, _byref(b), mask.data_ptr(), *rest)
     if code:
         _check(code)
     return (o, lse, st) if with_status else (o, lse)
+
+
+def attend_tree_workspace_bytes(cache, batch, n_heads) -> int:
+    """Workspace bytes of spec_attend_tree, as attend_workspace_bytes."""
+    shapes = SpecKvBatch(batch.B, batch.gamma_max, batch.max_pages, batch.prefix_len, batch.max_pages)
+    return _lib().spec_attend_tree_workspace_size(cache.ref, _byref(shapes), n_heads)
+
+
+def spec_attend_tree(q, cache, page_table, kv_len, mask, prefix_table=None, prefix_len=0, gamma_per_row=None,
+                     scale=None, workspace="auto", out=None, with_status=False, stream=None):
+    """The attention of a step whose tokens are a tree's nodes (see
+    spec_attend_tree in include/spec_kv.h): as spec_attend, but query i of
+    sequence b attends to positions 0 .. kv_len[b] - 1 and to those nodes j of
+    the step (position kv_len[b] + j) whose bit is set in its row of mask [B,
+    gamma_max + 1, ceil((gamma_max + 1) / 32)] int32: spec_tree_mask's, or any
+    other.  A query that sees nothing gives 0 and -inf.  workspace: a tensor of
+    attend_tree_workspace_bytes, or "auto"."""
+    if mask is None:
+        raise TypeError("mask must be an int32 tensor")
+    return _attend(q, cache, page_table, kv_len, mask, prefix_table, prefix_len, gamma_per_row, scale, workspace, out,
+                   with_status, stream)
+
+
+def spec_kv_compact(cache, page_table, kv_len, path, accepted_len, prefix_len=0, with_status=False, stream=None):
+    """Move the entries of an accepted path together (see spec_kv_compact in
+    include/spec_kv.h): for j = 1 .. accepted_len[b] the entry at kv_len[b] +
+    path[b, j] goes to kv_len[b] + j, with path [B, gamma_max + 1] and
+    accepted_len [B] of spec_tree_accept and kv_len the lengths before the
+    step.  One call for every cache of the model.  Updates the cache in place;
+    returns row_status [B] when with_status, else None."""
+    dev = cache.device
+    if path.dtype is not _i32:
+        raise TypeError("path must be int32")
+    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    if path.dim() != 2 or path.shape[0] != B or path.shape[1] < 1 or path.device != dev or not path.is_contiguous():
+        raise ValueError(f"path must be contiguous [{B}, gamma_max + 1] on {dev}")
+    acc = _int32("accepted_len", accepted_len, B, dev)
+    b = _batch(cache, page_table, kv_len, path.shape[1] - 1, None, 0, None)
+    if _elsewhere(stream, dev):
+        return _on(stream, dev, spec_kv_compact, cache, page_table, kv_len, path, accepted_len, prefix_len, with_status)
+    if prefix_len:
+        b.prefix_len = int(prefix_len)
+        b.prefix_table = b.page_table  # not read: the step is past the prefix
+    st = _status(with_status, B, dev)
+    code = _lib().spec_kv_compact(cache.ref, _byref(b), path.data_ptr(), acc, _ptr(st), _raw_stream(dev.index))
+    if code:
+        _check(code)
+    return st
+
+
+def _pool(refs, page_table, held, page_size, prefix_len):
+    dev = refs.device
+    n_pages = _int32("refs", refs, refs.shape[0] if refs.dim() == 1 else -1, dev)
+    if page_table.dtype is not _i32:
+        raise TypeError("page_table must be int32")
+    if page_table.dim() != 2 or page_table.device != dev:
+        raise ValueError(f"page_table must be [B, max_pages] on {dev}")
+    B, mp = page_table.shape
+    row, col = page_table.stride()
+    if (B and mp > 1 and col != 1) or (B > 1 and row < mp):
+        raise ValueError("page_table rows must be contiguous and not overlap")
+    return SpecKvPool(B, mp, refs.shape[0], int(page_size), int(prefix_len), row if B > 1 else mp, n_pages,
+                      page_table.data_ptr(), _int32("held", held, B, dev))
+
+
+def spec_kv_resize(refs, page_table, held, kv_len, n_step, page_size, prefix_len=0, with_status=False, stream=None):
+    """Let every row hold kv_len[b] + n_step tokens, or none where kv_len[b] is -1
+    (see spec_kv_resize in include/spec_kv.h): refs [n_pages] int32 counts the
+    table entries that hold each page (0: free); page_table [B, max_pages] int32;
+    held [B] int32 its entries in use.  Pages that are too many are given back,
+    then the free pages of the lowest numbers are taken, row by row.  No other
+    call may use refs meanwhile.  Updates the three in place; returns row_status
+    [B] when with_status (ROW_NO_PAGES: the row keeps what it has), else None."""
+    dev = refs.device
+    p = _pool(refs, page_table, held, page_size, prefix_len)
+    lens = _int32("kv_len", kv_len, p.B, dev)
+    if _elsewhere(stream, dev):
+        return _on(stream, dev, spec_kv_resize, refs, page_table, held, kv_len, n_step, page_size, prefix_len,
+                   with_status)
+    st = _status(with_status, p.B, dev)
+    code = _lib().spec_kv_resize(_byref(p), lens, int(n_step), _ptr(st), _raw_stream(dev.index))
+    if code:
+        _check(code)
+    return st
+
+
+def spec_kv_fork(refs, page_table, held, kv_len, src, dst, page_size, prefix_len=0, with_status=False, stream=None):
+    """Let rows dst [n] int32, which hold no pages, become forks of rows src [n]
+    (see spec_kv_fork in include/spec_kv.h): full pages are shared, a last page
+    that is not full is the fork's own.  refs, page_table and held as in
+    spec_kv_resize; kv_len [B] int32.  Updates the four in place; returns
+    copies [n, 3] int32, what spec_kv_copy is to copy in every cache, and the
+    forks' status [n] when with_status."""
+    dev = refs.device
+    p = _pool(refs, page_table, held, page_size, prefix_len)
+    lens = _int32("kv_len", kv_len, p.B, dev)
+    n = src.shape[0] if src.dim() == 1 else -1
+    s, d = _int32("src", src, n, dev), _int32("dst", dst, n, dev)
+    if _elsewhere(stream, dev):
+        return _on(stream, dev, spec_kv_fork, refs, page_table, held, kv_len, src, dst, page_size, prefix_len,
+                   with_status)
+    copies = torch.empty((n, 3), dtype=_i32, device=dev)
+    st = _status(with_status, n, dev)
+    code = _lib().spec_kv_fork(_byref(p), lens, s, d, n, copies.data_ptr(), _ptr(st), _raw_stream(dev.index))
+    if code:
+        _check(code)
+    return (copies, st) if with_status else copies
+
+
+def spec_kv_copy(cache, copies, stream=None):
+    """Copy entries between pages of a cache (see spec_kv_copy in
+    include/spec_kv.h): for each row (page, new page, tokens) of copies [n, 3]
+    int32 the first slots of all heads.  No page may be the target of two rows,
+    or the source of one and the target of another.  Updates the cache in place."""
+    dev = cache.device
+    if copies.dtype is not _i32:
+        raise TypeError("copies must be int32")
+    if copies.dim() != 2 or copies.shape[1] != 3 or copies.device != dev or not copies.is_contiguous():
+        raise ValueError(f"copies must be contiguous [n, 3] on {dev}")
+    if _elsewhere(stream, dev):
+        return _on(stream, dev, spec_kv_copy, cache, copies)
+    code = _lib().spec_kv_copy(cache.ref, copies.data_ptr(), copies.shape[0], _raw_stream(dev.index))
+    if code:
+        _check(code)
