@@ -23,7 +23,8 @@ _SOURCES = [os.path.join(_HERE, "csrc", f) for f in ("spec_verify.cu", "spec_str
                                                       "kv_span_e4m3_96_128.cu",
                                                       "kv_span_bf16_64_80.cu",
                                                       "kv_span_bf16_96_128.cu", "kv_dense_e4m3.cu",
-                                                      "kv_dense_bf16.cu", "kv_tree_e4m3_64_80.cu",
+                                                      "kv_dense_bf16.cu", "kv_dense_tree_e4m3.cu",
+                                                      "kv_dense_tree_bf16.cu", "kv_tree_e4m3_64_80.cu",
                                                       "kv_tree_e4m3_96_128.cu",
                                                       "kv_tree_bf16_64_80.cu",
                                                       "kv_tree_bf16_96_128.cu", "kv_pages.cu",

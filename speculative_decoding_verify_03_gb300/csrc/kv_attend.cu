@@ -27,7 +27,8 @@ struct MP {
   float *lse;
   int32_t *status;
   int32_t G, Hq, D;
-  int32_t rto, rtp, co, cp, kp;  // rows per item and CTAs, own and prefix; key tokens of a prefix tile
+  int32_t rto, rtp, co, cp, ko, kp;  // rows per item, CTAs and key tokens of a tile, own and prefix
+  const uint32_t *lost_own;          // as plan.lost, of the own items
 };
 
 // LPR lanes per row, four elements each: 16 for heads of 64, else a warp.
@@ -50,6 +51,8 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
   int lost = 0;
   if (P.plan.lost)
     for (int c = threadIdx.x; c < P.cp; c += MG_NT) lost |= P.plan.lost[c];
+  if (P.lost_own)
+    for (int c = threadIdx.x; c < P.co; c += MG_NT) lost |= P.lost_own[c];
   if (__syncthreads_or(bad)) st |= SPEC_ROW_BAD_PAGE;
   if (__syncthreads_or(lost)) st |= SPEC_ROW_WAIT_TIMEOUT;
   if (P.status && blockIdx.x == 0 && threadIdx.x == 0) P.status[b] = st;
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
       np = owner(item * tp + tp - 1, W, C) - c0 + 1;
       lp = static_cast<int64_t>(item + c0) * P.rtp + (k - y * P.rtp);
     }
-    const int to = (own + n + kTile - 1) / kTile, nj = (n * G + P.rto - 1) / P.rto;
+    const int to = (own + n + P.ko - 1) / P.ko, nj = (n * G + P.rto - 1) / P.rto;
     const uint32_t W = P.plan.tiles[w.B], C = min(static_cast<uint32_t>(P.co), W);
     const int y = r / P.rto;
     const uint32_t j = head * nj + y, x = P.plan.tiles[b] + j * to;
@@ -157,16 +160,21 @@ int row_warps(int64_t rows) {
 // rows and up to 3 us from 65 rows on, where the prefix is short.
 constexpr int64_t kDenseRows = 65;
 
+// Query rows of a sequence's key/value head from which a tree's own tokens go to the
+// dense kernel.
+constexpr int64_t kDenseTreeRows = 65;
+static_assert(2 * kMaxDense <= kMaxGrid, "plan: words for the CTAs of both dense launches");
+
 struct Layout {
   int wo, wp;               // row warps of own and prefix items
-  bool dense;
-  int rp, kp;               // rows and key tokens of a prefix tile
+  bool dense, dense_own;
+  int ro, ko, rp, kp;       // rows and key tokens of a tile, own and prefix
   int64_t tiles_o, tiles_p; // key tiles at most
   size_t plan, po, pl, qo, ql, bytes;
 };
 
 // Where each part of the workspace begins; false if the problem is too large.
-bool lay_out(const View &w, int D, int G, Layout &L) {
+bool lay_out(const View &w, int D, int G, bool tree, Layout &L) {
   const auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const int64_t ro = static_cast<int64_t>(w.N) * G, rp = ro * w.B;
   if (rp > (1 << 30)) return false;
@@ -175,14 +183,17 @@ bool lay_out(const View &w, int D, int G, Layout &L) {
   L.dense = w.prefix > 0 && rp >= kDenseRows;
   L.rp = L.dense ? DN_ROWS : 16 * L.wp;
   L.kp = L.dense ? 128 : kTile;
-  const int64_t io = (ro + 16 * L.wo - 1) / (16 * L.wo) * w.Hkv * w.B;
+  L.dense_own = tree && ro >= kDenseTreeRows;
+  L.ro = L.dense_own ? DN_ROWS : 16 * L.wo;
+  L.ko = L.dense_own ? 128 : kTile;
+  const int64_t io = (ro + L.ro - 1) / L.ro * w.Hkv * w.B;
   const int64_t ip = w.prefix && rp ? (rp + L.rp - 1) / L.rp * w.Hkv : 0;
   const int64_t cap = (static_cast<int64_t>(w.max_pages) << w.ps_log2);
-  L.tiles_o = io * ((cap + kTile - 1) / kTile);
+  L.tiles_o = io * ((cap + L.ko - 1) / L.ko);
   L.tiles_p = ip * ((w.prefix + static_cast<int64_t>(L.kp) - 1) / L.kp);
   if (io > INT32_MAX / 2 || ip > INT32_MAX / 2 || L.tiles_o > INT32_MAX || L.tiles_p > INT32_MAX)
     return false;
-  const size_t so = static_cast<size_t>(io + kMaxGrid) * 16 * L.wo;
+  const size_t so = static_cast<size_t>(io + (L.dense_own ? kMaxDense : kMaxGrid)) * L.ro;
   const size_t sp = ip ? static_cast<size_t>(ip + (L.dense ? kMaxDense : kMaxGrid)) * L.rp : 0;
   L.plan = 0;
   L.po = up(sizeof(uint32_t) * (3 * (w.B + 1) + kMaxGrid));
@@ -213,7 +224,7 @@ size_t workspace_of(const spec_kv_cache *cache, const spec_kv_batch *batch, int3
   s.page_table = s.prefix_table = s.kv_len = reinterpret_cast<const int32_t *>(256);
   if (make_view(&c, &s, true, w) != SPEC_OK || n_heads < 1 || n_heads % w.Hkv) return 0;
   if (tree && w.N > SPEC_TREE_MAX) return 0;
-  return lay_out(w, c.head_dim, n_heads / w.Hkv, L) ? L.bytes : 0;
+  return lay_out(w, c.head_dim, n_heads / w.Hkv, tree, L) ? L.bytes : 0;
 }
 
 // mask: of a tree, or null.
@@ -236,7 +247,7 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
   if (tree && (!mask || reinterpret_cast<uintptr_t>(mask) % 4)) return SPEC_ERR_INVALID_ARG;
   const int G = n_heads / P.w.Hkv, D = cache->head_dim;
   Layout L;
-  if (!lay_out(P.w, D, G, L)) return SPEC_ERR_UNSUPPORTED;
+  if (!lay_out(P.w, D, G, tree, L)) return SPEC_ERR_UNSUPPORTED;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 || workspace_bytes < L.bytes)
     return SPEC_ERR_WORKSPACE;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -244,7 +255,8 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
   P.plan.tiles = reinterpret_cast<uint32_t *>(ws + L.plan);
   P.plan.items = P.plan.tiles + P.w.B + 1;
   P.plan.rows = P.plan.items + P.w.B + 1;
-  P.plan.lost = L.dense ? P.plan.rows + P.w.B + 1 : nullptr;
+  uint32_t *lost = P.plan.rows + P.w.B + 1;
+  P.plan.lost = L.dense ? lost : nullptr;
   P.q = static_cast<const __nv_bfloat16 *>(q);
   P.qs0 = q_strides[0], P.qs1 = q_strides[1], P.qs2 = q_strides[2];
   const uintptr_t qbits = qa | static_cast<uintptr_t>((q_strides[0] | q_strides[1] | q_strides[2]) * 2);
@@ -254,7 +266,7 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
   MP m = {};
   m.w = P.w;
   m.plan = P.plan;
-  m.G = G, m.Hq = n_heads, m.D = D, m.rto = 16 * L.wo, m.rtp = L.rp, m.kp = L.kp;
+  m.G = G, m.Hq = n_heads, m.D = D, m.rto = L.ro, m.rtp = L.rp, m.ko = L.ko, m.kp = L.kp;
   m.out = static_cast<__nv_bfloat16 *>(out);
   m.lse = lse;
   m.status = row_status;
@@ -272,11 +284,18 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
   P.prefix = 0;
   P.mask = mask;
   P.mask_words = (P.w.N + 31) / 32;
-  P.qvec = qbits % (L.wo == 1 ? 16 : 4) == 0;
+  P.qvec = qbits % (L.dense_own || L.wo == 1 ? 16 : 4) == 0;
   P.po = reinterpret_cast<float *>(ws + L.po);
   P.pl = reinterpret_cast<float *>(ws + L.pl);
   m.po = P.po, m.pl = P.pl;
-  if (own(P, L.wo, L.tiles_o, &m.co, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (L.dense_own) {
+    m.lost_own = P.plan.lost = lost + kMaxDense;
+    const cudaError_t e = cache->format == SPEC_KV_E4M3 ? dense_tree_e4m3(P, D, L.tiles_o, &m.co, s)
+                                                        : dense_tree_bf16(P, D, L.tiles_o, &m.co, s);
+    if (e != cudaSuccess) return SPEC_ERR_CUDA;
+  } else if (own(P, L.wo, L.tiles_o, &m.co, s) != cudaSuccess) {
+    return SPEC_ERR_CUDA;
+  }
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

@@ -58,17 +58,48 @@ struct DenseCfg {
   static constexpr int Q = 0, K = 2 * OP, V = 4 * OP, OPER = 6 * OP;
 };
 
+// Where a role is among the CTA's tiles: tile tt of nt of an item.  Prefix items
+// are numbered through; own items are of sequence b, key/value head `head`, row
+// tile rt of `per`, with `own` tokens before the step's n.
+struct DenseAt {
+  int tt, nt, item;
+  int b, head, rt, per, own, n;
+};
+
 struct DenseShared {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t sfull[2][2], pfull[2][2];         // per row tile and score buffer
   uint64_t odone[2], ofull[2], drain[2];     // per row tile
   uint64_t consts[DN_RING], qfull[2];
   int exps[2][DN_RING];      // E, F
+  uint32_t hot[DN_RING];     // own items: a byte for each loading warp that took out values
   uint32_t tmem, dead;
-  uint32_t sum[DN_NT / 32];
+  uint32_t sum[DN_NT / 32], sum1[DN_NT / 32];
 };
 
+// The NaN and infinities among elements c .. c + 15 of the values of tokens t0 ..
+// end - 1, which were taken out of the products, added to a row that sees them.
 template <int D, bool E4M3>
+__device__ __noinline__ void add_odd(const View &w, int b, int head, int own, int t0, int end, const int32_t *mask, int c, float *o) {
+  const int lg = w.ps_log2, pm = (1 << lg) - 1;
+  for (int t = max(t0, own); t < end; ++t) {
+    const int j = t - own;
+    if (!(mask[j >> 5] >> (j & 31) & 1)) continue;
+    const int id = w.table[b * w.tstride + (t >> lg)];
+    if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(w.n_pages)) continue;
+    const uint8_t *v = w.v + id * w.vps + ((static_cast<int64_t>(head) << lg) + (t & pm)) * D * (E4M3 ? 1 : 2);
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (E4M3) {
+        if ((v[c + i] & 0x7f) == 0x7f) o[i] += NAN;
+      } else {
+        const uint16_t u = reinterpret_cast<const uint16_t *>(v)[c + i];
+        if ((u & 0x7f80) == 0x7f80) o[i] += __uint_as_float(static_cast<uint32_t>(u) << 16);
+      }
+    }
+  }
+}
+
+template <int D, bool E4M3, bool OWN>
 __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__ SpanParams P) {
   using C = DenseCfg<D>;
   constexpr float BIAS = E4M3 ? 11.0f : 0.0f, SLACK = E4M3 ? 4.0f : 8.0f;
@@ -77,7 +108,9 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   extern __shared__ uint8_t raw[];
   uint8_t *sm = raw + (-s32(raw) & 1023);  // operands: 1024-byte aligned
   DenseShared &S = *reinterpret_cast<DenseShared *>(sm + C::OPER);
-  uint32_t *cum = reinterpret_cast<uint32_t *>(sm + C::OPER + sizeof(DenseShared));  // B + 1
+  // B + 1 words: query rows before each sequence; own items: tiles before it, then items
+  uint32_t *cum = reinterpret_cast<uint32_t *>(sm + C::OPER + sizeof(DenseShared));
+  uint32_t *cum1 = cum + P.w.B + 1;
   const uint32_t base = s32(sm);
 
   const View &w = P.w;
@@ -99,47 +132,113 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   }
   if (warp == 16) tmem_alloc(&S.tmem, 512);
   const int per = (B + DN_NT - 1) / DN_NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  uint32_t a = 0;
+  uint32_t a = 0, a1 = 0;
   for (int b = b0; b < b1; ++b) {
     int own, n;
     row_shape(w, b, own, n);
     cum[b] = a;
-    a += n * G;
+    if constexpr (OWN) {
+      const uint32_t j = (n * G + DN_ROWS - 1) / DN_ROWS * w.Hkv;
+      cum1[b] = a1;
+      a1 += j;
+      a += j * ((own + n + DN_TILE - 1) / DN_TILE);
+    } else {
+      a += n * G;
+    }
   }
-  uint32_t e = a;
+  uint32_t e = a, e1 = a1;
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t t = __shfl_up_sync(~0u, e, o);
-    if (lane >= o) e += t;
+    const uint32_t t = __shfl_up_sync(~0u, e, o), t1 = OWN ? __shfl_up_sync(~0u, e1, o) : 0;
+    if (lane >= o) e += t, e1 += t1;
   }
-  if (lane == 31) S.sum[warp] = e;
+  if (lane == 31) {
+    S.sum[warp] = e;
+    if (OWN) S.sum1[warp] = e1;
+  }
   tc_before();
   __syncthreads();
   tc_after();
-  e -= a;
-  uint32_t rows = 0;
+  e -= a, e1 -= a1;
+  uint32_t rows = 0, items = 0;  // all query rows; own items: all tiles, all items
   for (int v = 0; v < DN_NT / 32; ++v) {
-    if (v < warp) e += S.sum[v];
+    if (v < warp) {
+      e += S.sum[v];
+      if (OWN) e1 += S.sum1[v];
+    }
     rows += S.sum[v];
+    if (OWN) items += S.sum1[v];
   }
+  uint32_t *out0 = OWN ? P.plan.tiles : P.plan.rows;
   for (int b = b0; b < b1; ++b) {
     cum[b] += e;
-    if (blockIdx.x == 0) P.plan.rows[b] = cum[b];
+    if (OWN) cum1[b] += e1;
+    if (blockIdx.x == 0) {
+      out0[b] = cum[b];
+      if (OWN) P.plan.items[b] = cum1[b];
+    }
   }
   if (tid == 0) {
     cum[B] = rows;
-    if (blockIdx.x == 0) P.plan.rows[B] = rows;
+    if (OWN) cum1[B] = items;
+    if (blockIdx.x == 0) {
+      out0[B] = rows;
+      if (OWN) P.plan.items[B] = items;
+    }
   }
   __syncthreads();
   const uint32_t tmem = S.tmem;
   volatile uint32_t *dead = &S.dead;
-  const int nt = (w.prefix + DN_TILE - 1) / DN_TILE;      // key tiles of an item
-  const int nj = (rows + DN_ROWS - 1) / DN_ROWS;          // items of a key/value head
-  const uint32_t W = static_cast<uint32_t>(nt) * nj * w.Hkv, ctas = min(gridDim.x, W);
+  const int nj = (rows + DN_ROWS - 1) / DN_ROWS;          // prefix: items of a key/value head
+  const uint32_t W = OWN ? rows : static_cast<uint32_t>((w.prefix + DN_TILE - 1) / DN_TILE) * nj * w.Hkv;
+  const uint32_t ctas = min(gridDim.x, W);
   const bool idle = blockIdx.x >= ctas;
   const uint32_t lo = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(W) * blockIdx.x / ctas);
   const uint32_t hi = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(W) * (blockIdx.x + 1) / ctas);
   const int tiles = static_cast<int>(hi - lo);
-  const int item0 = idle ? 0 : lo / nt, first0 = idle ? 0 : lo - item0 * nt;
+  // --- the first tile, and the next one
+  auto shape = [&](DenseAt &x) {
+    row_shape(w, x.b, x.own, x.n);
+    x.per = (x.n * G + DN_ROWS - 1) / DN_ROWS;
+    x.nt = (x.own + x.n + DN_TILE - 1) / DN_TILE;
+  };
+  auto begin = [&]() {
+    DenseAt x = {};
+    x.nt = 1;
+    if (idle) return x;
+    if constexpr (OWN) {
+      int r = B;
+      while (r - x.b > 1) {
+        const int m = (x.b + r) >> 1;
+        if (cum[m] <= lo) x.b = m;
+        else r = m;
+      }
+      shape(x);
+      const uint32_t y = lo - cum[x.b], j = y / x.nt;
+      x.head = j / x.per;
+      x.rt = j - x.head * x.per;
+      x.tt = y - j * x.nt;
+    } else {
+      x.nt = (w.prefix + DN_TILE - 1) / DN_TILE;
+      x.item = lo / x.nt;
+      x.tt = lo - x.item * x.nt;
+    }
+    return x;
+  };
+  auto step = [&](DenseAt &x) {  // there is a next tile
+    if (++x.tt < x.nt) return;
+    x.tt = 0;
+    if constexpr (OWN) {
+      if (++x.rt < x.per) return;
+      x.rt = 0;
+      if (++x.head < w.Hkv) return;
+      x.head = 0;
+      do ++x.b;
+      while (x.b + 1 < B && cum[x.b + 1] == cum[x.b]);
+      shape(x);
+    } else {
+      ++x.item;
+    }
+  };
 
   // All products that this thread issued are done, also where a wait gave up:
   // TMEM goes back behind this.
@@ -158,17 +257,25 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     const uint32_t oc = tmem + lanes + 256 + half * 128;
     const uint32_t wb = base + C::Q + half * C::OP + (warp & 3) * 32 * 128;  // the warp's query rows
     const int r = tid;  // row of the item
-    int item = item0, tt = first0;
+    DenseAt x = begin();
     float M = kNone, l = 0.0f, qc = 0.0f;
     float kt = 0.0f, F = 0.0f, invF = 1.0f;  // of the tile
     bool fresh = true;
+    int node = -1;  // own items: the row's place in the step
+    int begun = 0;  // own items: the CTA's first tile of the item
     int g = 0;  // items
     for (int u = 0; u < 2 * tiles; ++u) {
       const int t = u >> 1;  // half u & 1 of tile t
       if (fresh) {  // the row's query; the products with the item before are done
-        const uint32_t row = item % nj * DN_ROWS + r;
+        const uint32_t row = (OWN ? x.rt : x.item % nj) * DN_ROWS + r;
         int64_t off = -1;
-        if (row < rows) {
+        if (OWN) {
+          node = -1;
+          if (row < static_cast<uint32_t>(x.n * G)) {
+            node = row / G;
+            off = x.b * P.qs0 + node * P.qs1 + (x.head * G + static_cast<int>(row) - node * G) * P.qs2;
+          }
+        } else if (row < rows) {
           int b = 0, h = B;
           while (h - b > 1) {
             const int m = (b + h) >> 1;
@@ -176,7 +283,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
             else h = m;
           }
           const int y = row - cum[b], i = y / G;
-          off = b * P.qs0 + i * P.qs1 + (item / nj * G + y - i * G) * P.qs2;
+          off = b * P.qs0 + i * P.qs1 + (x.item / nj * G + y - i * G) * P.qs2;
         }
         // into shared memory by the warp's 32 rows together, neighbouring lanes
         // neighbouring chunks; then a row by its own thread
@@ -187,11 +294,11 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         };
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-          const int x = lane + 32 * k, y = x / CH;
+          const int z = lane + 32 * k, y = z / CH;
           const int64_t o = __shfl_sync(~0u, off, y);
           v[k] = make_uint4(0, 0, 0, 0);
           if (o >= 0) {
-            const __nv_bfloat16 *src = P.q + o + 8 * (x - y * CH);
+            const __nv_bfloat16 *src = P.q + o + 8 * (z - y * CH);
             if (P.qvec) {
               v[k] = __ldg(reinterpret_cast<const uint4 *>(src));
             } else {
@@ -202,8 +309,8 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         }
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-          const int x = lane + 32 * k, y = x / CH;
-          sts128(at(y, x - y * CH), v[k]);
+          const int z = lane + 32 * k, y = z / CH;
+          sts128(at(y, z - y * CH), v[k]);
         }
         qc = P.c;
         if constexpr (E4M3) {
@@ -234,6 +341,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         __syncwarp();
         if (lane == 0) bar_arrive(s32(&S.qfull[half]));
         M = kNone, l = 0.0f;
+        begun = t;
       }
       if (!(u & 1)) {
         kt = qc;
@@ -252,12 +360,22 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
 #pragma unroll
       for (int c = 0; c < 64; c += 16) tmem_ld16(sc + c, s + c);
       tmem_wait_ld(s, 64);
-      const int n = w.prefix - tt * DN_TILE - (u & 1) * 64;  // tokens from here on
+      // tokens from here on that all rows see
+      const int n = (OWN ? x.own : w.prefix) - x.tt * DN_TILE - (u & 1) * 64;
       float ks = kt;  // still to be multiplied by
       if (n < 64) {   // masked behind the multiplication: a factor of 0 would make NaN of -inf
         ks = 1.0f;
+        if constexpr (OWN) {
+          uint64_t see = 0;
+          if (node >= 0)
+            see = seen_nodes(P.mask + (static_cast<int64_t>(x.b) * w.N + node) * P.mask_words, P.mask_words, x.n, -n);
+          const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) s[c] = c >= n ? -INFINITY : s[c] * kt;
+          for (int c = 0; c < 64; ++c) s[c] = (c < 32 ? see0 : see1) >> (c & 31) & 1 ? s[c] * kt : -INFINITY;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) s[c] = c >= n ? -INFINITY : s[c] * kt;
+        }
       }
       float m2[2] = {s[0], s[1]};
 #pragma unroll
@@ -303,14 +421,21 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       __syncwarp();
       if (lane == 0) bar_arrive(s32(&S.pfull[half][u & 1]));
 
-      const bool last = (u & 1) && (tt + 1 == nt || t + 1 == tiles);
+      const bool last = (u & 1) && (x.tt + 1 == x.nt || t + 1 == tiles);
       if (last) {
-        const int64_t at = static_cast<int64_t>(item + blockIdx.x) * DN_ROWS + r;
-        const bool there = static_cast<uint32_t>(item % nj * DN_ROWS + r) < rows;
+        const uint32_t slot = (OWN ? cum1[x.b] + x.head * x.per + x.rt : x.item) + blockIdx.x;
+        const int64_t at = static_cast<int64_t>(slot) * DN_ROWS + r;
+        const bool there = OWN ? node >= 0 : static_cast<uint32_t>(x.item % nj * DN_ROWS + r) < rows;
         const float f = l == 0.0f ? 0.0f : 1.0f / l;
         if (there) P.pl[at] = l == 0.0f ? -INFINITY : M - (BIAS - SUM_LOG) + log2f(l);
         bar_wait(s32(&S.ofull[half]), g++ & 1, dead);
         tc_after();
+        int hot0 = t + 1;  // own items: the first tile that values were taken out of
+        if constexpr (OWN) {
+          const volatile uint32_t *hot = S.hot;
+          for (int k = t; k >= begun && (x.tt - (t - k) + 1) * DN_TILE > x.own; --k)
+            if (hot[k % DN_RING]) hot0 = k;
+        }
         // rows leave through the shared memory of the item's queries, 16 columns
         // at a time in two buffers, so that a store covers whole sectors
         float *dst = P.po + (at - lane) * D + (lane & 3) * 4;
@@ -321,6 +446,14 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           float o[16];
           tmem_ld16(oc + c, o);
           tmem_wait_ld(o, 16);
+          if (OWN && hot0 <= t && node >= 0) {  // rare: to the rows that see them
+            const int t0 = (x.tt - (t - hot0)) * DN_TILE;
+            float more[16] = {};
+            add_odd<D, E4M3>(w, x.b, x.head, x.own, t0, min(x.own + x.n, (x.tt + 1) * DN_TILE),
+                             P.mask + (static_cast<int64_t>(x.b) * w.N + node) * P.mask_words, c, more);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] += more[i];
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             sts128(buf + lane * 64 + ((i ^ lane >> 1) & 3) * 16,
@@ -338,7 +471,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         tc_before();
       }
       fresh = last;
-      if ((u & 1) && ++tt == nt) tt = 0, ++item;
+      if ((u & 1) && t + 1 < tiles) step(x);
     }
   } else if (warp < 16) {
     regs_to<DN_LOAD, DN_REGS>();
@@ -350,45 +483,53 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     const uint32_t dst0 = base + (vs ? C::V : C::K);
     uint64_t *full = vs ? S.vfull : S.kfull, *empty = vs ? S.vempty : S.kempty;
     const int lg = w.ps_log2, pm = (1 << lg) - 1;
-    int item = item0, tt = first0;
+    DenseAt x = begin();
+    // own items: the tile holds tokens that not all rows see; then no NaN or infinity
+    // of their values goes into a product, where a weight of zero would spread it
+    auto banded = [&]() { return OWN && vs && (x.tt + 1) * DN_TILE > x.own; };
+    // tokens of the item's list and the pages that hold them
+    auto held = [&]() { return OWN ? x.own + x.n : w.prefix; };
+    auto list = [&]() { return OWN ? w.table + x.b * w.tstride : w.ptable; };
+    auto head_of = [&]() { return static_cast<uint32_t>(OWN ? x.head : x.item / nj); };
     if constexpr (E4M3) {
       constexpr int CPR = D / 16;                     // 16-byte chunks of a row
       constexpr int PASS = DN_TILE * CPR / DN_FETCH;  // of a tile, per thread
       static_assert(DN_TILE * CPR % DN_FETCH == 0, "chunks");
       int id[PASS], ide = -1;  // page ids of the tile to be fetched next
-      auto pages = [&](int tile) {
-        const int t0 = tile * DN_TILE;
+      auto pages = [&]() {
+        const int t0 = x.tt * DN_TILE, end = held();
+        const int32_t *ids = list();
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
           const int tok = t0 + (p + i * DN_FETCH) / CPR;
-          id[i] = tok < w.prefix ? ldg_now(w.ptable + (tok >> lg)) : -1;
+          id[i] = tok < end ? ldg_now(ids + (tok >> lg)) : -1;
         }
-        ide = t0 + 4 * lane < w.prefix ? ldg_now(w.ptable + (t0 + 4 * lane >> lg)) : -1;
+        ide = t0 + 4 * lane < end ? ldg_now(ids + (t0 + 4 * lane >> lg)) : -1;
       };
       uint4 q[PASS] = {};
       uint32_t ex = 0;  // exponents of the lane's four tokens, the first `live` of them there
       int live = 0;
       // A chunk without a page is read from page 0 and put to zero in store(): the
       // loads stand in a row without branches.
-      auto fetch = [&](int it, int tile) {
+      auto fetch = [&]() {
         if (w.n_pages == 0) return;
-        const uint32_t row0 = static_cast<uint32_t>(it / nj) << lg;
-        const int t0 = tile * DN_TILE;
+        const uint32_t row0 = head_of() << lg;
+        const int t0 = x.tt * DN_TILE;
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
-          const int x = p + i * DN_FETCH, row = x / CPR;
+          const int z = p + i * DN_FETCH, row = z / CPR;
           const uint32_t pg = static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(w.n_pages) ? id[i] : 0;
-          q[i] = ldg_now16(src + pg * stride + (row0 + (t0 + row & pm)) * D + (x - row * CPR) * 16);
+          q[i] = ldg_now16(src + pg * stride + (row0 + (t0 + row & pm)) * D + (z - row * CPR) * 16);
         }
         // (masked when it is used: nothing here waits for a load)
-        live = static_cast<uint32_t>(ide) < static_cast<uint32_t>(w.n_pages) ? min(max(w.prefix - t0 - 4 * lane, 0), 4) : 0;
-        ex = ldg_now32((vs ? w.ve : w.ke) + ((static_cast<int64_t>(live ? ide : 0) * w.Hkv + it / nj) << lg) +
+        live = static_cast<uint32_t>(ide) < static_cast<uint32_t>(w.n_pages) ? min(max(held() - t0 - 4 * lane, 0), 4) : 0;
+        ex = ldg_now32((vs ? w.ve : w.ke) + ((static_cast<int64_t>(live ? ide : 0) * w.Hkv + head_of()) << lg) +
                        (t0 + 4 * lane & pm));
       };
       auto store = [&](uint32_t dst, int E) {
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
-          const int x = p + i * DN_FETCH, row = x / CPR, f = 2 * (x - row * CPR);
+          const int z = p + i * DN_FETCH, row = z / CPR, f = 2 * (z - row * CPR);
           const int e = static_cast<int8_t>(__shfl_sync(~0u, ex, row >> 2) >> 8 * (row & 3));
           const float one = pow2i(max(e - E, -126));  // e - E <= 7
           const uint32_t two = pack<true>(one, one), is = e == -128 ? 0u : ~0u;
@@ -408,7 +549,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         }
       };
       // the loads of a tile are issued when the tile before is stored
-      if (tiles > 0) pages(tt), fetch(item, tt);
+      if (tiles > 0) pages(), fetch();
       for (int t = 0; t < tiles; ++t) {
         if (live < 4) {  // -128 where there is no token
           const uint32_t in = (1u << 8 * live) - 1;
@@ -422,32 +563,81 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           S.exps[vs][t % DN_RING] = E;
           bar_arrive(s32(&S.consts[t % DN_RING]));
         }
-        if (++tt == nt) tt = 0, ++item;
-        if (t + 1 < tiles) pages(tt);
+        if constexpr (OWN) {
+          if (vs) {
+            bool odd = false;
+            if (banded()) {
+              const int first = x.own - x.tt * DN_TILE;
+#pragma unroll
+              for (int i = 0; i < PASS; ++i) {
+                uint32_t *u = reinterpret_cast<uint32_t *>(&q[i]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  uint32_t m = (((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 where the byte is NaN
+                  if ((p + i * DN_FETCH) / CPR < first) m = 0;
+                  odd |= m != 0;
+                  u[k] &= ~(m * 0xffu);
+                }
+              }
+            }
+            odd = __any_sync(~0u, odd);
+            if (lane == 0) reinterpret_cast<volatile uint8_t *>(&S.hot[t % DN_RING])[warp & 3] = odd;
+          }
+        }
+        if (t + 1 < tiles) step(x), pages();
         if (t >= 2) bar_wait(s32(empty + (t & 1)), (t >> 1) - 1 & 1, dead);
         store(dst0 + (t & 1) * C::OP, E);
         fence_async();
         __syncwarp();
         if (lane == 0) bar_arrive(s32(full + (t & 1)));
-        if (t + 1 < tiles) fetch(item, tt);
+        if (t + 1 < tiles) fetch();
       }
     } else {
       constexpr int CPR = D / 8;
       for (int t = 0; t < tiles; ++t) {
         if (t >= 2) bar_wait(s32(empty + (t & 1)), (t >> 1) - 1 & 1, dead);
-        const uint32_t row0 = static_cast<uint32_t>(item / nj) << lg, dst = dst0 + (t & 1) * C::OP;
+        const uint32_t row0 = head_of() << lg, dst = dst0 + (t & 1) * C::OP;
+        const int32_t *ids = list();
+        const int end = held();
+        if (OWN && banded()) {  // through registers
+          const int first = x.own - x.tt * DN_TILE;
+          bool odd = false;
+#pragma unroll 4
+          for (int i = 0; i < CPR; ++i) {
+            const int z = p + i * DN_FETCH, row = z / CPR, f = z - row * CPR, tok = x.tt * DN_TILE + row;
+            const int id = tok < end ? __ldg(ids + (tok >> lg)) : -1;
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages))
+              q = __ldg(reinterpret_cast<const uint4 *>(src + id * stride + ((row0 + (tok & pm)) * D + f * 8) * 2));
+            uint32_t *u = reinterpret_cast<uint32_t *>(&q);
 #pragma unroll
-        for (int i = 0; i < CPR; ++i) {
-          const int x = p + i * DN_FETCH, row = x / CPR, f = x - row * CPR, tok = tt * DN_TILE + row;
-          const int id = tok < w.prefix ? __ldg(w.ptable + (tok >> lg)) : -1;
-          const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages);
-          const uint32_t at = ((row0 + (tok & pm)) * D + f * 8) * 2;
-          cp16(dst + (f >> 3) * (DN_TILE * 128) + row * 128 + (((f ^ row) & 7) << 4),
-               ok ? src + id * stride + at : src, ok);
+            for (int k = 0; k < 4; ++k) {
+              uint32_t m = (((u[k] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u) >> 15;  // 1 where the exponent is full
+              if (row < first) m = 0;
+              odd |= m != 0;
+              u[k] &= ~(m * 0xffffu);
+            }
+            sts128(dst + (f >> 3) * (DN_TILE * 128) + row * 128 + (((f ^ row) & 7) << 4), q);
+          }
+          odd = __any_sync(~0u, odd);
+          if (lane == 0) reinterpret_cast<volatile uint8_t *>(&S.hot[t % DN_RING])[warp & 3] = odd;
+          fence_async();
+          bar_arrive(s32(full + (t & 1)));
+        } else {
+#pragma unroll
+          for (int i = 0; i < CPR; ++i) {
+            const int z = p + i * DN_FETCH, row = z / CPR, f = z - row * CPR, tok = x.tt * DN_TILE + row;
+            const int id = tok < end ? __ldg(ids + (tok >> lg)) : -1;
+            const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages);
+            const uint32_t at = ((row0 + (tok & pm)) * D + f * 8) * 2;
+            cp16(dst + (f >> 3) * (DN_TILE * 128) + row * 128 + (((f ^ row) & 7) << 4),
+                 ok ? src + id * stride + at : src, ok);
+          }
+          if (OWN && vs && lane == 0) reinterpret_cast<volatile uint8_t *>(&S.hot[t % DN_RING])[warp & 3] = 0;
+          // arrives when this thread's copies are in
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s32(full + (t & 1))) : "memory");
         }
-        // arrives when this thread's copies are in
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(s32(full + (t & 1))) : "memory");
-        if (++tt == nt) tt = 0, ++item;
+        if (t + 1 < tiles) step(x);
       }
       cp_wait<0>();
     }
@@ -460,7 +650,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     const int half = __shfl_sync(~0u, warp, 0) - 16;
     const uint32_t base = __shfl_sync(~0u, s32(sm), 0), tmem = __shfl_sync(~0u, S.tmem, 0);
     const int tiles = __shfl_sync(~0u, static_cast<int>(hi - lo), 0);
-    const int nt = __shfl_sync(~0u, (w.prefix + DN_TILE - 1) / DN_TILE, 0);
+    DenseAt x = begin();
     constexpr uint32_t sdesc = mma_desc(E4M3, 128, 64, false, false);
     constexpr uint32_t odesc = mma_desc(E4M3, 128, D, false, true);
     const uint64_t qd = smem_desc(base + C::Q + half * C::OP, 16, 1024), kd = smem_desc(base + C::K, 16, 1024);
@@ -490,9 +680,9 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       __syncwarp();
     };
     // ... and its weighted values.
-    auto values = [&](int u, int tt) {
+    auto values = [&](int u, int tt, bool end) {
       const int t = u >> 1, st = t & 1;
-      const bool last = (u & 1) && (tt + 1 == nt || t + 1 == tiles);
+      const bool last = (u & 1) && end;
       // (parities tell one phase from the next only: no phase is skipped)
       if (last) bar_wait(s32(&S.odone[half]), u - 1 & 1, dead);
       if (!(u & 1)) bar_wait(s32(&S.vfull[st]), t >> 1 & 1, dead);
@@ -511,17 +701,17 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       }
       __syncwarp();
     };
-    int tt = __shfl_sync(~0u, first0, 0);
     for (int t = 0; t < tiles; ++t) {
       // the next half tile's scores before these weights, except behind an item's
       // last, whose output has to be out before the next item's queries are in
-      const bool last = tt + 1 == nt || t + 1 == tiles;
+      const int tt = __shfl_sync(~0u, x.tt, 0);
+      const bool last = __shfl_sync(~0u, x.tt + 1 == x.nt || t + 1 == tiles, 0);
       if (t == 0 || tt == 0) scores(2 * t, tt);
       scores(2 * t + 1, tt);
-      values(2 * t, tt);
+      values(2 * t, tt, last);
       if (!last) scores(2 * t + 2, tt + 1);
-      values(2 * t + 1, tt);
-      if (++tt == nt) tt = 0;
+      values(2 * t + 1, tt, last);
+      if (t + 1 < tiles) step(x);
     }
     if (elected()) drained(half);
     __syncwarp();
@@ -534,21 +724,21 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   if (tid == 0) P.plan.lost[blockIdx.x] = S.dead;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool OWN = false>
 cudaError_t dense_go(const SpanParams &p, int64_t tiles, int *grid, cudaStream_t s) {
   constexpr int fixed = 1024 + DenseCfg<D>::OPER + sizeof(DenseShared);
-  static_assert(fixed + 4 * (kMaxB + 1) <= 232448, "shared memory");
-  auto *f = dense_kernel<D, E4M3>;
+  constexpr int smem = fixed + (OWN ? 8 : 4) * (kMaxB + 1);
+  static_assert(smem <= 232448, "shared memory");
+  auto *f = dense_kernel<D, E4M3, OWN>;
   static Slots slots;
   int sms = 0, occ = 0;
-  constexpr int smem = fixed + 4 * (kMaxB + 1);
   const cudaError_t e = slots.get(reinterpret_cast<const void *>(f), DN_NT, smem, smem, &sms, &occ);
   if (e != cudaSuccess) return e;
   int64_t n = sms < kMaxDense ? sms : kMaxDense;
   if (n > tiles) n = tiles;
   if (n < 1) n = 1;
   *grid = static_cast<int>(n);
-  f<<<*grid, DN_NT, fixed + 4 * (kMaxB + 1), s>>>(p);
+  f<<<*grid, DN_NT, smem, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -109,6 +109,9 @@ constexpr int kMaxDense = 152;  // CTAs of the dense kernel at most: one on each
 static_assert(kMaxDense <= kMaxGrid, "plan");
 cudaError_t dense_e4m3(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
 cudaError_t dense_bf16(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
+// The same over the own tokens of trees.
+cudaError_t dense_tree_e4m3(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
+cudaError_t dense_tree_bf16(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
 
 // The CTA that works on tile x of W (C <= W CTAs): the largest c with W c / C <= x.
 __host__ __device__ __forceinline__ uint32_t owner(uint32_t x, uint32_t W, uint32_t C) {
