@@ -9,7 +9,8 @@
 //
 // Tables: one cluster of CTAs does a whole call, so that counts, sums and
 // assignments can wait for one another.  What each row needs is summed over the
-// rows by every CTA for itself; then the counts are read, 32 a thread, and the
+// rows by every CTA for itself; where that is little the first CTA goes on alone,
+// without the cluster's barriers.  Then the counts are read, 32 a thread, and the
 // free pages numbered by sums over the warp, the CTA and the cluster, in the
 // order of the page ids: page of number k goes to the row in whose sum k falls.
 // Nothing depends on the order of atomics: they add to counts, or or bits.
@@ -18,6 +19,7 @@
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <utility>
 
 #include "kv_common.cuh"
 #include "spec_tree.h"
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(CY_NT) copy_kernel(const __grid_constant__ YP 
 constexpr int TB_NT = 1024;   // threads of a CTA
 constexpr int TB_CTAS = 8;    // of the cluster
 constexpr int TB_EACH = 32;   // counts of a thread and round: 8 loads of 4
-constexpr int64_t TB_ROUND = static_cast<int64_t>(TB_CTAS) * TB_NT * TB_EACH;
+constexpr uint32_t TB_ALONE = 4096;  // entries that one CTA sees to alone
 
 struct Pool {
   int32_t *refs, *table, *held;
@@ -165,45 +167,60 @@ struct Pool {
 };
 
 struct TableShared {
+  uint16_t list[TB_NT * TB_EACH];  // free pages of the CTA's part of a round
+  unsigned long long warp2[TB_NT / 32];
   uint32_t warp[TB_NT / 32];
   uint32_t found[2];  // free pages of this CTA's part of a round, by the round's parity
 };
 
+// Who works on the tables: the whole cluster, or its first CTA.
+struct Team {
+  unsigned rank, ctas;
+  __device__ void sync() const {
+    if (ctas > 1) cg::this_cluster().sync();
+    else __syncthreads();
+  }
+  __device__ int64_t round() const { return static_cast<int64_t>(ctas) * TB_NT * TB_EACH; }
+};
+
 // Exclusive sum over the CTA's threads; *all: the whole sum.  Barriers on both sides.
-__device__ uint32_t cta_sum(uint32_t x, uint32_t *warps, uint32_t *all) {
+template <class T>
+__device__ T cta_sum(T x, T *warps, T *all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t e = x;
+  T e = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t t = __shfl_up_sync(~0u, e, o);
+    const T t = __shfl_up_sync(~0u, e, o);
     if (lane >= o) e += t;
   }
   __syncthreads();
   if (lane == 31) warps[warp] = e;
   __syncthreads();
-  const uint32_t mine = warps[lane];
-  uint32_t s = mine;
+  const T mine = warps[lane];
+  T s = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t t = __shfl_up_sync(~0u, s, o);
+    const T t = __shfl_up_sync(~0u, s, o);
     if (lane >= o) s += t;
   }
   *all = __shfl_sync(~0u, s, 31);
   return e - x + __shfl_sync(~0u, s - mine, warp);
 }
 
-// cum[0 .. n]: sums of cum[0 .. n) before each entry, by the whole CTA.
-__device__ void sum_up(uint32_t *cum, int n, uint32_t *warps) {
+// a[0 .. n], b[0 .. n]: sums of a[0 .. n), b[0 .. n) before each entry, by the whole
+// CTA (both in one word of 64 bits: no sum reaches 2^32).
+__device__ void sum_up(uint32_t *a, uint32_t *b, int n, unsigned long long *warps) {
   const int per = (n + TB_NT - 1) / TB_NT, i0 = min(static_cast<int>(threadIdx.x) * per, n), i1 = min(i0 + per, n);
-  uint32_t mine = 0, all;
-  for (int i = i0; i < i1; ++i) mine += cum[i];
-  uint32_t at = cta_sum(mine, warps, &all);
+  unsigned long long mine = 0, all;
+  for (int i = i0; i < i1; ++i) mine += a[i] | static_cast<unsigned long long>(b[i]) << 32;
+  unsigned long long at = cta_sum(mine, warps, &all);
   for (int i = i0; i < i1; ++i) {
-    const uint32_t x = cum[i];
-    cum[i] = at;
-    at += x;
+    const uint32_t x = a[i], y = b[i];
+    a[i] = static_cast<uint32_t>(at);
+    b[i] = static_cast<uint32_t>(at >> 32);
+    at += x | static_cast<unsigned long long>(y) << 32;
   }
-  if (threadIdx.x == 0) cum[n] = all;
+  if (threadIdx.x == 0) a[n] = static_cast<uint32_t>(all), b[n] = static_cast<uint32_t>(all >> 32);
   __syncthreads();
 }
 
@@ -248,42 +265,48 @@ __device__ uint32_t free_bits(const Pool &P, int64_t at, unsigned rank) {
 // Takes the lowest free pages for the rows of cum (n + 1 sums of what they need):
 // give(row, k, page) for the k-th page of each row that is served, that is whose
 // sum is within what the pool has.  Returns the number of free pages, or any
-// number from the rows' sum on.  All CTAs of the cluster call it, after a cluster
+// number from the rows' sum on.  All CTAs of the team call it, after a team's
 // barrier behind the last change of a count.
 template <class F>
-__device__ uint32_t take_pages(const Pool &P, const uint32_t *cum, int n, TableShared &S, F give) {
-  cg::cluster_group cl = cg::this_cluster();
-  const unsigned rank = cl.block_rank();
+__device__ uint32_t take_pages(const Pool &P, const uint32_t *cum, int n, const Team &team, TableShared &S, F give) {
+  const unsigned rank = team.rank;
+  const int64_t round = team.round();
   const uint32_t total = cum[n];
   if (total == 0) return 0;
-  const int rounds = static_cast<int>((P.n_pages + TB_ROUND - 1) / TB_ROUND);
+  const int rounds = static_cast<int>((P.n_pages + round - 1) / round);
   const int lane = threadIdx.x & 31;
-  uint32_t bits = 0, at0 = 0, base = 0;
+  uint32_t bits = 0, at0 = 0, base = 0, all = 0;
   int turn = 0;
   // round r: the free pages of the thread, their number before the thread's warp in
-  // this CTA, and before this CTA in the round; returns that of the whole round
-  auto count = [&](int r) {
-    bits = free_bits(P, r * TB_ROUND, rank);
-    uint32_t all, here = 0;
-    at0 = __shfl_sync(~0u, cta_sum(__popc(bits), S.warp, &all), 0);
+  // this CTA, of this CTA, and before it in the round; returns that of the whole round
+  auto count = [&](int r) -> uint32_t {
+    bits = free_bits(P, r * round, rank);
+    uint32_t here = 0;
+    at0 = __shfl_sync(~0u, cta_sum<uint32_t>(__popc(bits), S.warp, &all), 0);
+    base = 0;
+    if (team.ctas == 1) return all;
+    cg::cluster_group cl = cg::this_cluster();
     uint32_t *slot = &S.found[turn++ & 1];
     if (threadIdx.x == 0) *slot = all;
     cl.sync();
-    base = 0;
+    uint32_t x[TB_CTAS];
+#pragma unroll
+    for (unsigned c = 0; c < TB_CTAS; ++c) x[c] = *cl.map_shared_rank(slot, c);
+#pragma unroll
     for (unsigned c = 0; c < TB_CTAS; ++c) {
-      const uint32_t x = *cl.map_shared_rank(slot, c);
-      if (c < rank) base += x;
-      here += x;
+      if (c < rank) base += x[c];
+      here += x[c];
     }
     return here;
   };
   uint32_t found = 0;
-  for (int r = 0; r < rounds && found < total; ++r) found += count(r);
+  int counted = 0;
+  for (; counted < rounds && found < total; ++counted) found += count(counted);
   // rows up to the last one whose sum the pool has
   const uint32_t limit = found >= total ? total : cum[before(cum, n, found)];
   uint32_t sum = 0;
   for (int r = 0; r < rounds && sum < limit; ++r) {
-    const uint32_t here = rounds == 1 ? found : count(r);  // one round: as counted
+    const uint32_t here = counted == 1 ? found : count(r);  // one round: as counted
     // a warp's pages in the order of u, lane, k: sums over the lanes for each u,
     // four of them in a word (32 x 4 counts fit eight bits)
     uint32_t lo = 0, hi = 0;
@@ -300,22 +323,25 @@ __device__ uint32_t take_pages(const Pool &P, const uint32_t *cum, int n, TableS
     }
     const uint32_t al = __shfl_sync(~0u, el, 31), ah = __shfl_sync(~0u, eh, 31);
     el -= lo, eh -= hi;
-    uint32_t at = sum + base + at0;  // of the warp
-    const int64_t i0 = r * TB_ROUND + (static_cast<int64_t>(rank) * (TB_NT / 32) + (threadIdx.x >> 5)) * 1024 + 4 * lane;
-    int row = -1;
+    // the CTA's free pages in their order, as numbers within its part of the round,
+    // so that the threads can take them side by side
+    const uint32_t first = sum + base, mine = first < limit ? min(limit - first, all) : 0;  // of the CTA
+    uint32_t at = at0;  // of the warp
 #pragma unroll 1
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < 8 && at < mine; ++u) {
       uint32_t k = at + ((u < 4 ? el : eh) >> (8 * (u & 3)) & 255);
-      uint32_t m = bits >> (4 * u) & 15;
-      while (m && k < limit) {
-        const int bit = __ffs(m) - 1;
-        m &= m - 1;
-        if (row < 0 || k >= cum[row + 1]) row = before(cum, n, k);
-        give(row, k - cum[row], static_cast<int32_t>(i0 + 128 * u + bit));
-        ++k;
-      }
+      for (uint32_t m = bits >> (4 * u) & 15; m && k < mine; m &= m - 1, ++k)
+        S.list[k] = static_cast<uint16_t>((threadIdx.x >> 5) * 1024 + 128 * u + 4 * lane + __ffs(m) - 1);
       at += (u < 4 ? al : ah) >> (8 * (u & 3)) & 255;
     }
+    __syncthreads();
+    const int64_t i0 = r * round + static_cast<int64_t>(rank) * TB_NT * TB_EACH;
+    int row = -1;
+    for (uint32_t k = threadIdx.x; k < mine; k += TB_NT) {
+      if (row < 0 || first + k >= cum[row + 1]) row = before(cum, n, first + k);
+      give(row, first + k - cum[row], static_cast<int32_t>(i0 + S.list[k]));
+    }
+    __syncthreads();
     sum += here;
   }
   return found;
@@ -337,53 +363,74 @@ __device__ __forceinline__ int wanted(const Pool &P, int len, int n, int held, i
 }
 
 __global__ void __cluster_dims__(TB_CTAS, 1, 1) __launch_bounds__(TB_NT) resize_kernel(const __grid_constant__ RP R) {
-  extern __shared__ uint32_t cum[];  // B + 1 pages to take, B + 1 pages to give back
-  __shared__ TableShared S;
+  extern __shared__ __align__(16) uint8_t tm[];
+  TableShared &S = *reinterpret_cast<TableShared *>(tm);
+  uint32_t *cum = reinterpret_cast<uint32_t *>(tm + sizeof(TableShared));  // B + 1 pages to take, B + 1 pages to give back, B held
   const Pool &P = R.p;
-  cg::cluster_group cl = cg::this_cluster();
-  const unsigned rank = cl.block_rank();
+  Team team = {cg::this_cluster().block_rank(), TB_CTAS};
   const int B = P.B, tid = threadIdx.x;
   uint32_t *gone = cum + B + 1;
+  int32_t *has = reinterpret_cast<int32_t *>(gone + B + 1);
   for (int b = tid; b < B; b += TB_NT) {
     const int held = P.held[b];
     int st;
     const int want = wanted(P, R.len[b], R.n, held, &st);
+    has[b] = held;
     cum[b] = want > held ? want - held : 0;
     gone[b] = want >= 0 && want < held ? held - want : 0;
-    if (rank == 0 && R.status) R.status[b] = st;
+    if (team.rank == 0 && R.status) R.status[b] = st;
   }
+  // the status words are written; what is held and the lengths have been read by all,
+  // so that all come to the same sums whatever one of them does behind the wait
+  auto read = cg::this_cluster().barrier_arrive();
   __syncthreads();
-  sum_up(cum, B, S.warp);
-  sum_up(gone, B, S.warp);
+  sum_up(cum, gone, B, S.warp2);
+  cg::this_cluster().barrier_wait(std::move(read));
+  if (!(cum[B] | gone[B])) return;
+  if (cum[B] + gone[B] <= TB_ALONE) {
+    if (team.rank) return;
+    team.ctas = 1;
+  }
   if (gone[B]) {
-    cl.sync();  // the status words are written
     const uint32_t np = static_cast<uint32_t>(P.n_pages);
     int row = -1;
     uint32_t end = 0;
-    for (uint32_t x = rank * TB_NT + tid; x < gone[B]; x += TB_CTAS * TB_NT) {
-      if (row < 0 || x >= end) row = before(gone, B, x), end = gone[row + 1];
-      // the last gone[row + 1] - gone[row] entries of the row
-      const int at = P.held[row] - static_cast<int>(end - x);
-      const int id = P.table[row * P.tstride + at];
-      if (static_cast<uint32_t>(id) < np) atomicSub(P.refs + id, 1);
-      else if (R.status) atomicOr(R.status + row, SPEC_ROW_BAD_PAGE);
+    const uint32_t stride = team.ctas * TB_NT;
+    for (uint32_t x0 = team.rank * TB_NT + tid; x0 < gone[B]; x0 += 4 * stride) {
+      int id[4], of[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t x = x0 + u * stride;
+        of[u] = -1;
+        if (x >= gone[B]) continue;
+        if (row < 0 || x >= end) row = before(gone, B, x), end = gone[row + 1];
+        // the last gone[row + 1] - gone[row] entries of the row
+        of[u] = row;
+        id[u] = P.table[row * P.tstride + has[row] - static_cast<int>(end - x)];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (of[u] < 0) continue;
+        if (static_cast<uint32_t>(id[u]) < np) atomicSub(P.refs + id[u], 1);
+        else if (R.status) atomicOr(R.status + of[u], SPEC_ROW_BAD_PAGE);
+      }
     }
-    __threadfence();
+    team.sync();  // the counts
   }
-  cl.sync();  // counts, status words; every CTA has read what is held
-  const uint32_t found = take_pages(P, cum, B, S, [&](int row, uint32_t k, int32_t id) {
-    P.table[row * P.tstride + P.held[row] + k] = id;
+  const uint32_t found = take_pages(P, cum, B, team, S, [&](int row, uint32_t k, int32_t id) {
+    P.table[row * P.tstride + has[row] + k] = id;
     P.refs[id] = 1;
   });
-  cl.sync();  // what is held is not read any more
-  for (int b = rank * TB_NT + tid; b < B; b += TB_CTAS * TB_NT) {
+  for (int b = team.rank * TB_NT + tid; b < B; b += team.ctas * TB_NT) {
     const uint32_t take = cum[b + 1] - cum[b], give = gone[b + 1] - gone[b];
     if (take && cum[b + 1] > found) {
       if (R.status) atomicOr(R.status + b, SPEC_ROW_NO_PAGES);
     } else if (take | give) {
-      P.held[b] += static_cast<int>(take) - static_cast<int>(give);
+      P.held[b] = has[b] + static_cast<int>(take) - static_cast<int>(give);
     }
   }
+  // no CTA ends while another one may read its part of the sums
+  if (team.ctas > 1 && cum[B]) team.sync();
 }
 
 struct FP {
@@ -395,15 +442,17 @@ struct FP {
 };
 
 __global__ void __cluster_dims__(TB_CTAS, 1, 1) __launch_bounds__(TB_NT) fork_kernel(const __grid_constant__ FP F) {
-  extern __shared__ uint32_t cum[];  // n + 1 pages to take, n + 1 pages to share, B first forks to each row, n flags
-  __shared__ TableShared S;
+  extern __shared__ __align__(16) uint8_t tm[];
+  TableShared &S = *reinterpret_cast<TableShared *>(tm);
+  // n + 1 pages to take, n + 1 pages to share, B first forks to each row, n lengths of the sources, n flags
+  uint32_t *cum = reinterpret_cast<uint32_t *>(tm + sizeof(TableShared));
   const Pool &P = F.p;
-  cg::cluster_group cl = cg::this_cluster();
-  const unsigned rank = cl.block_rank();
+  Team team = {cg::this_cluster().block_rank(), TB_CTAS};
   const int n = F.n, tid = threadIdx.x, lg = P.ps_log2;
   const uint32_t B = static_cast<uint32_t>(P.B), np = static_cast<uint32_t>(P.n_pages);
   uint32_t *shared = cum + n + 1, *first = shared + n + 1;
-  uint8_t *fine = reinterpret_cast<uint8_t *>(first + P.B);
+  int32_t *lens = reinterpret_cast<int32_t *>(first + P.B);
+  uint8_t *fine = reinterpret_cast<uint8_t *>(lens + n);
   for (int b = tid; b < P.B; b += TB_NT) first[b] = ~0u;
   __syncthreads();
   for (int j = tid; j < n; j += TB_NT) {
@@ -413,13 +462,16 @@ __global__ void __cluster_dims__(TB_CTAS, 1, 1) __launch_bounds__(TB_NT) fork_ke
   __syncthreads();
   for (int j = tid; j < n; j += TB_NT) {
     const uint32_t s = F.src[j], d = F.dst[j];
-    int st = 0, need = 0, full = 0;
-    if (s >= B || d >= B || s == d || first[d] != static_cast<uint32_t>(j) || P.held[d] != 0) {
+    int st = 0, need = 0, full = 0, len = 0;
+    if (s >= B || d >= B || s == d || first[d] != static_cast<uint32_t>(j)) {
       st = SPEC_ROW_BAD_FORK;
     } else {
-      const int len = F.len[s], held = P.held[s];
+      len = F.len[s];
+      const int held = P.held[s], taken = P.held[d];
       const int64_t t = len == -1 ? 0 : static_cast<int64_t>(len) - P.prefix;
-      if (len < -1 || t < 0 || held < 0 || held > P.max_pages || (t + (1 << lg) - 1) >> lg > held) {
+      if (taken != 0) {
+        st = SPEC_ROW_BAD_FORK;
+      } else if (len < -1 || t < 0 || held < 0 || held > P.max_pages || (t + (1 << lg) - 1) >> lg > held) {
         st = SPEC_ROW_BAD_LENGTH;
       } else {
         full = static_cast<int>(t >> lg);
@@ -428,51 +480,81 @@ __global__ void __cluster_dims__(TB_CTAS, 1, 1) __launch_bounds__(TB_NT) fork_ke
     }
     cum[j] = need;
     shared[j] = full;
+    lens[j] = len;
     fine[j] = !st;
-    if (rank == 0) {
+    if (team.rank == 0) {
       if (F.status) F.status[j] = st;
       F.copies[3 * j] = F.copies[3 * j + 1] = -1, F.copies[3 * j + 2] = 0;
     }
   }
+  // status words and copies are written, lengths and what is held have been read by all
+  auto read = cg::this_cluster().barrier_arrive();
   __syncthreads();
-  sum_up(cum, n, S.warp);
-  sum_up(shared, n, S.warp);
-  cl.sync();  // status words and copies
-  const uint32_t found = take_pages(P, cum, n, S, [&](int j, uint32_t, int32_t id) {
-    const int s = F.src[j], full = static_cast<int>(shared[j + 1] - shared[j]);
-    const int old = P.table[s * P.tstride + full];
+  sum_up(cum, shared, n, S.warp2);
+  cg::this_cluster().barrier_wait(std::move(read));
+  if (cum[n] + shared[n] <= TB_ALONE) {
+    if (team.rank) return;
+    team.ctas = 1;
+  }
+  const uint32_t found = take_pages(P, cum, n, team, S, [&](int j, uint32_t, int32_t id) {
+    const int full = static_cast<int>(shared[j + 1] - shared[j]);
+    const int old = P.table[F.src[j] * P.tstride + full];
     P.table[F.dst[j] * P.tstride + full] = id;
     P.refs[id] = 1;
     if (static_cast<uint32_t>(old) < np) {
       F.copies[3 * j] = old;
       F.copies[3 * j + 1] = id;
-      F.copies[3 * j + 2] = F.len[s] - P.prefix - (full << lg);
+      F.copies[3 * j + 2] = lens[j] - P.prefix - (full << lg);
     } else if (F.status) {
       atomicOr(F.status + j, SPEC_ROW_BAD_PAGE);
     }
   });
   int j = -1;
-  for (uint32_t x = rank * TB_NT + tid; x < shared[n]; x += TB_CTAS * TB_NT) {
-    if (j < 0 || x >= shared[j + 1]) j = before(shared, n, x);
-    if (cum[j + 1] > cum[j] && cum[j + 1] > found) continue;
-    const int at = static_cast<int>(x - shared[j]);
-    const int id = P.table[F.src[j] * P.tstride + at];
-    P.table[F.dst[j] * P.tstride + at] = id;
-    if (static_cast<uint32_t>(id) < np) atomicAdd(P.refs + id, 1);
-    else if (F.status) atomicOr(F.status + j, SPEC_ROW_BAD_PAGE);
+  const uint32_t stride = team.ctas * TB_NT;
+  for (uint32_t x0 = team.rank * TB_NT + tid; x0 < shared[n]; x0 += 4 * stride) {
+    int id[4], of[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t x = x0 + u * stride;
+      of[u] = -1;
+      if (x >= shared[n]) continue;
+      if (j < 0 || x >= shared[j + 1]) j = before(shared, n, x);
+      if (cum[j + 1] > cum[j] && cum[j + 1] > found) continue;
+      of[u] = j;
+      id[u] = P.table[F.src[j] * P.tstride + static_cast<int>(x - shared[j])];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (of[u] < 0) continue;
+      P.table[F.dst[of[u]] * P.tstride + static_cast<int>(x0 + u * stride - shared[of[u]])] = id[u];
+      if (static_cast<uint32_t>(id[u]) < np) atomicAdd(P.refs + id[u], 1);
+      else if (F.status) atomicOr(F.status + of[u], SPEC_ROW_BAD_PAGE);
+    }
   }
-  const int k = rank * TB_NT + tid;  // n is at most half as many
-  const bool mine = k < n && fine[k < n ? k : 0];
-  const uint32_t take = mine ? cum[k + 1] - cum[k] : 0;
-  const int len = mine ? F.len[F.src[k]] : 0;
-  cl.sync();  // lengths and what is held are not read any more
-  if (!mine) return;
-  if (take && cum[k + 1] > found) {
-    if (F.status) atomicOr(F.status + k, SPEC_ROW_NO_PAGES);
-    return;
+  for (int k = team.rank * TB_NT + tid; k < n; k += team.ctas * TB_NT) {
+    if (!fine[k]) continue;
+    const uint32_t take = cum[k + 1] - cum[k];
+    if (take && cum[k + 1] > found) {
+      if (F.status) atomicOr(F.status + k, SPEC_ROW_NO_PAGES);
+      continue;
+    }
+    P.held[F.dst[k]] = static_cast<int>(shared[k + 1] - shared[k] + take);
+    F.len[F.dst[k]] = lens[k];
   }
-  P.held[F.dst[k]] = static_cast<int>(shared[k + 1] - shared[k] + take);
-  F.len[F.dst[k]] = len;
+  // no CTA ends while another one may read its part of the sums
+  if (team.ctas > 1 && cum[n]) team.sync();
+}
+
+constexpr int kDevices = 64;
+
+// The kernel may use `most` bytes of shared memory: set once per device.
+bool allow_shared(const void *f, int most, std::atomic<bool> *ready) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
+  if (ready[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return false;
+  ready[dev].store(true, std::memory_order_release);
+  return true;
 }
 
 spec_status check_pool(const spec_kv_pool *p, Pool &P) {
@@ -555,7 +637,9 @@ extern "C" spec_status spec_kv_resize(const spec_kv_pool *pool, const int32_t *k
   R.len = kv_len;
   R.n = n_step;
   R.status = row_status;
-  const int smem = 2 * (pool->B + 1) * 4;
+  const int smem = sizeof(TableShared) + (3 * pool->B + 2) * 4;
+  static std::atomic<bool> ready[kDevices] = {};
+  if (!allow_shared(reinterpret_cast<const void *>(resize_kernel), sizeof(TableShared) + (3 * kv::kMaxB + 2) * 4, ready)) return SPEC_ERR_CUDA;
   resize_kernel<<<TB_CTAS, TB_NT, smem, static_cast<cudaStream_t>(stream)>>>(R);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
@@ -578,16 +662,9 @@ extern "C" spec_status spec_kv_fork(const spec_kv_pool *pool, int32_t *kv_len, c
   F.n = n;
   F.copies = copies;
   F.status = fork_status;
-  const int smem = (2 * (n + 1) + pool->B) * 4 + n;
-  constexpr int most = (2 * (kv::kMaxB + 1) + kv::kMaxB) * 4 + kv::kMaxB;
-  static std::atomic<bool> ready[64] = {};  // the kernel's shared memory limit, set once per device
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return SPEC_ERR_CUDA;
-  if (!ready[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
-      return SPEC_ERR_CUDA;
-    ready[dev].store(true, std::memory_order_release);
-  }
+  const int smem = sizeof(TableShared) + (2 * (n + 1) + pool->B + n) * 4 + n;
+  static std::atomic<bool> ready[kDevices] = {};
+  if (!allow_shared(reinterpret_cast<const void *>(fork_kernel), sizeof(TableShared) + (4 * kv::kMaxB + 2) * 4 + kv::kMaxB, ready)) return SPEC_ERR_CUDA;
   fork_kernel<<<TB_CTAS, TB_NT, smem, static_cast<cudaStream_t>(stream)>>>(F);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -5,10 +5,13 @@
 // reads the sequence once and counts the slice's tokens in shared memory (integer
 // atomics: the order does not matter), with a flag each for tokens of the prompt
 // and of the drafts; the last entry of the bias list for a token is the largest
-// index.  A bit per token then says whether anything is to be done at all, so that
-// the stream over the logits looks up one bit each and is else a copy.  A draft
-// counts at the positions that it comes before: tokens with the drafts' flag (a
-// few per slice) go through the list of drafts and the position's mask.
+// index.  Tokens with any of these go on a list.  The stream over the logits is
+// then a copy that knows the mask alone, and the listed tokens are changed behind
+// it, one by one, from the logits as they were: their lines are still in L2, and no
+// branch of the stream depends on the data.  In place
+// there is no stream but the mask's.  A draft counts at the positions that it
+// comes before: tokens with the drafts' flag (a few per slice) go through the list
+// of drafts and the position's mask.
 //
 // Bound: memory, the logits once in and once out.  The slice is a CTA's share of
 // the vocabulary such that the grid fills the machine; each slice reads the whole
@@ -26,6 +29,9 @@ namespace {
 
 constexpr int AJ_NT = 256;         // threads per CTA
 constexpr int AJ_SLICE = 8192;     // tokens of a slice at most
+constexpr int AJ_COUNT = 128;         // of them counting
+constexpr int AJ_UNROLL = 4;         // loads of a thread in flight together: of the stream,
+constexpr int AJ_SPARSE = 2;         // of a listed token (positions)
 constexpr uint32_t kPrompt = 1u << 31, kDraft = 1u << 30, kCount = kDraft - 1;
 
 struct JP {
@@ -65,24 +71,37 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t *w, int at, int last)
   return __funnelshift_r(lo, hi, at & 31);
 }
 
-// Shared memory: a word per token of the slice, a bit per token, then (with
-// biases) half a word per token; the drafts.
+// The lanes of a 32-bit word that hold elements whose bits are set in `no`
+// (VEC 4: one element, VEC 8: two).
+template <bool F32>
+__device__ __forceinline__ uint32_t masked(uint32_t x, uint32_t no) {
+  if constexpr (F32) return no & 1 ? 0xff800000u : x;
+  const uint32_t m = (no & 1 ? 0xffffu : 0u) | (no & 2 ? 0xffff0000u : 0u);
+  return (x & ~m) | (0xff80ff80u & m);
+}
+
+// Shared memory: a word per token of the slice, (with biases) another one, a list
+// of tokens, the drafts.
 template <bool F32>
 __global__ void __launch_bounds__(AJ_NT) adjust_kernel(const __grid_constant__ JP P) {
   using E = Elem<F32>;
   using T = typename E::T;
-  constexpr int VEC = E::VEC;
+  constexpr int VEC = E::VEC, U = AJ_UNROLL, S = AJ_SPARSE;
   extern __shared__ uint32_t sm[];
+  __shared__ uint32_t listed, next;  // tokens on the list; next part of the stream
   const spec_adjust_params &a = P.a;
-  const int tid = threadIdx.x;
-  const int slice = blockIdx.x % P.slices, bg = blockIdx.x / P.slices;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // the low tokens first: they are the frequent ones, and have the longest lists
+  const int bg = blockIdx.x % (a.B * P.groups), slice = blockIdx.x / (a.B * P.groups);
   const int grp = bg % P.groups, b = bg / P.groups;
   const int v0 = slice * P.slice, n = min(P.slice, a.V - v0);
   const int N = a.gamma_max + 1, i0 = grp * P.npos, i1 = min(i0 + P.npos, N);
-  uint32_t *count = sm, *touched = count + P.slice;
-  uint32_t *bias = touched + P.slice / 32;  // 0: none, else entry + 1
-  int32_t *drafts = reinterpret_cast<int32_t *>(bias + (a.n_bias ? P.slice : 0));
+  uint32_t *count = sm, *bias = count + P.slice;  // bias: 0: none, else entry + 1
+  uint16_t *list = reinterpret_cast<uint16_t *>(bias + (a.n_bias ? P.slice : 0));
+  int32_t *drafts = reinterpret_cast<int32_t *>(list + P.slice);
+  const bool counts = a.repetition || a.frequency || a.presence;
 
+  if (tid == 0) listed = 0, next = 0;
   const int g = a.gamma_per_row ? a.gamma_per_row[b] : a.gamma_max;
   const int len = a.seq_len[b], prompt = a.prompt_len ? a.prompt_len[b] : 0;
   const float r = a.repetition ? a.repetition[b] : 1.0f;
@@ -98,110 +117,133 @@ __global__ void __launch_bounds__(AJ_NT) adjust_kernel(const __grid_constant__ J
       for (int x = tid; x < n; x += AJ_NT) out[i * a.out_pos_stride + x] = E::kNan;
     return;
   }
-
-  // --- what the slice's tokens have behind them
-  for (int x = tid; x < P.slice + P.slice / 32 + (a.n_bias ? P.slice : 0); x += AJ_NT) sm[x] = 0;
   __syncthreads();
-  const bool counts = a.repetition || a.frequency || a.presence;
-  if (counts) {
-    const int32_t *seq = a.seq + b * a.seq_row_stride;
-    for (int s0 = tid; s0 < len; s0 += 4 * AJ_NT) {
-      int t[4];
+
+  // --- what the slice's tokens have behind them, by the first warps; the others
+  // begin with the stream
+  if (tid < AJ_COUNT && (counts || a.n_bias)) {
+    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(AJ_COUNT) : "memory"); };
+    for (int x = tid; x < P.slice * (a.n_bias ? 2 : 1) / 4; x += AJ_COUNT)
+      reinterpret_cast<uint4 *>(sm)[x] = make_uint4(0, 0, 0, 0);
+    meet();
+    if (counts) {
+      const int32_t *seq = a.seq + b * a.seq_row_stride;
+      constexpr int K = 8;
+      for (int s0 = tid; s0 < len; s0 += K * AJ_COUNT) {
+        int t[K];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) t[u] = s0 + u * AJ_NT < len ? __ldg(seq + s0 + u * AJ_NT) - v0 : -1;
+        for (int u = 0; u < K; ++u) t[u] = s0 + u * AJ_COUNT < len ? __ldg(seq + s0 + u * AJ_COUNT) - v0 : -1;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (static_cast<uint32_t>(t[u]) < static_cast<uint32_t>(n)) {
-          if (s0 + u * AJ_NT < prompt) atomicOr(count + t[u], kPrompt);
-          else atomicAdd(count + t[u], 1u);
-          atomicOr(touched + (t[u] >> 5), 1u << (t[u] & 31));
-        }
-    }
-    for (int j = tid; j < g; j += AJ_NT) {
-      const int t = __ldg(a.draft_tokens + static_cast<int64_t>(b) * a.gamma_max + j) - v0;
-      drafts[j] = t;
-      if (static_cast<uint32_t>(t) < static_cast<uint32_t>(n)) {
-        atomicOr(count + t, kDraft);
-        atomicOr(touched + (t >> 5), 1u << (t & 31));
+        for (int u = 0; u < K; ++u)
+          if (static_cast<uint32_t>(t[u]) < static_cast<uint32_t>(n)) {
+            if (s0 + u * AJ_COUNT < prompt) atomicOr(count + t[u], kPrompt);
+            else atomicAdd(count + t[u], 1u);
+          }
+      }
+      for (int j = tid; j < g; j += AJ_COUNT) {
+        const int t = __ldg(a.draft_tokens + static_cast<int64_t>(b) * a.gamma_max + j) - v0;
+        drafts[j] = t;
+        if (static_cast<uint32_t>(t) < static_cast<uint32_t>(n)) atomicOr(count + t, kDraft);
       }
     }
-  }
-  for (int j = tid; j < a.n_bias; j += AJ_NT) {
-    const int t = __ldg(a.bias_ids + static_cast<int64_t>(b) * a.n_bias + j) - v0;
-    if (static_cast<uint32_t>(t) < static_cast<uint32_t>(n)) {
-      atomicMax(bias + t, static_cast<uint32_t>(j + 1));
-      atomicOr(touched + (t >> 5), 1u << (t & 31));
+    for (int j = tid; j < a.n_bias; j += AJ_COUNT) {
+      const int t = __ldg(a.bias_ids + static_cast<int64_t>(b) * a.n_bias + j) - v0;
+      if (static_cast<uint32_t>(t) < static_cast<uint32_t>(n)) atomicMax(bias + t, static_cast<uint32_t>(j + 1));
+    }
+    meet();
+    for (int x0 = tid & ~31; x0 < n; x0 += AJ_COUNT) {  // 32 tokens' places side by side, so that their accesses are too
+      const int x = x0 + lane;
+      const bool on = x < n && (count[x] || (a.n_bias && bias[x]));
+      const uint32_t all = __ballot_sync(~0u, on);
+      uint32_t at = 0;
+      if (lane == 0 && all) at = atomicAdd(&listed, __popc(all));
+      at = __shfl_sync(~0u, at, 0);
+      if (on) list[at + __popc(all & ((1u << lane) - 1))] = static_cast<uint16_t>(x);
     }
   }
-  __syncthreads();
 
+  // --- the stream, in parts of 32 U x 16 bytes of a position, a warp each
+  const uint32_t *allowed = a.allowed ? reinterpret_cast<const uint32_t *>(a.allowed) + b * a.allowed_row_stride : nullptr;
+  const int last = (a.V - 1) >> 5;
+  auto banned = [&](int i, int x) {  // token x of the slice at position i
+    return allowed && i <= g && !(allowed[i * a.allowed_pos_stride + ((v0 + x) >> 5)] >> ((v0 + x) & 31) & 1);
+  };
+  const int end = P.same ? (allowed ? min(i1, g + 1) : i0) : i1;
+  const int per = (n + 32 * U * VEC - 1) / (32 * U * VEC), parts = max(end - i0, 0) * per;
+  for (;;) {
+    int part = 0;
+    if (lane == 0) part = atomicAdd(&next, 1u);
+    part = __shfl_sync(~0u, part, 0);
+    if (part >= parts) break;
+    const int i = i0 + part / per, c0 = part % per * (32 * U);
+    const T *src = in + i * a.logits_pos_stride;
+    T *dst = out + i * a.out_pos_stride;
+    auto one = [&](int x) {
+      if (banned(i, x)) dst[x] = E::kMinf;
+      else if (!P.same) dst[x] = src[x];
+    };
+    if (!P.vec) {
+      for (int x = c0 * VEC + lane; x < min(n, (c0 + 32 * U) * VEC); x += 32) one(x);
+      continue;
+    }
+    // elements before the first multiple of 16 bytes and behind the last one by one
+    const int head = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / static_cast<int>(sizeof(T)), n);
+    const int chunks = (n - head) / VEC, behind = head + chunks * VEC;
+    if (c0 == 0 && lane < head + n - behind) one(lane < head ? lane : behind + lane - head);
+    const uint32_t *row = allowed && i <= g ? allowed + i * a.allowed_pos_stride : nullptr;
+    uint4 q[U];
+    uint32_t no[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + 32 * u + lane;
+      no[u] = row && c < chunks ? ~bits_at(row, v0 + head + c * VEC, last) & ((1u << VEC) - 1) : 0;
+      if (c < chunks && (!P.same || no[u])) q[u] = __ldcs(reinterpret_cast<const uint4 *>(src + head) + c);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + 32 * u + lane;
+      if (c >= chunks || (P.same && !no[u])) continue;
+      if (row) {
+        constexpr int W = VEC / 4;  // elements of a word
+        q[u].x = masked<F32>(q[u].x, no[u]), q[u].y = masked<F32>(q[u].y, no[u] >> W);
+        q[u].z = masked<F32>(q[u].z, no[u] >> 2 * W), q[u].w = masked<F32>(q[u].w, no[u] >> 3 * W);
+      }
+      __stcs(reinterpret_cast<uint4 *>(dst + head) + c, q[u]);
+    }
+  }
+  __syncthreads();  // the listed tokens' places are written again below
+
+  // --- the tokens that something applies to, at the positions up to gamma_b
   const float *bias_of = a.bias + static_cast<int64_t>(b) * a.n_bias - 1;
-  // logit z of the slice's token x at position i
-  auto change = [&](float z, int x, int i) {
-    const uint32_t c = count[x];
-    if (c) {
+  const int stop = min(i1, g + 1), blocks = stop > i0 ? (stop - i0 + S - 1) / S : 0;
+  const int many = static_cast<int>(listed);
+  for (int y = tid; y < many * blocks; y += AJ_NT) {
+    const int ib = i0 + y / many * S, x = list[y % many];
+    const uint32_t c = count[x], e = a.n_bias ? bias[x] : 0;
+    const float more = e ? __ldg(bias_of + e) : 0.0f;
+    T from[S];
+    bool on[S];
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+      on[u] = ib + u < stop && !banned(ib + u, x);  // banned: -inf already
+      if (on[u]) from[u] = in[(ib + u) * a.logits_pos_stride + x];
+    }
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+      if (!on[u]) continue;
+      const int i = ib + u;
+      float z = E::value(from[u]);
       uint32_t made = c & kCount;
       if (c & kDraft) {  // rare
         const int32_t *mask = a.tree_mask ? a.tree_mask + (static_cast<int64_t>(b) * N + i) * P.W : nullptr;
         for (int j = 0; j < (mask ? g : min(g, i)); ++j)
           if (drafts[j] == x && (!mask || (mask[(j + 1) >> 5] >> ((j + 1) & 31) & 1))) ++made;
       }
+      if (!made && !(c & kPrompt) && !e) continue;
       if (made || (c & kPrompt)) z = z > 0.0f ? __fdiv_rn(z, r) : z * r;
       if (made) z = (z - f * static_cast<float>(made)) - p;
-    }
-    if (a.n_bias) {
-      const uint32_t e = bias[x];
-      if (e) z += bias_of[e];
-    }
-    return z;
-  };
-
-  const int last = (a.V - 1) >> 5, tlast = P.slice / 32 - 1;
-  for (int i = i0; i < i1; ++i) {
-    const T *src = in + i * a.logits_pos_stride;
-    T *dst = out + i * a.out_pos_stride;
-    const bool live = i <= g;
-    if (!live && P.same) break;
-    const uint32_t *allowed = a.allowed && live ? reinterpret_cast<const uint32_t *>(a.allowed) + b * a.allowed_row_stride + i * a.allowed_pos_stride : nullptr;
-    auto one = [&](int x) {
-      T e = src[x];
-      if (live && (touched[x >> 5] >> (x & 31) & 1)) e = E::bits(change(E::value(e), x, i));
-      if (allowed && !(allowed[(v0 + x) >> 5] >> ((v0 + x) & 31) & 1)) e = E::kMinf;
-      dst[x] = e;
-    };
-    if (!P.vec) {
-      for (int x = tid; x < n; x += AJ_NT) one(x);
-      continue;
-    }
-    // up to the first multiple of 16 bytes, and behind the last
-    const int head = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / static_cast<int>(sizeof(T)), n);
-    const int chunks = (n - head) / VEC, tail = head + chunks * VEC;
-    if (tid < head) one(tid);
-    if (tid < n - tail) one(tail + tid);
-    for (int c0 = tid; c0 < chunks; c0 += 4 * AJ_NT) {
-      uint4 q[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (c0 + u * AJ_NT < chunks) q[u] = __ldcs(reinterpret_cast<const uint4 *>(src + head) + c0 + u * AJ_NT);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = c0 + u * AJ_NT, x = head + c * VEC;
-        if (c >= chunks) break;
-        constexpr uint32_t all = (1u << VEC) - 1;
-        const uint32_t t = live ? bits_at(touched, x, tlast) & all : 0;
-        const uint32_t no = allowed ? ~bits_at(allowed, v0 + x, last) & all : 0;
-        if (t | no) {
-          T *e = reinterpret_cast<T *>(&q[u]);
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            if (t >> k & 1) e[k] = E::bits(change(E::value(e[k]), x + k, i));
-            if (no >> k & 1) e[k] = E::kMinf;
-          }
-        } else if (P.same) {
-          continue;
-        }
-        __stcs(reinterpret_cast<uint4 *>(dst + head) + c, q[u]);
-      }
+      if (e) z += more;
+      out[i * a.out_pos_stride + x] = E::bits(z);
     }
   }
 }
@@ -249,10 +291,14 @@ extern "C" spec_status spec_adjust(const void *logits, const spec_adjust_params 
   const uintptr_t off = (x ^ y) | static_cast<uintptr_t>(a.B > 1 ? (a.logits_row_stride - a.out_row_stride) * static_cast<int64_t>(es) : 0) |
                         static_cast<uintptr_t>(a.gamma_max > 0 ? (a.logits_pos_stride - a.out_pos_stride) * static_cast<int64_t>(es) : 0);
   P.vec = off % 16 == 0;
-  // Slices: as many as give the machine some 8 CTAs a multiprocessor, of 1024
-  // tokens at least; then positions, down to one.
-  const int64_t want = 152 * 8;
-  int64_t slices = std::min<int64_t>((want + a.B - 1) / a.B, (a.V + 1023) / 1024);
+  // Slices: as many as give the machine some 16 CTAs a multiprocessor, of 2048
+  // tokens at least (each reads the whole sequence), of 512 where there would not be
+  // one CTA a multiprocessor; then positions, down to one.  Measured, in us, 64 x 5 rows of
+  // 50304 in float32 with 8 / 16 / 24 CTAs wanted: 30.5 / 29.1 / 42.9; of 1024
+  // tokens at least: 30.4 / 33.6 / 37.0; 32 x 31 rows of 152064 in bfloat16: 123 / 114 / 114.
+  const int64_t want = 152 * 16;
+  int64_t slices = std::min<int64_t>((want + a.B - 1) / a.B, (a.V + 2047) / 2048);
+  if (slices * a.B < 152) slices = std::min<int64_t>((152 + a.B - 1) / a.B, (a.V + 511) / 512);
   slices = std::max<int64_t>(slices, (a.V + AJ_SLICE - 1) / AJ_SLICE);
   P.slice = static_cast<int>(((a.V + slices - 1) / slices + 31) / 32 * 32);
   P.slices = (a.V + P.slice - 1) / P.slice;
@@ -262,7 +308,7 @@ extern "C" spec_status spec_adjust(const void *logits, const spec_adjust_params 
   P.groups = (N + P.npos - 1) / P.npos;
   const int64_t grid = have * P.groups;
   if (grid > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
-  const int smem = (P.slice + P.slice / 32 + (a.n_bias ? P.slice : 0) + std::min(a.gamma_max, 4096)) * 4;
+  const int smem = P.slice * (a.n_bias ? 8 : 4) + P.slice * 2 + std::min(a.gamma_max, 4096) * 4;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto *k = a.dtype == SPEC_F32 ? adjust_kernel<true> : adjust_kernel<false>;
   if (smem > 48 * 1024 &&

@@ -249,8 +249,8 @@ def spec_kv_read(cache, page_table, kv_len, n, begin=0, prefix_table=None, prefi
                    with_status)
     n, begin = int(n), int(begin)
     shape = (b.B, n, cache.n_kv_heads, cache.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=dev)
-    v = torch.empty(shape, dtype=dtype, device=dev)
+    k = torch.empty(*shape, dtype=dtype, device=dev)
+    v = torch.empty(*shape, dtype=dtype, device=dev)
     st = _status(with_status, b.B, dev)
     code = _lib().spec_kv_read(cache.ref, _byref(b), begin, n, 0 if dtype is _f32 else 1, k.data_ptr(), v.data_ptr(),
                                _ptr(st), _raw_stream(dev.index))
@@ -319,8 +319,8 @@ def _attend(q, cache, page_table, kv_len, mask, prefix_table, prefix_len, gamma_
     elif workspace is None or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be 'auto' or a contiguous tensor on {dev}")
     if out is None:
-        o = torch.empty(shape, dtype=_bf16, device=dev)
-        lse = torch.empty(shape[:3], dtype=_f32, device=dev)
+        o = torch.empty(B, N, Hq, D, dtype=_bf16, device=dev)  # sizes one by one: 1 us less each
+        lse = torch.empty(B, N, Hq, dtype=_f32, device=dev)
     else:
         o, lse = out
         if (o.shape != shape or o.dtype is not _bf16 or not o.is_contiguous() or lse.shape != shape[:3] or
@@ -438,7 +438,7 @@ def spec_kv_fork(refs, page_table, held, kv_len, src, dst, page_size, prefix_len
     if _elsewhere(stream, dev):
         return _on(stream, dev, spec_kv_fork, refs, page_table, held, kv_len, src, dst, page_size, prefix_len,
                    with_status)
-    copies = torch.empty((n, 3), dtype=_i32, device=dev)
+    copies = torch.empty(n, 3, dtype=_i32, device=dev)
     st = _status(with_status, n, dev)
     code = _lib().spec_kv_fork(_byref(p), lens, s, d, n, copies.data_ptr(), _ptr(st), _raw_stream(dev.index))
     if code:

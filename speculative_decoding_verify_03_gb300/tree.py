@@ -23,12 +23,21 @@ class SpecAdjustParams(ctypes.Structure):
 
 
 def _table(name, t, shape, device):
-    """A contiguous int32 tensor of this shape on the device: its address (None without elements)."""
+    """A contiguous int32 tensor of this shape on the device: its address (0 without elements)."""
     if t.dtype is not _i32:
         raise TypeError(f"{name} must be int32")
     if t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)} on {device}")
-    return t.data_ptr() if t.numel() else None
+    return t.data_ptr()
+
+
+def _float(name, t, shape, device):
+    """As _table, float32."""
+    if t.dtype is not _f32:
+        raise TypeError(f"{name} must be float32")
+    if t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)} on {device}")
+    return t.data_ptr()
 
 
 def spec_tree_mask(parents, gamma_per_row=None, with_status=False, stream=None):
@@ -46,8 +55,8 @@ def spec_tree_mask(parents, gamma_per_row=None, with_status=False, stream=None):
     gam = None if gamma_per_row is None else _int32("gamma_per_row", gamma_per_row, B, dev)
     if _elsewhere(stream, dev):
         return _on(stream, dev, spec_tree_mask, parents, gamma_per_row, with_status)
-    mask = torch.empty((B, G + 1, (G + 32) // 32), dtype=_i32, device=dev)
-    depth = torch.empty((B, G + 1), dtype=_i32, device=dev)
+    mask = torch.empty(B, G + 1, (G + 32) // 32, dtype=_i32, device=dev)
+    depth = torch.empty(B, G + 1, dtype=_i32, device=dev)
     st = _status(with_status, B, dev)
     code = _lib().spec_tree_mask(B, G, up, gam, mask.data_ptr(), depth.data_ptr(), _ptr(st), _raw_stream(dev.index))
     if code:
@@ -72,8 +81,10 @@ def spec_tree_accept(target_tokens, draft_tokens, parents, gamma_per_row=None, w
     gam = None if gamma_per_row is None else _int32("gamma_per_row", gamma_per_row, B, dev)
     if _elsewhere(stream, dev):
         return _on(stream, dev, spec_tree_accept, target_tokens, draft_tokens, parents, gamma_per_row, with_status)
-    new = lambda *s: torch.empty(s, dtype=_i32, device=dev)  # noqa: E731
-    acc, nxt, path, tokens = new(B), new(B), new(B, N), new(B, N - 1)
+    acc = torch.empty(B, dtype=_i32, device=dev)
+    nxt = torch.empty(B, dtype=_i32, device=dev)
+    path = torch.empty(B, N, dtype=_i32, device=dev)
+    tokens = torch.empty(B, N - 1, dtype=_i32, device=dev)
     st = _status(with_status, B, dev)
     code = _lib().spec_tree_accept(B, N - 1, tgt, tok, up, gam, acc.data_ptr(), nxt.data_ptr(), path.data_ptr(),
                                    tokens.data_ptr(), _ptr(st), _raw_stream(dev.index))
@@ -103,7 +114,8 @@ def spec_adjust(logits, seq, seq_len, draft_tokens=None, tree_mask=None, prompt_
     if logits.dtype is not _f32 and logits.dtype is not _bf16:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     B, N, V = logits.shape
-    if logits.stride(2) != 1 and V > 1:
+    in_row, in_pos, one = logits.stride()
+    if one != 1 and V > 1:
         raise ValueError("the vocabulary axis must be contiguous")
     if out is not None and (out.shape != logits.shape or out.dtype != logits.dtype or out.device != dev or
                             (out.stride(2) != 1 and V > 1)):
@@ -116,44 +128,36 @@ def spec_adjust(logits, seq, seq_len, draft_tokens=None, tree_mask=None, prompt_
         raise ValueError("draft_tokens must be given where there are drafts")
     if (bias_ids is None) != (bias is None):
         raise ValueError("bias_ids and bias go together")
-    P = SpecAdjustParams(B=B, gamma_max=N - 1, V=V, dtype=0 if logits.dtype is _f32 else 1, capacity=seq.shape[1],
-                         logits_row_stride=logits.stride(0), logits_pos_stride=logits.stride(1),
-                         seq_row_stride=seq.stride(0) if B > 1 else seq.shape[1], seq=seq.data_ptr())
-    P.seq_len = _int32("seq_len", seq_len, B, dev)
-    for name, t in (("prompt_len", prompt_len), ("gamma_per_row", gamma_per_row)):
-        if t is not None:
-            setattr(P, name, _int32(name, t, B, dev))
-    if draft_tokens is not None:
-        P.draft_tokens = _table("draft_tokens", draft_tokens, (B, N - 1), dev)
-    if tree_mask is not None:
-        P.tree_mask = _table("tree_mask", tree_mask, (B, N, (N + 31) // 32), dev)
-    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency)):
-        if t is not None:
-            if t.dtype is not _f32:
-                raise TypeError(f"{name} must be float32")
-            if t.shape != (B,) or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous [{B}] on {dev}")
-            setattr(P, name, t.data_ptr())
+    lens = _int32("seq_len", seq_len, B, dev)
+    prompt = None if prompt_len is None else _int32("prompt_len", prompt_len, B, dev)
+    gam = None if gamma_per_row is None else _int32("gamma_per_row", gamma_per_row, B, dev)
+    drafts = None if draft_tokens is None else _table("draft_tokens", draft_tokens, (B, N - 1), dev)
+    tree = None if tree_mask is None else _table("tree_mask", tree_mask, (B, N, (N + 31) // 32), dev)
+    rep, pres, freq = (None if t is None else _float(name, t, (B,), dev) for name, t in
+                       (("repetition", repetition), ("presence", presence), ("frequency", frequency)))
+    n_bias, ids, values = 0, None, None
     if bias is not None:
-        if bias.dim() != 2 or bias.shape[0] != B or bias.device != dev or not bias.is_contiguous():
-            raise ValueError(f"bias must be contiguous [{B}, n] on {dev}")
-        if bias.dtype is not _f32:
-            raise TypeError("bias must be float32")
-        P.bias_ids = _table("bias_ids", bias_ids, bias.shape, dev)
-        P.n_bias, P.bias = bias.shape[1], bias.data_ptr() if bias.numel() else None
+        n_bias = bias.shape[1] if bias.dim() == 2 else -1
+        values = _float("bias", bias, (B, n_bias), dev)
+        ids = _table("bias_ids", bias_ids, (B, n_bias), dev)
+    words, allowed_row, allowed_pos = None, 0, 0
     if allowed is not None:
         if allowed.dtype is not _i32:
             raise TypeError("allowed must be int32")
-        words = (V + 31) // 32
-        if allowed.shape != (B, N, words) or allowed.device != dev or (words > 1 and allowed.stride(2) != 1):
-            raise ValueError(f"allowed must be [{B}, {N}, {words}] on {dev} with contiguous words")
-        P.allowed, P.allowed_row_stride, P.allowed_pos_stride = allowed.data_ptr(), allowed.stride(0), allowed.stride(1)
+        n = (V + 31) // 32
+        allowed_row, allowed_pos, one = allowed.stride() if allowed.dim() == 3 else (0, 0, 0)
+        if allowed.shape != (B, N, n) or allowed.device != dev or (n > 1 and one != 1):
+            raise ValueError(f"allowed must be [{B}, {N}, {n}] on {dev} with contiguous words")
+        words = allowed.data_ptr()
     if _elsewhere(stream, dev):
         return _on(stream, dev, spec_adjust, logits, seq, seq_len, draft_tokens, tree_mask, prompt_len, repetition,
                    presence, frequency, bias_ids, bias, allowed, gamma_per_row, out, with_status)
     if out is None:
-        out = torch.empty((B, N, V), dtype=logits.dtype, device=dev)
-    P.out_row_stride, P.out_pos_stride = out.stride(0), out.stride(1)
+        out = torch.empty(B, N, V, dtype=logits.dtype, device=dev)
+    row, pos, _ = out.stride()
+    P = SpecAdjustParams(B, N - 1, V, 0 if logits.dtype is _f32 else 1, seq.shape[1], n_bias, in_row, in_pos, row, pos,
+                         seq.stride(0) if B > 1 else seq.shape[1], allowed_row, allowed_pos, seq.data_ptr(), lens, prompt,
+                         drafts, tree, gam, rep, pres, freq, ids, values, words)
     st = _status(with_status, B, dev)
     code = _lib().spec_adjust(logits.data_ptr(), _byref(P), out.data_ptr(), _ptr(st), _raw_stream(dev.index))
     if code:
