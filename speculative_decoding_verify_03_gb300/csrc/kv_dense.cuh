@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   tc_after();
   e -= a, e1 -= a1;
   uint32_t rows = 0, items = 0;  // all query rows; own items: all tiles, all items
+#pragma unroll 4
   for (int v = 0; v < DN_NT / 32; ++v) {
     if (v < warp) {
       e += S.sum[v];
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     int node = -1;  // own items: the row's place in the step
     int begun = 0;  // own items: the CTA's first tile of the item
     int g = 0;  // items
+#pragma unroll 1
     for (int u = 0; u < 2 * tiles; ++u) {
       const int t = u >> 1;  // half u & 1 of tile t
       if (fresh) {  // the row's query; the products with the item before are done
@@ -287,30 +289,33 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
         }
         // into shared memory by the warp's 32 rows together, neighbouring lanes
         // neighbouring chunks; then a row by its own thread
+        // (loops, not one long piece of code: an item's first tile would wait for its
+        // instructions)
         constexpr int CH = D / 8;
-        uint4 v[CH];
         auto at = [&](int y, int c) {
           return wb + (c >> 3) * (DN_TILE * 128) + y * 128 + (((c ^ y) & 7) << 4);
         };
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-          const int z = lane + 32 * k, y = z / CH;
-          const int64_t o = __shfl_sync(~0u, off, y);
-          v[k] = make_uint4(0, 0, 0, 0);
-          if (o >= 0) {
-            const __nv_bfloat16 *src = P.q + o + 8 * (z - y * CH);
-            if (P.qvec) {
-              v[k] = __ldg(reinterpret_cast<const uint4 *>(src));
-            } else {
-              const uint16_t *u = reinterpret_cast<const uint16_t *>(src);
-              v[k] = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
-            }
+        if (P.qvec) {
+#pragma unroll 4
+          for (int k = 0; k < CH; ++k) {
+            const int z = lane + 32 * k, y = z / CH, c = z - y * CH;
+            const int64_t o = __shfl_sync(~0u, off, y);
+            cp16(at(y, c), P.q + (o < 0 ? 0 : o + 8 * c), o >= 0);
           }
-        }
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-          const int z = lane + 32 * k, y = z / CH;
-          sts128(at(y, z - y * CH), v[k]);
+          cp_commit();
+          cp_wait<0>();
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < CH; ++k) {
+            const int z = lane + 32 * k, y = z / CH, c = z - y * CH;
+            const int64_t o = __shfl_sync(~0u, off, y);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (o >= 0) {
+              const uint16_t *u = reinterpret_cast<const uint16_t *>(P.q + o + 8 * c);
+              v = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+            }
+            sts128(at(y, c), v);
+          }
         }
         qc = P.c;
         if constexpr (E4M3) {
@@ -322,10 +327,10 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
             const uint32_t a = u & 0x7fffu, b = u >> 16 & 0x7fffu;
             m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
           };
-#pragma unroll
+#pragma unroll 2
           for (int k = 0; k < CH; ++k) {
-            v[k] = lds128(at(lane, k));
-            most(v[k].x), most(v[k].y), most(v[k].z), most(v[k].w);
+            const uint4 v = lds128(at(lane, k));
+            most(v.x), most(v.y), most(v.z), most(v.w);
           }
           const int eq = max(static_cast<int>(m >> 7) - 127 - 10, -100);
           qc = P.c * pow2i(eq);
@@ -333,9 +338,11 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           auto two = [&](uint32_t u) {
             return pack<true>(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
           };
-#pragma unroll
-          for (int k = 0; k < CH; ++k)
-            sts128(at(lane, k), make_uint4(two(v[k].x), two(v[k].y), two(v[k].z), two(v[k].w)));
+#pragma unroll 2
+          for (int k = 0; k < CH; ++k) {
+            const uint4 v = lds128(at(lane, k));
+            sts128(at(lane, k), make_uint4(two(v.x), two(v.y), two(v.z), two(v.w)));
+          }
         }
         fence_async();
         __syncwarp();
@@ -495,105 +502,152 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       constexpr int CPR = D / 16;                     // 16-byte chunks of a row
       constexpr int PASS = DN_TILE * CPR / DN_FETCH;  // of a tile, per thread
       static_assert(DN_TILE * CPR % DN_FETCH == 0, "chunks");
-      int id[PASS], ide = -1;  // page ids of the tile to be fetched next
-      auto pages = [&]() {
-        const int t0 = x.tt * DN_TILE, end = held();
-        const int32_t *ids = list();
-#pragma unroll
-        for (int i = 0; i < PASS; ++i) {
-          const int tok = t0 + (p + i * DN_FETCH) / CPR;
-          id[i] = tok < end ? ldg_now(ids + (tok >> lg)) : -1;
-        }
-        ide = t0 + 4 * lane < end ? ldg_now(ids + (t0 + 4 * lane >> lg)) : -1;
+      // A thread's chunk and, in each pass, its row.  Rows of 4 or 8 chunks: eight
+      // neighbouring lanes have four chunks of two rows, an even and an odd one, whose
+      // float16 chunks 2c (or 2c + 1) are in eight different groups of banks; the
+      // passes are RPP rows apart, and the warp's 32 rows are a lane's each for the scales.
+      constexpr bool EVEN = CPR == 8 || CPR == 4;
+      constexpr int RPP = EVEN ? DN_FETCH / CPR : 1, RPW = RPP / 4;  // rows of a pass, of a warp
+      const int wl = warp & 3, sub = CPR == 8 ? lane >> 2 & 3 : lane >> 2, chunk = CPR == 8 ? (lane & 3) | lane >> 4 << 2 : lane & 3;
+      auto row_of = [&](int i) { return EVEN ? wl * RPW + sub + RPP * i : (p + i * DN_FETCH) / CPR; };
+      auto chunk_of = [&](int i) { return EVEN ? chunk : p + i * DN_FETCH - row_of(i) * CPR; };
+      int ids = -1, idn = -1;  // pages of tokens 16 j .. of the tile to be fetched next, j = lane & 7; of the one behind it
+      auto pages = [&](int tt) {
+        const int tok = tt * DN_TILE + 16 * (lane & 7);
+        return tok < held() ? ldg_now(list() + (tok >> lg)) : -1;
       };
       uint4 q[PASS] = {};
       uint32_t ex = 0;  // exponents of the lane's four tokens, the first `live` of them there
       int live = 0;
+      const bool any = w.n_pages > 0;
       // A chunk without a page is read from page 0 and put to zero in store(): the
       // loads stand in a row without branches.
-      auto fetch = [&]() {
-        if (w.n_pages == 0) return;
-        const uint32_t row0 = head_of() << lg;
-        const int t0 = x.tt * DN_TILE;
-#pragma unroll
-        for (int i = 0; i < PASS; ++i) {
-          const int z = p + i * DN_FETCH, row = z / CPR;
-          const uint32_t pg = static_cast<uint32_t>(id[i]) < static_cast<uint32_t>(w.n_pages) ? id[i] : 0;
-          q[i] = ldg_now16(src + pg * stride + (row0 + (t0 + row & pm)) * D + (z - row * CPR) * 16);
-        }
-        // (masked when it is used: nothing here waits for a load)
-        live = static_cast<uint32_t>(ide) < static_cast<uint32_t>(w.n_pages) ? min(max(held() - t0 - 4 * lane, 0), 4) : 0;
-        ex = ldg_now32((vs ? w.ve : w.ke) + ((static_cast<int64_t>(live ? ide : 0) * w.Hkv + head_of()) << lg) +
-                       (t0 + 4 * lane & pm));
+      auto page = [&](int row) {
+        const int id = __shfl_sync(~0u, ids, row >> 4);
+        return static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages) ? id : -1;
       };
-      auto store = [&](uint32_t dst, int E) {
-#pragma unroll
-        for (int i = 0; i < PASS; ++i) {
-          const int z = p + i * DN_FETCH, row = z / CPR, f = 2 * (z - row * CPR);
-          const int e = static_cast<int8_t>(__shfl_sync(~0u, ex, row >> 2) >> 8 * (row & 3));
-          const float one = pow2i(max(e - E, -126));  // e - E <= 7
-          const uint32_t two = pack<true>(one, one), is = e == -128 ? 0u : ~0u;
-          const __half2 sc = *reinterpret_cast<const __half2 *>(&two);
-          auto scaled = [&](uint32_t h) {
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), sc);
-            return *reinterpret_cast<const uint32_t *>(&y);
-          };
-          const uint4 b = make_uint4(q[i].x & is, q[i].y & is, q[i].z & is, q[i].w & is);
-          const uint4 lo4 = make_uint4(scaled(cvt_lo(b.x)), scaled(cvt_hi(b.x)), scaled(cvt_lo(b.y)), scaled(cvt_hi(b.y)));
-          const uint4 hi4 = make_uint4(scaled(cvt_lo(b.z)), scaled(cvt_hi(b.z)), scaled(cvt_lo(b.w)), scaled(cvt_hi(b.w)));
-          const uint32_t to = dst + (f >> 3) * (DN_TILE * 128) + row * 128;
-          const uint32_t c0 = ((f ^ row) & 7) << 4, c1 = ((f + 1 ^ row) & 7) << 4;
-          const bool swap = f & 8;  // lanes of one row: all eight chunk positions at once
-          sts128(to + (swap ? c1 : c0), swap ? hi4 : lo4);
-          sts128(to + (swap ? c0 : c1), swap ? lo4 : hi4);
-        }
+      auto load = [&](int i) {
+        const int row = row_of(i), pg = max(page(row), 0);
+        const uint32_t at = ((head_of() << lg) + (x.tt * DN_TILE + row & pm)) * D + chunk_of(i) * 16;
+        if (any) q[i] = ldg_now16(src + pg * stride + at);
       };
-      // the loads of a tile are issued when the tile before is stored
-      if (tiles > 0) pages(), fetch();
-      for (int t = 0; t < tiles; ++t) {
-        if (live < 4) {  // -128 where there is no token
-          const uint32_t in = (1u << 8 * live) - 1;
-          ex = (ex & in) | (0x80808080u & ~in);
-        }
-        int E = -128;  // seven below the tile's largest exponent
+      // (masked when they are used: nothing here waits for a load)
+      auto load_exps = [&]() {
+        const int t0 = x.tt * DN_TILE, id = page(4 * lane);
+        live = id >= 0 ? min(max(held() - t0 - 4 * lane, 0), 4) : 0;
+        if (any)
+          ex = ldg_now32((vs ? w.ve : w.ke) + ((static_cast<int64_t>(live ? id : 0) * w.Hkv + head_of()) << lg) +
+                         (t0 + 4 * lane & pm));
+      };
+      bool ahead = false;
+      // tile t goes to shared memory, then tile t + 1 is asked for (t = -1: the first one)
+#pragma unroll 1
+      for (int t = -1; t < tiles; ++t) {
+        const bool more = t + 1 < tiles;
+        if (t < 0) {
+          if (more) ids = pages(x.tt);
+          ahead = tiles > 1 && x.tt + 1 < x.nt;
+          if (ahead) idn = pages(x.tt + 1);
+        } else {
+          const bool partial = __any_sync(~0u, live < 4);
+          if (live < 4) {  // -128 where there is no token
+            const uint32_t in = (1u << 8 * live) - 1;
+            ex = (ex & in) | (0x80808080u & ~in);
+          }
+          int E = -128;  // seven below the tile's largest exponent
 #pragma unroll
-        for (int i = 0; i < 4; ++i) E = max(E, static_cast<int>(static_cast<int8_t>(ex >> 8 * i)));
-        E = max(__reduce_max_sync(~0u, E), kExpMin) - 7;
-        if (p == 0) {
-          S.exps[vs][t % DN_RING] = E;
-          bar_arrive(s32(&S.consts[t % DN_RING]));
-        }
-        if constexpr (OWN) {
-          if (vs) {
-            bool odd = false;
-            if (banded()) {
-              const int first = x.own - x.tt * DN_TILE;
+          for (int i = 0; i < 4; ++i) E = max(E, static_cast<int>(static_cast<int8_t>(ex >> 8 * i)));
+          E = max(__reduce_max_sync(~0u, E), kExpMin) - 7;
+          if (p == 0) {
+            S.exps[vs][t % DN_RING] = E;
+            bar_arrive(s32(&S.consts[t % DN_RING]));
+          }
+          if constexpr (OWN) {
+            if (vs) {
+              bool odd = false;
+              if (banded()) {
+                const int first = x.own - x.tt * DN_TILE;
 #pragma unroll
-              for (int i = 0; i < PASS; ++i) {
-                uint32_t *u = reinterpret_cast<uint32_t *>(&q[i]);
+                for (int i = 0; i < PASS; ++i) {
+                  uint32_t *u = reinterpret_cast<uint32_t *>(&q[i]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  uint32_t m = (((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 where the byte is NaN
-                  if ((p + i * DN_FETCH) / CPR < first) m = 0;
-                  odd |= m != 0;
-                  u[k] &= ~(m * 0xffu);
+                  for (int k = 0; k < 4; ++k) {
+                    uint32_t m = (((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 where the byte is NaN
+                    if (row_of(i) < first) m = 0;
+                    odd |= m != 0;
+                    u[k] &= ~(m * 0xffu);
+                  }
                 }
               }
+              odd = __any_sync(~0u, odd);
+              if (lane == 0) reinterpret_cast<volatile uint8_t *>(&S.hot[t % DN_RING])[wl] = odd;
             }
-            odd = __any_sync(~0u, odd);
-            if (lane == 0) reinterpret_cast<volatile uint8_t *>(&S.hot[t % DN_RING])[warp & 3] = odd;
           }
+          // the factors 2^(e - E) of the warp's rows, twice in a word: a lane each (e - E <= 7)
+          auto factor = [&](int e) {
+            const float one = pow2i(max(e - E, -126));
+            return pack<true>(one, one);
+          };
+          const int mine = wl * RPW + lane % (EVEN ? RPW : 1) + RPP * (lane / (EVEN ? RPW : 1));
+          const uint32_t was = ex;
+          const int exr = EVEN ? static_cast<int8_t>(__shfl_sync(~0u, was, mine >> 2 & 31) >> 8 * (mine & 3)) : 0;
+          const uint32_t factors = EVEN ? factor(exr) : 0;
+          if (more) {
+            step(x);
+            ids = ahead ? idn : pages(x.tt);
+          }
+          ahead = t + 2 < tiles && x.tt + 1 < x.nt;
+          if (ahead) idn = pages(x.tt + 1);
+          uint32_t two[PASS];
+          if constexpr (EVEN) {
+#pragma unroll
+            for (int i = 0; i < PASS; ++i) two[i] = __shfl_sync(~0u, factors, i * RPW + sub);
+            if (partial) {
+#pragma unroll
+              for (int i = 0; i < PASS; ++i) {
+                const uint32_t is = __shfl_sync(~0u, exr, i * RPW + sub) == -128 ? 0u : ~0u;
+                q[i].x &= is, q[i].y &= is, q[i].z &= is, q[i].w &= is;
+              }
+            }
+          }
+          if (t >= 2) bar_wait(s32(empty + (t & 1)), (t >> 1) - 1 & 1, dead);
+          const uint32_t dst = dst0 + (t & 1) * C::OP;
+#pragma unroll
+          for (int i = 0; i < PASS; ++i) {
+            const int row = row_of(i), f = 2 * chunk_of(i);
+            if constexpr (!EVEN) {
+              const int e = static_cast<int8_t>(__shfl_sync(~0u, was, row >> 2) >> 8 * (row & 3));
+              two[i] = factor(e);
+              const uint32_t is = e == -128 ? 0u : ~0u;
+              q[i].x &= is, q[i].y &= is, q[i].z &= is, q[i].w &= is;
+            }
+            const __half2 sc = *reinterpret_cast<const __half2 *>(&two[i]);
+            auto scaled = [&](uint32_t h) {
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), sc);
+              return *reinterpret_cast<const uint32_t *>(&y);
+            };
+            const uint4 b = q[i];
+            const uint4 lo4 = make_uint4(scaled(cvt_lo(b.x)), scaled(cvt_hi(b.x)), scaled(cvt_lo(b.y)), scaled(cvt_hi(b.y)));
+            const uint4 hi4 = make_uint4(scaled(cvt_lo(b.z)), scaled(cvt_hi(b.z)), scaled(cvt_lo(b.w)), scaled(cvt_hi(b.w)));
+            const uint32_t to = dst + (f >> 3) * (DN_TILE * 128) + row * 128;
+            const uint32_t c0 = ((f ^ row) & 7) << 4, c1 = ((f + 1 ^ row) & 7) << 4;
+            const bool swap = !EVEN && f & 8;  // lanes of one row: all eight chunk positions at once
+            sts128(to + (swap ? c1 : c0), swap ? hi4 : lo4);
+            sts128(to + (swap ? c0 : c1), swap ? lo4 : hi4);
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) bar_arrive(s32(full + (t & 1)));
         }
-        if (t + 1 < tiles) step(x), pages();
-        if (t >= 2) bar_wait(s32(empty + (t & 1)), (t >> 1) - 1 & 1, dead);
-        store(dst0 + (t & 1) * C::OP, E);
-        fence_async();
-        __syncwarp();
-        if (lane == 0) bar_arrive(s32(full + (t & 1)));
-        if (t + 1 < tiles) fetch();
+        if (more) {
+#pragma unroll
+          for (int i = 0; i < PASS; ++i) load(i);
+          load_exps();
+        }
       }
     } else {
       constexpr int CPR = D / 8;
+#pragma unroll 1
       for (int t = 0; t < tiles; ++t) {
         if (t >= 2) bar_wait(s32(empty + (t & 1)), (t >> 1) - 1 & 1, dead);
         const uint32_t row0 = head_of() << lg, dst = dst0 + (t & 1) * C::OP;
@@ -701,17 +755,20 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       }
       __syncwarp();
     };
-    for (int t = 0; t < tiles; ++t) {
-      // the next half tile's scores before these weights, except behind an item's
-      // last, whose output has to be out before the next item's queries are in
+    // The next half tile's scores come before these weights, except behind an item's
+    // last, whose output has to be out before the next item's queries are in.  (One
+    // copy each of the two in the code: the roles' loops together are to stay in the
+    // instruction cache.)
+    int next = 0;
+#pragma unroll 1
+    for (int u = 0; u < 2 * tiles; ++u) {
       const int tt = __shfl_sync(~0u, x.tt, 0);
-      const bool last = __shfl_sync(~0u, x.tt + 1 == x.nt || t + 1 == tiles, 0);
-      if (t == 0 || tt == 0) scores(2 * t, tt);
-      scores(2 * t + 1, tt);
-      values(2 * t, tt, last);
-      if (!last) scores(2 * t + 2, tt + 1);
-      values(2 * t + 1, tt, last);
-      if (t + 1 < tiles) step(x);
+      const bool last = __shfl_sync(~0u, x.tt + 1 == x.nt || (u >> 1) + 1 == tiles, 0);
+      const int upto = (u & 1) && last ? u : u + 1;
+#pragma unroll 1
+      for (; next <= upto; ++next) scores(next, tt + (next >> 1) - (u >> 1));
+      values(u, tt, last);
+      if ((u & 1) && (u >> 1) + 1 < tiles) step(x);
     }
     if (elected()) drained(half);
     __syncwarp();

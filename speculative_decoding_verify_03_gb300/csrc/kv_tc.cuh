@@ -22,6 +22,7 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 // behind a wait runs to its end either way, so that no barrier of the CTA is
 // left waiting; the CTA's results are then marked invalid.
 __device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t *dead) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kPolls; ++i) {
     uint32_t ok;
     asm volatile(
