@@ -281,6 +281,7 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
                                                           : dense_bf16(P, D, L.tiles_p, &m.cp, s);
     if (e != cudaSuccess) return SPEC_ERR_CUDA;
   }
+  P.behind = P.w.prefix > 0;
   P.prefix = 0;
   P.mask = mask;
   P.mask_words = (P.w.N + 31) / 32;

@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   uint32_t *cum1 = cum + P.w.B + 1;
   const uint32_t base = s32(sm);
 
+  cudaTriggerProgrammaticLaunchCompletion();  // for the call's next kernel (launch())
   const View &w = P.w;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = P.G, B = w.B;
@@ -520,21 +521,26 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       uint32_t ex = 0;  // exponents of the lane's four tokens, the first `live` of them there
       int live = 0;
       const bool any = w.n_pages > 0;
-      // A chunk without a page is read from page 0 and put to zero in store(): the
-      // loads stand in a row without branches.
-      auto page = [&](int row) {
-        const int id = __shfl_sync(~0u, ids, row >> 4);
-        return static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages) ? id : -1;
+      // A chunk without a page is read from page 0 and put to zero below: the loads
+      // stand in a row without branches.  Where tokens 16 j .. of the tile begin is worked
+      // out once, by lane j; a pass's rows are a few of 16 such.
+      auto page = [&](int id) { return static_cast<uint32_t>(id) < static_cast<uint32_t>(w.n_pages); };
+      const uint8_t *begins = src;
+      auto places = [&]() {
+        const int id = page(ids) ? ids : 0;
+        const uint32_t in = (head_of() << lg) + (x.tt * DN_TILE + 16 * (lane & 7) & pm);
+        begins = src + id * stride + static_cast<uint64_t>(in) * D;
       };
       auto load = [&](int i) {
-        const int row = row_of(i), pg = max(page(row), 0);
-        const uint32_t at = ((head_of() << lg) + (x.tt * DN_TILE + row & pm)) * D + chunk_of(i) * 16;
-        if (any) q[i] = ldg_now16(src + pg * stride + at);
+        const int row = row_of(i);
+        const uint8_t *from = reinterpret_cast<const uint8_t *>(
+            __shfl_sync(~0u, reinterpret_cast<unsigned long long>(begins), CPR == 8 ? i : row >> 4));
+        if (any) q[i] = ldg_now16(from + ((row & 15) * D + chunk_of(i) * 16));
       };
       // (masked when they are used: nothing here waits for a load)
       auto load_exps = [&]() {
-        const int t0 = x.tt * DN_TILE, id = page(4 * lane);
-        live = id >= 0 ? min(max(held() - t0 - 4 * lane, 0), 4) : 0;
+        const int t0 = x.tt * DN_TILE, id = __shfl_sync(~0u, ids, lane >> 2);
+        live = page(id) ? min(max(held() - t0 - 4 * lane, 0), 4) : 0;
         if (any)
           ex = ldg_now32((vs ? w.ve : w.ke) + ((static_cast<int64_t>(live ? id : 0) * w.Hkv + head_of()) << lg) +
                          (t0 + 4 * lane & pm));
@@ -640,6 +646,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           if (lane == 0) bar_arrive(s32(full + (t & 1)));
         }
         if (more) {
+          places();
 #pragma unroll
           for (int i = 0; i < PASS; ++i) load(i);
           load_exps();
@@ -779,6 +786,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   tc_after();
   if (warp == 16) tmem_free(tmem, 512);
   if (tid == 0) P.plan.lost[blockIdx.x] = S.dead;
+  wait_for_first(P);
 }
 
 template <int D, bool E4M3, bool OWN = false>
@@ -795,8 +803,7 @@ cudaError_t dense_go(const SpanParams &p, int64_t tiles, int *grid, cudaStream_t
   if (n > tiles) n = tiles;
   if (n < 1) n = 1;
   *grid = static_cast<int>(n);
-  f<<<*grid, DN_NT, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch(f, *grid, DN_NT, smem, s, p);
 }
 
 }  // namespace kv

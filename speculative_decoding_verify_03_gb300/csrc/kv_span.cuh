@@ -204,7 +204,10 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
   const int pnt = (w.prefix + kTile - 1) / kTile, pnj = (rows_all + RT - 1) / RT;
   const uint32_t W = pre ? static_cast<uint32_t>(pnt) * pnj * w.Hkv : cum0[B];
   const uint32_t ctas = min(gridDim.x, W);  // every one of them has a tile
-  if (blockIdx.x >= ctas) return;
+  if (blockIdx.x >= ctas) {
+    wait_for_first(P);
+    return;
+  }
   const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(W) * blockIdx.x / ctas);
   const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(W) * (blockIdx.x + 1) / ctas);
 
@@ -753,6 +756,7 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
     }
   }
   cp_wait<0>();
+  wait_for_first(P);
 }
 
 template <int D, bool E4M3, int WR, int WT, bool TREE>
@@ -772,8 +776,7 @@ cudaError_t span_go(const SpanParams &p, int64_t tiles, int *grid, cudaStream_t 
   if (n > tiles) n = tiles;
   if (n < 1) n = 1;
   *grid = static_cast<int>(n);
-  f<<<*grid, C::NT, smem, s>>>(p);
-  return cudaGetLastError();
+  return launch(f, *grid, C::NT, smem, s, p);
 }
 
 template <int D, bool E4M3, bool TREE = false>

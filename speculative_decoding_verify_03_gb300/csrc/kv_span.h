@@ -38,6 +38,7 @@ struct SpanParams {
   int32_t prefix;         // 1: prefix items
   bool qvec;              // q rows are 4-byte aligned; 16-byte (dense kernel, 16 rows)
   const int32_t *mask;    // trees: [B, N, mask_words]
+  bool behind;            // a kernel of the same call was launched before
   int32_t mask_words;
 };
 
@@ -101,6 +102,28 @@ __device__ __forceinline__ uint64_t seen_nodes(const int32_t *row, int words, in
   const uint64_t see = static_cast<uint64_t>(__funnelshift_r(x[1], x[2], off & 31)) << 32 | __funnelshift_r(x[0], x[1], off & 31);
   const int left = n - off;
   return left >= 64 ? see : left <= 0 ? 0 : see & ((1ull << left) - 1);
+}
+
+// Launches one of the attention kernels.  The second one of a call begins while the
+// first still runs, on multiprocessors that are done with it: neither reads what the
+// other writes.  It ends behind the first one's end (wait_for_first), so that
+// whoever waits for the second waits for both.
+template <class F>
+cudaError_t launch(F *f, int grid, int threads, int smem, cudaStream_t s, const SpanParams &p) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.behind ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, f, p);
+}
+__device__ __forceinline__ void wait_for_first(const SpanParams &p) {
+  if (p.behind) cudaGridDependencySynchronize();
 }
 
 // The dense kernel: prefix items of DN_ROWS rows, tiles of 128 tokens.
