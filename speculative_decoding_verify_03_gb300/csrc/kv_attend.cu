@@ -161,7 +161,16 @@ int row_warps(int64_t rows) {
 constexpr int64_t kDenseRows = 65;
 
 // Query rows of a sequence's key/value head from which a tree's own tokens go to the
-// dense kernel.
+// dense kernel: from the 65th on the span kernel reads the keys again.  Measured, 8
+// key/value heads of 128 in e4m3, sequences x tokens, replayed calls, span / dense
+// kernel in us:
+//   rows   1 x 100   1 x 8000   8 x 500   8 x 4000   64 x 100   64 x 1000
+//     48   12 / 15    47 / 33   20 / 26    50 / 54    35 / 47     88 / 106
+//     64   12 / 15    45 / 33   29 / 28    54 / 56    42 / 51    106 / 110
+//     80   12 / 15    42 / 33   28 / 28    69 / 56    54 / 56    150 / 115
+//    128   13 / 16    43 / 34   32 / 29    84 / 57    81 / 79    207 / 140
+//    256   14 / 19    57 / 38   45 / 40   152 / 69   157 / 128   398 / 195
+// Heads of 64 and bfloat16 caches cross over at the same rows.
 constexpr int64_t kDenseTreeRows = 65;
 static_assert(2 * kMaxDense <= kMaxGrid, "plan: words for the CTAs of both dense launches");
 
@@ -276,12 +285,14 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
     P.pl = reinterpret_cast<float *>(ws + L.ql);
     m.qo = P.po, m.ql = P.pl;
     P.qvec = qbits % (L.dense || L.wp == 1 ? 16 : 4) == 0;
+    P.halves = static_cast<int64_t>(P.w.N) * G * P.w.B <= DN_ROWS / 2 ? 1 : 2;
     const cudaError_t e = !L.dense ? span(P, L.wp, L.tiles_p, &m.cp, s)
                           : cache->format == SPEC_KV_E4M3 ? dense_e4m3(P, D, L.tiles_p, &m.cp, s)
                                                           : dense_bf16(P, D, L.tiles_p, &m.cp, s);
     if (e != cudaSuccess) return SPEC_ERR_CUDA;
   }
   P.behind = P.w.prefix > 0;
+  P.halves = static_cast<int64_t>(P.w.N) * G <= DN_ROWS / 2 ? 1 : 2;
   P.prefix = 0;
   P.mask = mask;
   P.mask_words = (P.w.N + 31) / 32;

@@ -27,7 +27,8 @@
 // 8-11 bring keys, 12-15 values into shared memory (e4m3 through registers as
 // float16, a tile ahead, bfloat16 by asynchronous copies); warps 16 and 17
 // issue the products of a row tile each, as soon as its operands are there.
-// Two stages of keys and of values.
+// Two stages of keys and of values.  Where no item has more than 128 rows the second
+// row tile's warps stand aside.
 //
 // Measured: 256 x 9 queries of 32 heads (9216 rows a key/value head of 128) over
 // 8192 e4m3 tokens 437 us, 707 TFLOP/s, 37 % of the products' rate; tensor pipe 31 %
@@ -121,8 +122,8 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   // --- rows before each sequence
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      bar_init(s32(&S.kfull[i]), E4M3 ? DN_FETCH / 32 : DN_FETCH), bar_init(s32(&S.kempty[i]), 2);
-      bar_init(s32(&S.vfull[i]), E4M3 ? DN_FETCH / 32 : DN_FETCH), bar_init(s32(&S.vempty[i]), 2);
+      bar_init(s32(&S.kfull[i]), E4M3 ? DN_FETCH / 32 : DN_FETCH), bar_init(s32(&S.kempty[i]), P.halves);
+      bar_init(s32(&S.vfull[i]), E4M3 ? DN_FETCH / 32 : DN_FETCH), bar_init(s32(&S.vempty[i]), P.halves);
       for (int k = 0; k < 2; ++k) bar_init(s32(&S.sfull[i][k]), 1), bar_init(s32(&S.pfull[i][k]), 4);
       bar_init(s32(&S.odone[i]), 1), bar_init(s32(&S.ofull[i]), 1), bar_init(s32(&S.drain[i]), 1);
     }
@@ -252,234 +253,236 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   };
 
   if (warp < 8) {
-    regs_to<DN_SOFT, DN_REGS>();
-    // ================================================= softmax and output
-    const int half = warp >> 2;
-    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 TMEM lanes a warp
-    const uint32_t oc = tmem + lanes + 256 + half * 128;
-    const uint32_t wb = base + C::Q + half * C::OP + (warp & 3) * 32 * 128;  // the warp's query rows
-    const int r = tid;  // row of the item
-    DenseAt x = begin();
-    float M = kNone, l = 0.0f, qc = 0.0f;
-    float kt = 0.0f, F = 0.0f, invF = 1.0f;  // of the tile
-    bool fresh = true;
-    int node = -1;  // own items: the row's place in the step
-    int begun = 0;  // own items: the CTA's first tile of the item
-    int g = 0;  // items
+    if (warp < 4 * P.halves) {
+      regs_to<DN_SOFT, DN_REGS>();
+      // ================================================= softmax and output
+      const int half = warp >> 2;
+      const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 TMEM lanes a warp
+      const uint32_t oc = tmem + lanes + 256 + half * 128;
+      const uint32_t wb = base + C::Q + half * C::OP + (warp & 3) * 32 * 128;  // the warp's query rows
+      const int r = tid;  // row of the item
+      DenseAt x = begin();
+      float M = kNone, l = 0.0f, qc = 0.0f;
+      float kt = 0.0f, F = 0.0f, invF = 1.0f;  // of the tile
+      bool fresh = true;
+      int node = -1;  // own items: the row's place in the step
+      int begun = 0;  // own items: the CTA's first tile of the item
+      int g = 0;  // items
 #pragma unroll 1
-    for (int u = 0; u < 2 * tiles; ++u) {
-      const int t = u >> 1;  // half u & 1 of tile t
-      if (fresh) {  // the row's query; the products with the item before are done
-        const uint32_t row = (OWN ? x.rt : x.item % nj) * DN_ROWS + r;
-        int64_t off = -1;
-        if (OWN) {
-          node = -1;
-          if (row < static_cast<uint32_t>(x.n * G)) {
-            node = row / G;
-            off = x.b * P.qs0 + node * P.qs1 + (x.head * G + static_cast<int>(row) - node * G) * P.qs2;
-          }
-        } else if (row < rows) {
-          int b = 0, h = B;
-          while (h - b > 1) {
-            const int m = (b + h) >> 1;
-            if (cum[m] <= row) b = m;
-            else h = m;
-          }
-          const int y = row - cum[b], i = y / G;
-          off = b * P.qs0 + i * P.qs1 + (x.item / nj * G + y - i * G) * P.qs2;
-        }
-        // into shared memory by the warp's 32 rows together, neighbouring lanes
-        // neighbouring chunks; then a row by its own thread
-        // (loops, not one long piece of code: an item's first tile would wait for its
-        // instructions)
-        constexpr int CH = D / 8;
-        auto at = [&](int y, int c) {
-          return wb + (c >> 3) * (DN_TILE * 128) + y * 128 + (((c ^ y) & 7) << 4);
-        };
-        if (P.qvec) {
-#pragma unroll 4
-          for (int k = 0; k < CH; ++k) {
-            const int z = lane + 32 * k, y = z / CH, c = z - y * CH;
-            const int64_t o = __shfl_sync(~0u, off, y);
-            cp16(at(y, c), P.q + (o < 0 ? 0 : o + 8 * c), o >= 0);
-          }
-          cp_commit();
-          cp_wait<0>();
-        } else {
-#pragma unroll 1
-          for (int k = 0; k < CH; ++k) {
-            const int z = lane + 32 * k, y = z / CH, c = z - y * CH;
-            const int64_t o = __shfl_sync(~0u, off, y);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (o >= 0) {
-              const uint16_t *u = reinterpret_cast<const uint16_t *>(P.q + o + 8 * c);
-              v = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+      for (int u = 0; u < 2 * tiles; ++u) {
+        const int t = u >> 1;  // half u & 1 of tile t
+        if (fresh) {  // the row's query; the products with the item before are done
+          const uint32_t row = (OWN ? x.rt : x.item % nj) * DN_ROWS + r;
+          int64_t off = -1;
+          if (OWN) {
+            node = -1;
+            if (row < static_cast<uint32_t>(x.n * G)) {
+              node = row / G;
+              off = x.b * P.qs0 + node * P.qs1 + (x.head * G + static_cast<int>(row) - node * G) * P.qs2;
             }
-            sts128(at(y, c), v);
+          } else if (row < rows) {
+            int b = 0, h = B;
+            while (h - b > 1) {
+              const int m = (b + h) >> 1;
+              if (cum[m] <= row) b = m;
+              else h = m;
+            }
+            const int y = row - cum[b], i = y / G;
+            off = b * P.qs0 + i * P.qs1 + (x.item / nj * G + y - i * G) * P.qs2;
           }
-        }
-        qc = P.c;
-        if constexpr (E4M3) {
-          // bring the row's largest finite magnitude to [2^10, 2^11): exact in
-          // float16 for all elements above 2^-28 of it
+          // into shared memory by the warp's 32 rows together, neighbouring lanes
+          // neighbouring chunks; then a row by its own thread
+          // (loops, not one long piece of code: an item's first tile would wait for its
+          // instructions)
+          constexpr int CH = D / 8;
+          auto at = [&](int y, int c) {
+            return wb + (c >> 3) * (DN_TILE * 128) + y * 128 + (((c ^ y) & 7) << 4);
+          };
+          if (P.qvec) {
+#pragma unroll 4
+            for (int k = 0; k < CH; ++k) {
+              const int z = lane + 32 * k, y = z / CH, c = z - y * CH;
+              const int64_t o = __shfl_sync(~0u, off, y);
+              cp16(at(y, c), P.q + (o < 0 ? 0 : o + 8 * c), o >= 0);
+            }
+            cp_commit();
+            cp_wait<0>();
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < CH; ++k) {
+              const int z = lane + 32 * k, y = z / CH, c = z - y * CH;
+              const int64_t o = __shfl_sync(~0u, off, y);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (o >= 0) {
+                const uint16_t *u = reinterpret_cast<const uint16_t *>(P.q + o + 8 * c);
+                v = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+              }
+              sts128(at(y, c), v);
+            }
+          }
+          qc = P.c;
+          if constexpr (E4M3) {
+            // bring the row's largest finite magnitude to [2^10, 2^11): exact in
+            // float16 for all elements above 2^-28 of it
+            __syncwarp();
+            uint32_t m = 0;
+            auto most = [&](uint32_t u) {
+              const uint32_t a = u & 0x7fffu, b = u >> 16 & 0x7fffu;
+              m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+            };
+#pragma unroll 2
+            for (int k = 0; k < CH; ++k) {
+              const uint4 v = lds128(at(lane, k));
+              most(v.x), most(v.y), most(v.z), most(v.w);
+            }
+            const int eq = max(static_cast<int>(m >> 7) - 127 - 10, -100);
+            qc = P.c * pow2i(eq);
+            const float f = pow2i(-eq);
+            auto two = [&](uint32_t u) {
+              return pack<true>(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
+            };
+#pragma unroll 2
+            for (int k = 0; k < CH; ++k) {
+              const uint4 v = lds128(at(lane, k));
+              sts128(at(lane, k), make_uint4(two(v.x), two(v.y), two(v.z), two(v.w)));
+            }
+          }
+          fence_async();
           __syncwarp();
-          uint32_t m = 0;
-          auto most = [&](uint32_t u) {
-            const uint32_t a = u & 0x7fffu, b = u >> 16 & 0x7fffu;
-            m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
-          };
-#pragma unroll 2
-          for (int k = 0; k < CH; ++k) {
-            const uint4 v = lds128(at(lane, k));
-            most(v.x), most(v.y), most(v.z), most(v.w);
-          }
-          const int eq = max(static_cast<int>(m >> 7) - 127 - 10, -100);
-          qc = P.c * pow2i(eq);
-          const float f = pow2i(-eq);
-          auto two = [&](uint32_t u) {
-            return pack<true>(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xffff0000u) * f);
-          };
-#pragma unroll 2
-          for (int k = 0; k < CH; ++k) {
-            const uint4 v = lds128(at(lane, k));
-            sts128(at(lane, k), make_uint4(two(v.x), two(v.y), two(v.z), two(v.w)));
+          if (lane == 0) bar_arrive(s32(&S.qfull[half]));
+          M = kNone, l = 0.0f;
+          begun = t;
+        }
+        if (!(u & 1)) {
+          kt = qc;
+          if constexpr (E4M3) {
+            bar_wait(s32(&S.consts[t % DN_RING]), t / DN_RING & 1, dead);
+            const int fe = S.exps[1][t % DN_RING];
+            kt = qc * pow2i(S.exps[0][t % DN_RING]);
+            F = static_cast<float>(fe);
+            invF = pow2i(-fe - 13) * (SUM * 0x1p13f);  // 2^-F SUM, subnormal for the largest F
           }
         }
-        fence_async();
+        const uint32_t sc = tmem + lanes + half * 128 + (u & 1) * 64;
+        bar_wait(s32(&S.sfull[half][u & 1]), t & 1, dead);
+        tc_after();
+        float s[64];
+#pragma unroll
+        for (int c = 0; c < 64; c += 16) tmem_ld16(sc + c, s + c);
+        tmem_wait_ld(s, 64);
+        // tokens from here on that all rows see
+        const int n = (OWN ? x.own : w.prefix) - x.tt * DN_TILE - (u & 1) * 64;
+        float ks = kt;  // still to be multiplied by
+        if (n < 64) {   // masked behind the multiplication: a factor of 0 would make NaN of -inf
+          ks = 1.0f;
+          if constexpr (OWN) {
+            uint64_t see = 0;
+            if (node >= 0)
+              see = seen_nodes(P.mask + (static_cast<int64_t>(x.b) * w.N + node) * P.mask_words, P.mask_words, x.n, -n);
+            const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] = (c < 32 ? see0 : see1) >> (c & 31) & 1 ? s[c] * kt : -INFINITY;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[c] = c >= n ? -INFINITY : s[c] * kt;
+          }
+        }
+        float m2[2] = {s[0], s[1]};
+#pragma unroll
+        for (int c = 2; c < 62; c += 4) m2[0] = max3(m2[0], s[c], s[c + 1]), m2[1] = max3(m2[1], s[c + 2], s[c + 3]);
+        const float m = fmaf(max3(fmaxf(m2[0], m2[1]), s[62], s[63]), ks, F);
+        if (__any_sync(~0u, fresh || m > M + SLACK)) {
+          const float nm = fmaxf(M, m), f = ex2(M - nm);
+          M = nm;
+          l *= f;
+          if (!fresh) {
+            bar_wait(s32(&S.odone[half]), u - 1 & 1, dead);  // products up to the half tile before
+            tc_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tmem_ld16(oc + c, o);
+              tmem_wait_ld(o, 16);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tmem_st16(oc + c, reinterpret_cast<const uint32_t *>(o));
+            }
+            tmem_wait_st();
+          }
+        }
+        const float2 k2 = {ks, ks}, b2 = {F - M + BIAS, F - M + BIAS};
+        float2 acc[2] = {{0, 0}, {0, 0}};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 z = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), k2, b2);
+            z.x = ex2(z.x), z.y = ex2(z.y);
+            acc[i & 1] = add2(acc[i & 1], z);
+            p[i] = pack<E4M3>(z.x, z.y);
+          }
+          tmem_st16(sc + 16 * c, p);  // over scores that are read
+        }
+        acc[0] = add2(acc[0], acc[1]);
+        l = fmaf(acc[0].x + acc[0].y, invF, l);
+        tmem_wait_st();
+        tc_before();
         __syncwarp();
-        if (lane == 0) bar_arrive(s32(&S.qfull[half]));
-        M = kNone, l = 0.0f;
-        begun = t;
-      }
-      if (!(u & 1)) {
-        kt = qc;
-        if constexpr (E4M3) {
-          bar_wait(s32(&S.consts[t % DN_RING]), t / DN_RING & 1, dead);
-          const int fe = S.exps[1][t % DN_RING];
-          kt = qc * pow2i(S.exps[0][t % DN_RING]);
-          F = static_cast<float>(fe);
-          invF = pow2i(-fe - 13) * (SUM * 0x1p13f);  // 2^-F SUM, subnormal for the largest F
-        }
-      }
-      const uint32_t sc = tmem + lanes + half * 128 + (u & 1) * 64;
-      bar_wait(s32(&S.sfull[half][u & 1]), t & 1, dead);
-      tc_after();
-      float s[64];
-#pragma unroll
-      for (int c = 0; c < 64; c += 16) tmem_ld16(sc + c, s + c);
-      tmem_wait_ld(s, 64);
-      // tokens from here on that all rows see
-      const int n = (OWN ? x.own : w.prefix) - x.tt * DN_TILE - (u & 1) * 64;
-      float ks = kt;  // still to be multiplied by
-      if (n < 64) {   // masked behind the multiplication: a factor of 0 would make NaN of -inf
-        ks = 1.0f;
-        if constexpr (OWN) {
-          uint64_t see = 0;
-          if (node >= 0)
-            see = seen_nodes(P.mask + (static_cast<int64_t>(x.b) * w.N + node) * P.mask_words, P.mask_words, x.n, -n);
-          const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
-#pragma unroll
-          for (int c = 0; c < 64; ++c) s[c] = (c < 32 ? see0 : see1) >> (c & 31) & 1 ? s[c] * kt : -INFINITY;
-        } else {
-#pragma unroll
-          for (int c = 0; c < 64; ++c) s[c] = c >= n ? -INFINITY : s[c] * kt;
-        }
-      }
-      float m2[2] = {s[0], s[1]};
-#pragma unroll
-      for (int c = 2; c < 62; c += 4) m2[0] = max3(m2[0], s[c], s[c + 1]), m2[1] = max3(m2[1], s[c + 2], s[c + 3]);
-      const float m = fmaf(max3(fmaxf(m2[0], m2[1]), s[62], s[63]), ks, F);
-      if (__any_sync(~0u, fresh || m > M + SLACK)) {
-        const float nm = fmaxf(M, m), f = ex2(M - nm);
-        M = nm;
-        l *= f;
-        if (!fresh) {
-          bar_wait(s32(&S.odone[half]), u - 1 & 1, dead);  // products up to the half tile before
+        if (lane == 0) bar_arrive(s32(&S.pfull[half][u & 1]));
+
+        const bool last = (u & 1) && (x.tt + 1 == x.nt || t + 1 == tiles);
+        if (last) {
+          const uint32_t slot = (OWN ? cum1[x.b] + x.head * x.per + x.rt : x.item) + blockIdx.x;
+          const int64_t at = static_cast<int64_t>(slot) * DN_ROWS + r;
+          const bool there = OWN ? node >= 0 : static_cast<uint32_t>(x.item % nj * DN_ROWS + r) < rows;
+          const float f = l == 0.0f ? 0.0f : 1.0f / l;
+          if (there) P.pl[at] = l == 0.0f ? -INFINITY : M - (BIAS - SUM_LOG) + log2f(l);
+          bar_wait(s32(&S.ofull[half]), g++ & 1, dead);
           tc_after();
+          int hot0 = t + 1;  // own items: the first tile that values were taken out of
+          if constexpr (OWN) {
+            const volatile uint32_t *hot = S.hot;
+            for (int k = t; k >= begun && (x.tt - (t - k) + 1) * DN_TILE > x.own; --k)
+              if (hot[k % DN_RING]) hot0 = k;
+          }
+          // rows leave through the shared memory of the item's queries, 16 columns
+          // at a time in two buffers, so that a store covers whole sectors
+          float *dst = P.po + (at - lane) * D + (lane & 3) * 4;
+          const uint32_t there32 = __ballot_sync(~0u, there);
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
+            const uint32_t buf = wb + (c & 16) * 128;
             float o[16];
             tmem_ld16(oc + c, o);
             tmem_wait_ld(o, 16);
+            if (OWN && hot0 <= t && node >= 0) {  // rare: to the rows that see them
+              const int t0 = (x.tt - (t - hot0)) * DN_TILE;
+              float more[16] = {};
+              add_odd<D, E4M3>(w, x.b, x.head, x.own, t0, min(x.own + x.n, (x.tt + 1) * DN_TILE),
+                               P.mask + (static_cast<int64_t>(x.b) * w.N + node) * P.mask_words, c, more);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= f;
-            tmem_st16(oc + c, reinterpret_cast<const uint32_t *>(o));
+              for (int i = 0; i < 16; ++i) o[i] += more[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sts128(buf + lane * 64 + ((i ^ lane >> 1) & 3) * 16,
+                     make_uint4(__float_as_uint(o[4 * i] * SUM * f), __float_as_uint(o[4 * i + 1] * SUM * f),
+                                __float_as_uint(o[4 * i + 2] * SUM * f), __float_as_uint(o[4 * i + 3] * SUM * f)));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int y = 8 * i + (lane >> 2);
+              const uint4 x = lds128(buf + y * 64 + ((lane ^ y >> 1) & 3) * 16);
+              if (there32 >> y & 1) *reinterpret_cast<uint4 *>(dst + y * D + c) = x;
+            }
           }
-          tmem_wait_st();
-        }
-      }
-      const float2 k2 = {ks, ks}, b2 = {F - M + BIAS, F - M + BIAS};
-      float2 acc[2] = {{0, 0}, {0, 0}};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 z = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), k2, b2);
-          z.x = ex2(z.x), z.y = ex2(z.y);
-          acc[i & 1] = add2(acc[i & 1], z);
-          p[i] = pack<E4M3>(z.x, z.y);
-        }
-        tmem_st16(sc + 16 * c, p);  // over scores that are read
-      }
-      acc[0] = add2(acc[0], acc[1]);
-      l = fmaf(acc[0].x + acc[0].y, invF, l);
-      tmem_wait_st();
-      tc_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(s32(&S.pfull[half][u & 1]));
-
-      const bool last = (u & 1) && (x.tt + 1 == x.nt || t + 1 == tiles);
-      if (last) {
-        const uint32_t slot = (OWN ? cum1[x.b] + x.head * x.per + x.rt : x.item) + blockIdx.x;
-        const int64_t at = static_cast<int64_t>(slot) * DN_ROWS + r;
-        const bool there = OWN ? node >= 0 : static_cast<uint32_t>(x.item % nj * DN_ROWS + r) < rows;
-        const float f = l == 0.0f ? 0.0f : 1.0f / l;
-        if (there) P.pl[at] = l == 0.0f ? -INFINITY : M - (BIAS - SUM_LOG) + log2f(l);
-        bar_wait(s32(&S.ofull[half]), g++ & 1, dead);
-        tc_after();
-        int hot0 = t + 1;  // own items: the first tile that values were taken out of
-        if constexpr (OWN) {
-          const volatile uint32_t *hot = S.hot;
-          for (int k = t; k >= begun && (x.tt - (t - k) + 1) * DN_TILE > x.own; --k)
-            if (hot[k % DN_RING]) hot0 = k;
-        }
-        // rows leave through the shared memory of the item's queries, 16 columns
-        // at a time in two buffers, so that a store covers whole sectors
-        float *dst = P.po + (at - lane) * D + (lane & 3) * 4;
-        const uint32_t there32 = __ballot_sync(~0u, there);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          const uint32_t buf = wb + (c & 16) * 128;
-          float o[16];
-          tmem_ld16(oc + c, o);
-          tmem_wait_ld(o, 16);
-          if (OWN && hot0 <= t && node >= 0) {  // rare: to the rows that see them
-            const int t0 = (x.tt - (t - hot0)) * DN_TILE;
-            float more[16] = {};
-            add_odd<D, E4M3>(w, x.b, x.head, x.own, t0, min(x.own + x.n, (x.tt + 1) * DN_TILE),
-                             P.mask + (static_cast<int64_t>(x.b) * w.N + node) * P.mask_words, c, more);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] += more[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            sts128(buf + lane * 64 + ((i ^ lane >> 1) & 3) * 16,
-                   make_uint4(__float_as_uint(o[4 * i] * SUM * f), __float_as_uint(o[4 * i + 1] * SUM * f),
-                              __float_as_uint(o[4 * i + 2] * SUM * f), __float_as_uint(o[4 * i + 3] * SUM * f)));
           __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int y = 8 * i + (lane >> 2);
-            const uint4 x = lds128(buf + y * 64 + ((lane ^ y >> 1) & 3) * 16);
-            if (there32 >> y & 1) *reinterpret_cast<uint4 *>(dst + y * D + c) = x;
-          }
+          tc_before();
         }
-        __syncwarp();
-        tc_before();
+        fresh = last;
+        if ((u & 1) && t + 1 < tiles) step(x);
       }
-      fresh = last;
-      if ((u & 1) && t + 1 < tiles) step(x);
     }
   } else if (warp < 16) {
     regs_to<DN_LOAD, DN_REGS>();
@@ -705,7 +708,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   } else {
     regs_to<DN_REST, DN_REGS>();
     // =========================================================== products
-    if (warp < 18) {
+    if (warp < 16 + P.halves) {
     // one lane issues, chosen by elect.sync, and all that its products are
     // described by is the warp's: kept in uniform registers, where they are wanted
     const int half = __shfl_sync(~0u, warp, 0) - 16;

@@ -39,6 +39,7 @@ struct SpanParams {
   bool qvec;              // q rows are 4-byte aligned; 16-byte (dense kernel, 16 rows)
   const int32_t *mask;    // trees: [B, N, mask_words]
   bool behind;            // a kernel of the same call was launched before
+  int32_t halves;         // dense kernel: 1 where no item has more than 128 rows, else 2
   int32_t mask_words;
 };
 
