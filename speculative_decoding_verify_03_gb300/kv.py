@@ -104,11 +104,11 @@ class KVCache:
 
 def _int32(name, t, n, device):
     """A contiguous int32 vector of n elements on the cache's device."""
-    if t.dtype != _i32:
+    if t.dtype is not _i32:
         raise TypeError(f"{name} must be int32")
-    if t.dim() != 1 or t.shape[0] != n or t.device != device:
+    if t.shape != (n,) or t.device != device:
         raise ValueError(f"{name} must be [{n}] on {device}")
-    if n > 1 and t.stride(0) != 1:
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
@@ -388,18 +388,19 @@ def spec_kv_compact(cache, page_table, kv_len, path, accepted_len, prefix_len=0,
 
 
 def _pool(refs, page_table, held, page_size, prefix_len):
-    dev = refs.device
-    n_pages = _int32("refs", refs, refs.shape[0] if refs.dim() == 1 else -1, dev)
+    dev, n_pages = refs.device, refs.numel()
+    counts = _int32("refs", refs, n_pages, dev)
     if page_table.dtype is not _i32:
         raise TypeError("page_table must be int32")
-    if page_table.dim() != 2 or page_table.device != dev:
+    shape = page_table.shape
+    if len(shape) != 2 or page_table.device != dev:
         raise ValueError(f"page_table must be [B, max_pages] on {dev}")
-    B, mp = page_table.shape
+    B, mp = shape
     row, col = page_table.stride()
     if (B and mp > 1 and col != 1) or (B > 1 and row < mp):
         raise ValueError("page_table rows must be contiguous and not overlap")
-    return SpecKvPool(B, mp, refs.shape[0], int(page_size), int(prefix_len), row if B > 1 else mp, n_pages,
-                      page_table.data_ptr(), _int32("held", held, B, dev))
+    return SpecKvPool(B, mp, n_pages, page_size, prefix_len, row if B > 1 else mp, counts, page_table.data_ptr(),
+                      _int32("held", held, B, dev))
 
 
 def spec_kv_resize(refs, page_table, held, kv_len, n_step, page_size, prefix_len=0, with_status=False, stream=None):
@@ -433,7 +434,7 @@ def spec_kv_fork(refs, page_table, held, kv_len, src, dst, page_size, prefix_len
     dev = refs.device
     p = _pool(refs, page_table, held, page_size, prefix_len)
     lens = _int32("kv_len", kv_len, p.B, dev)
-    n = src.shape[0] if src.dim() == 1 else -1
+    n = src.numel()
     s, d = _int32("src", src, n, dev), _int32("dst", dst, n, dev)
     if _elsewhere(stream, dev):
         return _on(stream, dev, spec_kv_fork, refs, page_table, held, kv_len, src, dst, page_size, prefix_len,

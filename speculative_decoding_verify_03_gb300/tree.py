@@ -83,7 +83,7 @@ def spec_tree_accept(target_tokens, draft_tokens, parents, gamma_per_row=None, w
         return _on(stream, dev, spec_tree_accept, target_tokens, draft_tokens, parents, gamma_per_row, with_status)
     acc = torch.empty(B, dtype=_i32, device=dev)
     nxt = torch.empty(B, dtype=_i32, device=dev)
-    path = torch.empty(B, N, dtype=_i32, device=dev)
+    path = torch.empty(B, N, dtype=_i32, device=dev)  # sizes one by one: 1 us less each than a shape
     tokens = torch.empty(B, N - 1, dtype=_i32, device=dev)
     st = _status(with_status, B, dev)
     code = _lib().spec_tree_accept(B, N - 1, tgt, tok, up, gam, acc.data_ptr(), nxt.data_ptr(), path.data_ptr(),
@@ -133,8 +133,9 @@ def spec_adjust(logits, seq, seq_len, draft_tokens=None, tree_mask=None, prompt_
     gam = None if gamma_per_row is None else _int32("gamma_per_row", gamma_per_row, B, dev)
     drafts = None if draft_tokens is None else _table("draft_tokens", draft_tokens, (B, N - 1), dev)
     tree = None if tree_mask is None else _table("tree_mask", tree_mask, (B, N, (N + 31) // 32), dev)
-    rep, pres, freq = (None if t is None else _float(name, t, (B,), dev) for name, t in
-                       (("repetition", repetition), ("presence", presence), ("frequency", frequency)))
+    rep = None if repetition is None else _float("repetition", repetition, (B,), dev)
+    pres = None if presence is None else _float("presence", presence, (B,), dev)
+    freq = None if frequency is None else _float("frequency", frequency, (B,), dev)
     n_bias, ids, values = 0, None, None
     if bias is not None:
         n_bias = bias.shape[1] if bias.dim() == 2 else -1
