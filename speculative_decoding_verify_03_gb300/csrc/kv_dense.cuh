@@ -653,6 +653,11 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
 #pragma unroll
           for (int i = 0; i < PASS; ++i) load(i);
           load_exps();
+          if (OWN && ahead) {  // the tile behind that one comes to L2: a row a thread
+            const int id = __shfl_sync(~0u, idn, p >> 4), tok = (x.tt + 1) * DN_TILE + p;
+            if (page(id) && tok < held())
+              prefetch_l2(src + id * stride + static_cast<uint64_t>((head_of() << lg) + (tok & pm)) * D);
+          }
         }
       }
     } else {
