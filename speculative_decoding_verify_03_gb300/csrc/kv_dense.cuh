@@ -73,6 +73,7 @@ struct DenseShared {
   uint64_t odone[2], ofull[2], drain[2];     // per row tile
   uint64_t consts[DN_RING], qfull[2];
   int exps[2][DN_RING];      // E, F
+  uint32_t last[DN_RING];    // the tile is the CTA's last one of its item
   uint32_t hot[DN_RING];     // own items: a byte for each loading warp that took out values
   uint32_t tmem, dead;
   uint32_t sum[DN_NT / 32], sum1[DN_NT / 32];
@@ -569,6 +570,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           E = max(__reduce_max_sync(~0u, E), kExpMin) - 7;
           if (p == 0) {
             S.exps[vs][t % DN_RING] = E;
+            if (!vs) S.last[t % DN_RING] = x.tt + 1 == x.nt || t + 1 == tiles;
             bar_arrive(s32(&S.consts[t % DN_RING]));
           }
           if constexpr (OWN) {
@@ -665,6 +667,10 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t) {
         if (t >= 2) bar_wait(s32(empty + (t & 1)), (t >> 1) - 1 & 1, dead);
+        if (p == 0) {
+          if (!vs) S.last[t % DN_RING] = x.tt + 1 == x.nt || t + 1 == tiles;
+          bar_arrive(s32(&S.consts[t % DN_RING]));
+        }
         const uint32_t row0 = head_of() << lg, dst = dst0 + (t & 1) * C::OP;
         const int32_t *ids = list();
         const int end = held();
@@ -719,19 +725,18 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     const int half = __shfl_sync(~0u, warp, 0) - 16;
     const uint32_t base = __shfl_sync(~0u, s32(sm), 0), tmem = __shfl_sync(~0u, S.tmem, 0);
     const int tiles = __shfl_sync(~0u, static_cast<int>(hi - lo), 0);
-    DenseAt x = begin();
     constexpr uint32_t sdesc = mma_desc(E4M3, 128, 64, false, false);
     constexpr uint32_t odesc = mma_desc(E4M3, 128, D, false, true);
     const uint64_t qd = smem_desc(base + C::Q + half * C::OP, 16, 1024), kd = smem_desc(base + C::K, 16, 1024);
     const uint64_t vd = smem_desc(base + C::V, DN_TILE * 128, 1024);
     const uint32_t sc = tmem + half * 128, oc = tmem + 256 + half * 128;
     int g = 0;
-    // Half tile u, tile tt of its item: scores into buffer u & 1 ...
-    auto scores = [&](int u, int tt) {
+    // Half tile u (begin: the CTA's first one of its item): scores into buffer u & 1 ...
+    auto scores = [&](int u, bool begin) {
       const int t = u >> 1, st = t & 1;
-      if (!(u & 1) && (t == 0 || tt == 0)) bar_wait(s32(&S.qfull[half]), g++ & 1, dead);
+      if (begin) bar_wait(s32(&S.qfull[half]), g++ & 1, dead);
       // the weights of half tile u - 2 are read; behind an item, all of it is done
-      const bool behind = u > 0 && !(u & 1) && tt == 0;
+      const bool behind = u > 0 && begin;
       if (u >= 2) bar_wait(s32(&S.odone[half]), behind ? u - 1 & 1 : u & 1, dead);
       if (!(u & 1)) bar_wait(s32(&S.kfull[st]), t >> 1 & 1, dead);
       if (!E4M3) fence_async();  // the copies' writes, before the products' reads
@@ -749,7 +754,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       __syncwarp();
     };
     // ... and its weighted values.
-    auto values = [&](int u, int tt, bool end) {
+    auto values = [&](int u, bool begin, bool end) {
       const int t = u >> 1, st = t & 1;
       const bool last = (u & 1) && end;
       // (parities tell one phase from the next only: no phase is skipped)
@@ -760,10 +765,9 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
       tc_after();
       if (elected() && !*dead) {
         const uint64_t vv = vd + st * (C::OP >> 4) + (u & 1) * (64 * 128 >> 4);
-        const bool fresh = !(u & 1) && (t == 0 || tt == 0);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_ts(oc, sc + (u & 1) * 64 + 8 * k, vv + (k * 2048 >> 4), odesc, !fresh || k > 0);
+          mma_ts(oc, sc + (u & 1) * 64 + 8 * k, vv + (k * 2048 >> 4), odesc, !begin || k > 0);
         mma_commit(s32(&S.odone[half]));
         if (u & 1) mma_commit(s32(&S.vempty[st]));
         if (last) mma_commit(s32(&S.ofull[half]));
@@ -775,15 +779,18 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     // copy each of the two in the code: the roles' loops together are to stay in the
     // instruction cache.)
     int next = 0;
+    bool end = false;  // of the item, behind this tile
 #pragma unroll 1
     for (int u = 0; u < 2 * tiles; ++u) {
-      const int tt = __shfl_sync(~0u, x.tt, 0);
-      const bool last = __shfl_sync(~0u, x.tt + 1 == x.nt || (u >> 1) + 1 == tiles, 0);
-      const int upto = (u & 1) && last ? u : u + 1;
+      const bool begin = next == u;  // of the item: its scores were not formed ahead
+      if (!(u & 1)) {
+        bar_wait(s32(&S.consts[(u >> 1) % DN_RING]), (u >> 1) / DN_RING & 1, dead);
+        end = __shfl_sync(~0u, S.last[(u >> 1) % DN_RING], 0);
+      }
+      const int upto = (u & 1) && end ? u : u + 1;
 #pragma unroll 1
-      for (; next <= upto; ++next) scores(next, tt + (next >> 1) - (u >> 1));
-      values(u, tt, last);
-      if ((u & 1) && (u >> 1) + 1 < tiles) step(x);
+      for (; next <= upto; ++next) scores(next, begin && next == u);
+      values(u, begin, end);
     }
     if (elected()) drained(half);
     __syncwarp();
