@@ -554,17 +554,15 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
 #pragma unroll 1
       for (int t = -1; t < tiles; ++t) {
         const bool more = t + 1 < tiles;
-        if (t < 0) {
-          if (more) ids = pages(x.tt);
-          ahead = tiles > 1 && x.tt + 1 < x.nt;
-          if (ahead) idn = pages(x.tt + 1);
-        } else {
-          const bool partial = __any_sync(~0u, live < 4);
+        bool partial = false;
+        int E = -128;        // seven below the tile's largest exponent
+        int band = DN_TILE;  // own items: the first row of values that not all rows see
+        if (t >= 0) {
+          partial = __any_sync(~0u, live < 4);
           if (live < 4) {  // -128 where there is no token
             const uint32_t in = (1u << 8 * live) - 1;
             ex = (ex & in) | (0x80808080u & ~in);
           }
-          int E = -128;  // seven below the tile's largest exponent
 #pragma unroll
           for (int i = 0; i < 4; ++i) E = max(E, static_cast<int>(static_cast<int8_t>(ex >> 8 * i)));
           E = max(__reduce_max_sync(~0u, E), kExpMin) - 7;
@@ -573,42 +571,24 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
             if (!vs) S.last[t % DN_RING] = x.tt + 1 == x.nt || t + 1 == tiles;
             bar_arrive(s32(&S.consts[t % DN_RING]));
           }
-          if constexpr (OWN) {
-            if (vs) {
-              bool odd = false;
-              if (banded()) {
-                const int first = x.own - x.tt * DN_TILE;
-#pragma unroll
-                for (int i = 0; i < PASS; ++i) {
-                  uint32_t *u = reinterpret_cast<uint32_t *>(&q[i]);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    uint32_t m = (((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 where the byte is NaN
-                    if (row_of(i) < first) m = 0;
-                    odd |= m != 0;
-                    u[k] &= ~(m * 0xffu);
-                  }
-                }
-              }
-              odd = __any_sync(~0u, odd);
-              if (lane == 0) reinterpret_cast<volatile uint8_t *>(&S.hot[t % DN_RING])[wl] = odd;
-            }
-          }
+          if (OWN && vs) band = x.own - x.tt * DN_TILE;
+        }
+        const uint32_t was = ex;
+        if (more) {
+          if (t >= 0) step(x);
+          ids = ahead ? idn : pages(x.tt);
+        }
+        ahead = t + 2 < tiles && x.tt + 1 < x.nt;
+        if (ahead) idn = pages(x.tt + 1);
+        if (t >= 0) {
           // the factors 2^(e - E) of the warp's rows, twice in a word: a lane each (e - E <= 7)
           auto factor = [&](int e) {
             const float one = pow2i(max(e - E, -126));
             return pack<true>(one, one);
           };
           const int mine = wl * RPW + lane % (EVEN ? RPW : 1) + RPP * (lane / (EVEN ? RPW : 1));
-          const uint32_t was = ex;
           const int exr = EVEN ? static_cast<int8_t>(__shfl_sync(~0u, was, mine >> 2 & 31) >> 8 * (mine & 3)) : 0;
           const uint32_t factors = EVEN ? factor(exr) : 0;
-          if (more) {
-            step(x);
-            ids = ahead ? idn : pages(x.tt);
-          }
-          ahead = t + 2 < tiles && x.tt + 1 < x.nt;
-          if (ahead) idn = pages(x.tt + 1);
           uint32_t two[PASS];
           if constexpr (EVEN) {
 #pragma unroll
@@ -623,6 +603,9 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
           }
           if (t >= 2) bar_wait(s32(empty + (t & 1)), (t >> 1) - 1 & 1, dead);
           const uint32_t dst = dst0 + (t & 1) * C::OP;
+          auto to = [&](int i, int c) {  // chunk c of the row's float16 elements
+            return dst + (c >> 3) * (DN_TILE * 128) + row_of(i) * 128 + (((c ^ row_of(i)) & 7) << 4);
+          };
 #pragma unroll
           for (int i = 0; i < PASS; ++i) {
             const int row = row_of(i), f = 2 * chunk_of(i);
@@ -640,11 +623,33 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
             const uint4 b = q[i];
             const uint4 lo4 = make_uint4(scaled(cvt_lo(b.x)), scaled(cvt_hi(b.x)), scaled(cvt_lo(b.y)), scaled(cvt_hi(b.y)));
             const uint4 hi4 = make_uint4(scaled(cvt_lo(b.z)), scaled(cvt_hi(b.z)), scaled(cvt_lo(b.w)), scaled(cvt_hi(b.w)));
-            const uint32_t to = dst + (f >> 3) * (DN_TILE * 128) + row * 128;
-            const uint32_t c0 = ((f ^ row) & 7) << 4, c1 = ((f + 1 ^ row) & 7) << 4;
             const bool swap = !EVEN && f & 8;  // lanes of one row: all eight chunk positions at once
-            sts128(to + (swap ? c1 : c0), swap ? hi4 : lo4);
-            sts128(to + (swap ? c0 : c1), swap ? lo4 : hi4);
+            sts128(to(i, swap ? f + 1 : f), swap ? hi4 : lo4);
+            sts128(to(i, swap ? f : f + 1), swap ? lo4 : hi4);
+          }
+          if constexpr (OWN) {
+            if (vs) {
+              bool odd = false;
+              if (band < DN_TILE) {  // what is NaN among these values comes out again
+#pragma unroll 1
+                for (int i = 0; i < 2 * PASS; ++i) {
+                  if (row_of(i >> 1) < band) continue;
+                  const uint32_t at = to(i >> 1, 2 * chunk_of(i >> 1) + (i & 1));
+                  uint4 v = lds128(at);
+                  uint32_t any = 0;
+                  auto clean = [&](uint32_t u) {  // 1 where the exponent is full
+                    const uint32_t m = (((u & 0x7fff7fffu) + 0x04000400u) & 0x80008000u) >> 15;
+                    any |= m;
+                    return u & ~(m * 0xffffu);
+                  };
+                  v = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+                  if (any) sts128(at, v);
+                  odd |= any != 0;
+                }
+              }
+              odd = __any_sync(~0u, odd);
+              if (lane == 0) reinterpret_cast<volatile uint8_t *>(&S.hot[t % DN_RING])[wl] = odd;
+            }
           }
           fence_async();
           __syncwarp();
