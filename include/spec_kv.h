@@ -139,7 +139,10 @@ spec_status spec_attend(const spec_kv_cache *cache, const spec_kv_batch *batch, 
  * (position kv_len[b] + j) whose bit is set in its mask row.  mask: device int32
  * [B, gamma_max+1, W], contiguous, W = ceil((gamma_max+1) / 32), bit j & 31 of
  * word j >> 5: spec_tree_mask's, or any other (a query that sees nothing gives
- * 0 and -inf).  gamma_max < SPEC_TREE_MAX.  All else is as for spec_attend.
+ * 0 and -inf).  gamma_max < SPEC_TREE_MAX.  All else is as for spec_attend; with
+ * more than 64 query rows of a key/value head ((gamma_max + 1) n_heads /
+ * n_kv_heads) the sequences' own tokens have the roundings of a prefix that as many
+ * share (exponents by 128 tokens of a sequence, its nodes among them).
  */
 size_t spec_attend_tree_workspace_size(const spec_kv_cache *cache, const spec_kv_batch *batch,
                                        int32_t n_heads);

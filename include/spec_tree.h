@@ -88,10 +88,11 @@ spec_status spec_tree_accept(int32_t B, int32_t gamma_max, const int32_t *target
 typedef struct {
   int32_t B, gamma_max, V; /* B = 0: no-op; V in [1, 2^24] */
   int32_t dtype;           /* spec_dtype of logits and out */
-  int32_t capacity;        /* columns of seq */
+  int32_t capacity;        /* columns of seq, below 2^30 */
   int32_t n_bias;          /* entries of a row's bias list, 0 .. 65534 */
   /* strides in elements: logits and out [B, gamma_max + 1, V], seq [B, capacity],
-     allowed [B, gamma_max + 1, ceil(V / 32)] (words; 0: one for all) */
+     allowed [B, gamma_max + 1, ceil(V / 32)] (words; 0: one for all).  No two
+     positions of out overlap. */
   int64_t logits_row_stride, logits_pos_stride, out_row_stride, out_pos_stride;
   int64_t seq_row_stride, allowed_row_stride, allowed_pos_stride;
   /* device arrays; the optional ones may be NULL */

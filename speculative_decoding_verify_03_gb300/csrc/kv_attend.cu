@@ -48,6 +48,10 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
       bad |= static_cast<uint32_t>(__ldg(w.ptable + p)) >= np;
   }
   cudaGridDependencySynchronize();  // from here on: the span kernels' results
+  // what the plan says of the sequence, before the barriers wait for anything
+  uint32_t prow = 0, rows = 0;
+  if (w.prefix) prow = P.plan.rows[b], rows = P.plan.rows[w.B];
+  const uint32_t Wo = P.plan.tiles[w.B], tile0 = P.plan.tiles[b], item0 = P.plan.items[b];
   int lost = 0;
   if (P.plan.lost)
     for (int c = threadIdx.x; c < P.cp; c += MG_NT) lost |= P.plan.lost[c];
@@ -69,20 +73,20 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
   if (!st && there && i < n) {
     if (w.prefix) {
       const int tp = (w.prefix + P.kp - 1) / P.kp;
-      const int nj = (P.plan.rows[w.B] + P.rtp - 1) / P.rtp;
+      const int nj = (rows + P.rtp - 1) / P.rtp;
       const uint32_t W = static_cast<uint32_t>(nj) * w.Hkv * tp, C = min(static_cast<uint32_t>(P.cp), W);
-      const uint32_t k = P.plan.rows[b] + r, y = k / P.rtp, item = head * nj + y;
+      const uint32_t k = prow + r, y = k / P.rtp, item = head * nj + y;
       const uint32_t c0 = owner(item * tp, W, C);
       np = owner(item * tp + tp - 1, W, C) - c0 + 1;
       lp = static_cast<int64_t>(item + c0) * P.rtp + (k - y * P.rtp);
     }
     const int to = (own + n + P.ko - 1) / P.ko, nj = (n * G + P.rto - 1) / P.rto;
-    const uint32_t W = P.plan.tiles[w.B], C = min(static_cast<uint32_t>(P.co), W);
+    const uint32_t C = min(static_cast<uint32_t>(P.co), Wo);
     const int y = r / P.rto;
-    const uint32_t j = head * nj + y, x = P.plan.tiles[b] + j * to;
-    const uint32_t c0 = owner(x, W, C);
-    all = np + owner(x + to - 1, W, C) - c0 + 1;
-    lo = static_cast<int64_t>(P.plan.items[b] + j + c0) * P.rto + (r - y * P.rto);
+    const uint32_t j = head * nj + y, x = tile0 + j * to;
+    const uint32_t c0 = owner(x, Wo, C);
+    all = np + owner(x + to - 1, Wo, C) - c0 + 1;
+    lo = static_cast<int64_t>(item0 + j + c0) * P.rto + (r - y * P.rto);
   }
   const bool on = lane * 4 < D;
   const unsigned most = __reduce_max_sync(~0u, static_cast<unsigned>(all));  // of the warp's rows

@@ -27,9 +27,10 @@
 
 namespace {
 
-constexpr int AJ_NT = 256;         // threads per CTA
-constexpr int AJ_SLICE = 8192;     // tokens of a slice at most
-constexpr int AJ_COUNT = 128;         // of them counting
+constexpr int AJ_NT = 256;           // threads per CTA
+constexpr int AJ_SLICE = 8192;       // tokens of a slice at most
+constexpr int AJ_COUNT = 128;        // of them counting, while the others begin with the stream;
+constexpr int AJ_LONG = 16384;       // all of them for sequences of this length
 constexpr int AJ_UNROLL = 4;         // loads of a thread in flight together: of the stream,
 constexpr int AJ_SPARSE = 2;         // of a listed token (positions)
 constexpr uint32_t kPrompt = 1u << 31, kDraft = 1u << 30, kCount = kDraft - 1;
@@ -121,37 +122,48 @@ __global__ void __launch_bounds__(AJ_NT) adjust_kernel(const __grid_constant__ J
 
   // --- what the slice's tokens have behind them, by the first warps; the others
   // begin with the stream
-  if (tid < AJ_COUNT && (counts || a.n_bias)) {
-    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(AJ_COUNT) : "memory"); };
-    for (int x = tid; x < P.slice * (a.n_bias ? 2 : 1) / 4; x += AJ_COUNT)
+  const int nc = len < AJ_LONG ? AJ_COUNT : AJ_NT;  // threads that count
+  if (tid < nc && (counts || a.n_bias)) {
+    auto meet = [&] { asm volatile("bar.sync 1, %0;" ::"r"(nc) : "memory"); };
+    for (int x = tid; x < P.slice * (a.n_bias ? 2 : 1) / 4; x += nc)
       reinterpret_cast<uint4 *>(sm)[x] = make_uint4(0, 0, 0, 0);
     meet();
     if (counts) {
       const int32_t *seq = a.seq + b * a.seq_row_stride;
-      constexpr int K = 8;
-      for (int s0 = tid; s0 < len; s0 += K * AJ_COUNT) {
-        int t[K];
-#pragma unroll
-        for (int u = 0; u < K; ++u) t[u] = s0 + u * AJ_COUNT < len ? __ldg(seq + s0 + u * AJ_COUNT) - v0 : -1;
+      auto see = [&](int t, int s) {  // token t of the sequence's place s
+        t -= v0;
+        if (static_cast<uint32_t>(t) >= static_cast<uint32_t>(n)) return;
+        if (s < prompt) atomicOr(count + t, kPrompt);
+        else atomicAdd(count + t, 1u);
+      };
+      // four tokens at a time from the first multiple of 16 bytes on, four such loads in flight
+      constexpr int K = 4;
+      const int first = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(seq) & 15)) & 15) / 4, len), quads = (len - first) / 4;
+      for (int s = tid; s < first; s += nc) see(__ldg(seq + s), s);
+      for (int s = first + 4 * quads + tid; s < len; s += nc) see(__ldg(seq + s), s);
+      for (int q0 = tid; q0 < quads; q0 += K * nc) {
+        int4 t[K];
 #pragma unroll
         for (int u = 0; u < K; ++u)
-          if (static_cast<uint32_t>(t[u]) < static_cast<uint32_t>(n)) {
-            if (s0 + u * AJ_COUNT < prompt) atomicOr(count + t[u], kPrompt);
-            else atomicAdd(count + t[u], 1u);
-          }
+          if (q0 + u * nc < quads) t[u] = __ldg(reinterpret_cast<const int4 *>(seq + first) + q0 + u * nc);
+#pragma unroll
+        for (int u = 0; u < K; ++u) {
+          const int s = first + 4 * (q0 + u * nc);
+          if (q0 + u * nc < quads) see(t[u].x, s), see(t[u].y, s + 1), see(t[u].z, s + 2), see(t[u].w, s + 3);
+        }
       }
-      for (int j = tid; j < g; j += AJ_COUNT) {
+      for (int j = tid; j < g; j += nc) {
         const int t = __ldg(a.draft_tokens + static_cast<int64_t>(b) * a.gamma_max + j) - v0;
         drafts[j] = t;
         if (static_cast<uint32_t>(t) < static_cast<uint32_t>(n)) atomicOr(count + t, kDraft);
       }
     }
-    for (int j = tid; j < a.n_bias; j += AJ_COUNT) {
+    for (int j = tid; j < a.n_bias; j += nc) {
       const int t = __ldg(a.bias_ids + static_cast<int64_t>(b) * a.n_bias + j) - v0;
       if (static_cast<uint32_t>(t) < static_cast<uint32_t>(n)) atomicMax(bias + t, static_cast<uint32_t>(j + 1));
     }
     meet();
-    for (int x0 = tid & ~31; x0 < n; x0 += AJ_COUNT) {  // 32 tokens' places side by side, so that their accesses are too
+    for (int x0 = tid & ~31; x0 < n; x0 += nc) {  // 32 tokens' places side by side, so that their accesses are too
       const int x = x0 + lane;
       const bool on = x < n && (count[x] || (a.n_bias && bias[x]));
       const uint32_t all = __ballot_sync(~0u, on);
@@ -263,7 +275,7 @@ extern "C" spec_status spec_adjust(const void *logits, const spec_adjust_params 
       a.seq_row_stride < 0 || a.allowed_row_stride < 0 || a.allowed_pos_stride < 0)
     return SPEC_ERR_INVALID_ARG;
   const int N = a.gamma_max + 1;
-  if (a.gamma_max >= 1 << 20 || a.n_bias > 65534 || a.B > 1 << 20 || (a.tree_mask && N > SPEC_TREE_MAX) ||
+  if (a.gamma_max >= 1 << 20 || a.capacity >= 1 << 30 || a.n_bias > 65534 || a.B > 1 << 20 || (a.tree_mask && N > SPEC_TREE_MAX) ||
       (a.gamma_max > 4096 && (a.repetition || a.presence || a.frequency)))
     return SPEC_ERR_UNSUPPORTED;
   if (a.B == 0) return SPEC_OK;
@@ -277,7 +289,9 @@ extern "C" spec_status spec_adjust(const void *logits, const spec_adjust_params 
       !aligned(a.frequency) || !aligned(a.bias_ids) || !aligned(a.bias) || !aligned(a.allowed) || !aligned(row_status))
     return SPEC_ERR_INVALID_ARG;
   // rows of the output must not overlap, nor, in place, be read with other strides
-  if ((a.gamma_max > 0 && a.out_pos_stride < a.V) || (a.B > 1 && a.out_row_stride < a.V)) return SPEC_ERR_INVALID_ARG;
+  const int64_t rs = a.out_row_stride, ps = a.out_pos_stride;
+  if ((a.gamma_max > 0 && ps < a.V) || (a.B > 1 && rs < a.V)) return SPEC_ERR_INVALID_ARG;
+  if (a.gamma_max > 0 && a.B > 1 && rs < a.gamma_max * ps + a.V && ps < (a.B - 1) * rs + a.V) return SPEC_ERR_INVALID_ARG;
   JP P = {};
   P.a = a;
   P.in = logits;

@@ -248,3 +248,22 @@ def test_adjust_offsets_past_32_bits(sv):  # noqa: F811
     kw = dict(repetition=f32([2, 3, 4]), frequency=f32([1, 1, 1]))
     want = sv.spec_adjust(x.clone(), seq, n, **kw)
     assert torch.equal(sv.spec_adjust(x, seq, n, out=x, **kw), want)
+
+
+@pytest.mark.parametrize("off", [0, 1, 2, 3])
+@pytest.mark.parametrize("length", [16383, 16384, 40001])
+def test_adjust_long_sequences(sv, off, length):  # noqa: F811
+    """Sequences that begin anywhere within 16 bytes, at both sides of the length from which all threads count."""
+    import torch
+    rng = np.random.default_rng(length + off)
+    V, B = 3001, 3
+    seq = rng.integers(-1, V + 1, (B, length))
+    store = torch.zeros((B, length + 9), dtype=torch.int32, device="cuda")
+    view = store[:, off:off + length]
+    view.copy_(i32(seq))
+    n, prompt = np.array([length, length - 5, 7]), np.array([0, 1000, 3])
+    out = sv.spec_adjust(torch.zeros((B, 1, V), device="cuda"), view, i32(n), prompt_len=i32(prompt), frequency=f32([1.0] * B))
+    for b in range(B):
+        tail = seq[b, prompt[b]:n[b]]
+        want = np.bincount(tail[(tail >= 0) & (tail < V)], minlength=V)
+        assert np.array_equal(-out[b, 0].cpu().numpy(), want)

@@ -137,6 +137,8 @@ def _adjust(L, logits=P, out=2 * P, **kw):
     (dict(seq_row_stride=-1), 1), (dict(allowed=P, allowed_row_stride=-1), 1), (dict(allowed=P + 2), 1), (dict(tree_mask=P + 1), 1),
     (dict(out=P, logits_pos_stride=200, logits_row_stride=400), 1), (dict(n_bias=65535, bias=P, bias_ids=P), 2),
     (dict(gamma_max=512, tree_mask=P), 2), (dict(gamma_max=5000, presence=P), 2), (dict(gamma_max=1 << 20), 2), (dict(B=0), 0),
+    (dict(capacity=1 << 30), 2), (dict(out_row_stride=100, out_pos_stride=100), 1), (dict(out_row_stride=100, out_pos_stride=199), 1),
+    (dict(out_row_stride=199, out_pos_stride=100), 1), (dict(out_row_stride=100, out_pos_stride=200, B=0), 0),
 ])
 def test_adjust_arguments(L, bad, code):
     assert _adjust(L, **bad) == code
