@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   if (warp == 16) tmem_alloc(&S.tmem, 512);
   const int per = (B + DN_NT - 1) / DN_NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
   uint32_t a = 0, a1 = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     int own, n;
     row_shape(w, b, own, n);
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
     }
   }
   uint32_t e = a, e1 = a1;
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t t = __shfl_up_sync(~0u, e, o), t1 = OWN ? __shfl_up_sync(~0u, e1, o) : 0;
     if (lane >= o) e += t, e1 += t1;
@@ -162,17 +164,20 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   __syncthreads();
   tc_after();
   e -= a, e1 -= a1;
-  uint32_t rows = 0, items = 0;  // all query rows; own items: all tiles, all items
-#pragma unroll 4
-  for (int v = 0; v < DN_NT / 32; ++v) {
-    if (v < warp) {
-      e += S.sum[v];
-      if (OWN) e1 += S.sum1[v];
-    }
-    rows += S.sum[v];
-    if (OWN) items += S.sum1[v];
+  // sums of the warps before: a lane each
+  static_assert(DN_NT / 32 <= 32, "warps");
+  const uint32_t of = lane < DN_NT / 32 ? S.sum[lane] : 0, of1 = OWN && lane < DN_NT / 32 ? S.sum1[lane] : 0;
+  uint32_t up = of, up1 = of1;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(~0u, up, o), t1 = OWN ? __shfl_up_sync(~0u, up1, o) : 0;
+    if (lane >= o) up += t, up1 += t1;
   }
+  // all query rows; own items: all tiles, all items
+  const uint32_t rows = __shfl_sync(~0u, up, 31), items = __shfl_sync(~0u, up1, 31);
+  e += __shfl_sync(~0u, up - of, warp), e1 += __shfl_sync(~0u, up1 - of1, warp);
   uint32_t *out0 = OWN ? P.plan.tiles : P.plan.rows;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     cum[b] += e;
     if (OWN) cum1[b] += e1;
