@@ -169,12 +169,13 @@ constexpr int64_t kDenseRows = 65;
 // key/value heads of 128 in e4m3, sequences x tokens, replayed calls, span / dense
 // kernel in us:
 //   rows   1 x 100   1 x 8000   8 x 500   8 x 4000   64 x 100   64 x 1000
-//     48   12 / 15    47 / 33   20 / 26    50 / 54    35 / 47     88 / 106
-//     64   12 / 15    45 / 33   29 / 28    54 / 56    42 / 51    106 / 110
-//     80   12 / 15    42 / 33   28 / 28    69 / 56    54 / 56    150 / 115
-//    128   13 / 16    43 / 34   32 / 29    84 / 57    81 / 79    207 / 140
-//    256   14 / 19    57 / 38   45 / 40   152 / 69   157 / 128   398 / 195
-// Heads of 64 and bfloat16 caches cross over at the same rows.
+//     48   12 / 14    47 / 31   21 / 24    50 / 48    36 / 44     87 / 93
+//     64   13 / 14    45 / 31   29 / 26    54 / 48    42 / 48    106 / 99
+//     80   12 / 14    42 / 31   28 / 26    69 / 48    54 / 53    149 / 104
+//    128   13 / 15    43 / 32   32 / 27    84 / 49    81 / 75    206 / 129
+//    256   14 / 18    57 / 36   45 / 37   152 / 62   157 / 125   398 / 186
+// Heads of 64 cross over between 64 and 104 rows, bfloat16 caches as these do.  From
+// here on the dense kernel loses 4 us at most, where the context is short.
 constexpr int64_t kDenseTreeRows = 65;
 static_assert(2 * kMaxDense <= kMaxGrid, "plan: words for the CTAs of both dense launches");
 
