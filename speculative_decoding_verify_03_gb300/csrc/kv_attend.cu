@@ -154,14 +154,15 @@ int row_warps(int64_t rows) {
 // from the 65th on the span kernel reads the keys again.  Measured, 8 heads of 128
 // in e4m3, replayed calls, span / dense kernel in us:
 //   prefix   16 rows      64 rows      80 rows      320 rows
-//      500   20.5 / 25.6  23.5 / 26.4  23.6 / 26.6  34.0 / 35.9
-//     1000   24.1 / 27.0  27.0 / 28.0  27.7 / 28.0  40.8 / 37.8
-//     2000   30.9 / 30.7  34.8 / 32.0  36.8 / 32.0  46.1 / 41.2
-//     4096   43.3 / 34.7  49.0 / 36.2  43.3 / 36.5  56.0 / 50.6
-//     8192   45.1 / 40.0  52.6 / 42.5  50.0 / 42.0  74.0 / 62.6
-// Heads of 64 and bfloat16 caches cross over between 500 and 2000 tokens too.  So the
-// prefix's length says more than the rows do: this rule costs up to 13 us below 65
-// rows and up to 3 us from 65 rows on, where the prefix is short.
+//      500   14.2 / 15.8  17.7 / 16.7  19.4 / 16.9  35.6 / 31.6
+//     1000   17.7 / 17.4  26.7 / 18.4  23.1 / 18.9  43.5 / 37.1
+//     2000   24.3 / 21.1  33.8 / 27.5  35.0 / 27.5  48.7 / 39.3
+//     4096   40.7 / 28.0  46.9 / 33.2  41.0 / 30.3  58.5 / 47.2
+//     8192   42.1 / 31.7  50.7 / 32.9  47.5 / 33.3  76.3 / 54.6
+// Heads of 64 and bfloat16 caches cross over at 500 to 1000 tokens too.  So the
+// prefix's length says more than the rows do; the rule is one of rows because the
+// two kernels round differently (include/spec_kv.h).  It costs up to 18 us below 65
+// rows, where the prefix is long, and gains everywhere above.
 constexpr int64_t kDenseRows = 65;
 
 // Query rows of a sequence's key/value head from which a tree's own tokens go to the

@@ -1,5 +1,6 @@
-// kv_dense.cuh -- the dense kernel of spec_attend: partial attention of the
-// query rows of all sequences over the prefix that they share.
+// kv_dense.cuh -- the dense kernel of spec_attend and spec_attend_tree: partial
+// attention of the query rows of all sequences over the prefix that they share, or
+// of a tree's many query rows over their sequence's own tokens.
 //
 // Mathematics: as in the span kernel (kv_span.cuh), but the stored exponents
 // go into the operands: within a tile of 128 tokens the keys enter as
@@ -30,11 +31,24 @@
 // Two stages of keys and of values.  Where no item has more than 128 rows the second
 // row tile's warps stand aside.
 //
+// Own items (OWN): the nodes of a drafted tree over their sequence's own tokens.  The
+// row tiles are those of a sequence and key/value head, the tiles of all items are
+// numbered through as in the span kernel, a row's mask says what it sees of the
+// step's tokens (64 bits at a time, only where a tile holds some), and of values that
+// not all rows see the ones that are not finite are taken out of the tile and added,
+// at the item's end, to the rows that see them.
+//
+// The roles' loops together have to stay in the instruction cache: with polls, query
+// loads and products unrolled the code was 161 KB, the cache that a GPC shares was 80 %
+// busy with it, and the first line below took 437 us.  So what runs once an item is a
+// loop of a few instructions, and a role's loop stands once in the code (54 KB, 67 KB
+// with own items).
+//
 // Measured: 256 x 9 queries of 32 heads (9216 rows a key/value head of 128) over
-// 8192 e4m3 tokens 437 us, 707 TFLOP/s, 37 % of the products' rate; tensor pipe 31 %
-// active, one instruction issued every other cycle, and of 10 warps per issue 2.2
-// wait for instructions: the roles' code is larger than the nearest instruction cache.
-// Heads of 128, 96 and 64 in e4m3 spill 80, 32 and 20 bytes a thread.
+// 8192 e4m3 tokens 287 us, 1077 TFLOP/s, 57 % of the products' rate: tensor pipe 46 %
+// active, 58 % of the issue slots used (over bfloat16 tokens a call takes 7 % less: the
+// conversions).  16 trees of 64 nodes of 32 heads over
+// 2000..8192 tokens 108 us, 781 TFLOP/s: 34 tiles and two items a CTA, whose ends show.
 #pragma once
 
 #include <cuda_fp16.h>

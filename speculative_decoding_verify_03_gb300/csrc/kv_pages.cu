@@ -15,7 +15,12 @@
 // order of the page ids: page of number k goes to the row in whose sum k falls.
 // Nothing depends on the order of atomics: they add to counts, or or bits.
 //
-// Bound: the chain of loads and cluster barriers; copies by memory.
+// Bound: the chain of loads and cluster barriers; copies by memory.  Measured (replayed
+// calls): four entries each of 256 accepted paths, 8 heads of 128 in bfloat16, 5.7 us.
+// 512 rows' room for nine tokens (287 pages of 98304) and back 11.5 us for both calls, 2.8
+// where there is nothing to do; 64 x 1024 pages of 262144 and back 27 us.  31 forks each
+// of 8 rows of 23 .. 31 pages of 128 tokens and back 20 us, the copies of their last pages
+// (62 MB in and out) 8.0 us, 7.8 TB/s: what was read just before is in L2.
 #include <cooperative_groups.h>
 
 #include <atomic>

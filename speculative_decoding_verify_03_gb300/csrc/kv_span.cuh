@@ -42,6 +42,9 @@
 // 512 x 2..9 queries of 16 heads of 64 over 0..300 bfloat16 tokens 134 us (2.5
 // TB/s): what an item costs once.  A prompt of 2048 tokens at position 0, 32 heads:
 // 344 us (100 TFLOP/s of what its queries see; each row tile walks all keys).
+// Trees (TREE): up to 64 rows a key/value head.  All rows see what is before the step;
+// in the tiles that hold the step's tokens a row's 64 bits say which of them it sees.
+// 48 trees of 2..15 nodes of 16 heads of 64 behind 1001 + 0..300 bfloat16 tokens: 21 us.
 #pragma once
 
 #include <cuda_fp16.h>

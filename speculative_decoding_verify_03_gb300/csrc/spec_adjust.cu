@@ -15,7 +15,11 @@
 //
 // Bound: memory, the logits once in and once out.  The slice is a CTA's share of
 // the vocabulary such that the grid fills the machine; each slice reads the whole
-// sequence, from L2.
+// sequence, from L2.  Measured (replayed calls): 32 x 31 rows of 152064 in bfloat16 with
+// penalties, biases and a mask for every row 114 us, 5.5 TB/s, 81 % of a copy's rate;
+// 64 x 5 rows of 50304 in float32 29 us (a plain copy of them 22.6); one
+// row of 50304 3.6 us.  More warps a multiprocessor (fewer registers) or wider slices
+// lose: 123 to 170 us for the first.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

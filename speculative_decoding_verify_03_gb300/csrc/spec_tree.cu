@@ -11,7 +11,8 @@
 // at a time, and the lowest match is the next node: about 60 clocks a step, and
 // nothing but the first loads waits for memory.
 //
-// Bound: both by their launch and a chain of two loads.
+// Bound: both by their launch and a chain of two loads: 2.7 us each for one tree of 26
+// nodes (replayed calls), 2.9 and 3.3 us for 256 trees of 64.
 #include <cuda_runtime.h>
 
 #include <cstdint>
