@@ -16,6 +16,8 @@ import threading
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
+_BINDING_SOURCE = os.path.join(_HERE, "csrc", "binding.cpp")
 _SOURCES = [os.path.join(_HERE, "csrc", f) for f in ("spec_verify.cu", "spec_strip.cu", "spec_row.cu",
                                                       "spec_commit.cu", "spec_law.cu",
                                                       "spec_cascade.cu", "kv_cache.cu",
@@ -32,8 +34,9 @@ _SOURCES = [os.path.join(_HERE, "csrc", f) for f in ("spec_verify.cu", "spec_str
 _DEPS = _SOURCES + [os.path.join(_HERE, "csrc", f)
                     for f in ("sv_common.cuh", "sv_core.cuh", "sv_strip.h", "sv_row.h",
                               "sv_verify.h", "kv_common.cuh", "kv_span.h", "kv_span.cuh",
-                              "kv_dense.cuh", "kv_tc.cuh")] + [
-    os.path.join(_ROOT, "include", h) for h in ("spec_verify.h", "spec_kv.h", "spec_tree.h")]
+                              "kv_dense.cuh", "kv_tc.cuh")]
+_HEADERS = [os.path.join(_ROOT, "include", h) for h in ("spec_verify.h", "spec_kv.h", "spec_tree.h")]
+_DEPS += _HEADERS
 
 SPEC_F32, SPEC_BF16 = 0, 1
 ROW_BAD_TOKEN, ROW_BAD_LOGIT, ROW_NO_FINITE, ROW_Q_ZERO, ROW_BAD_GAMMA, ROW_BAD_UNIFORM = (
@@ -104,15 +107,43 @@ def _compile(out: str, extra=()):
                 os.remove(o)
 
 
+def _binding_cmd(out: str) -> list:
+    """One g++ command that compiles the host-side binding (PyTorch's own headers and libraries)."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    libs = os.path.join(home, "lib")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    include = [os.path.join(_ROOT, "include"), os.path.join(home, "include"),
+               os.path.join(home, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            *(x for path in include for x in ("-I", path)), _BINDING_SOURCE, "-L", libs, "-ltorch_python", "-ltorch_cpu",
+            "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}", "-o", out]
+
+
 def build(force: bool = False, out: str = None, extra=()) -> str:
-    """Compile libspecverify.so in-tree for sm_103a (skipped when up to date)."""
+    """Compile libspecverify.so in-tree for sm_103a, and the host-side binding
+    beside it (each skipped when up to date)."""
+    def stale(path, deps):
+        return force or not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
+
+    binding = None
+    if out is None and stale(BINDING_PATH, [_BINDING_SOURCE] + _HEADERS):
+        made = BINDING_PATH + f".tmp{os.getpid()}"
+        binding = subprocess.Popen(_binding_cmd(made))
     out = out or LIB_PATH
-    stale = (not os.path.exists(out)) or any(
-        os.path.getmtime(p) > os.path.getmtime(out) for p in _DEPS)
-    if force or stale:
-        tmp = out + f".tmp{os.getpid()}"
-        _compile(tmp, extra)
-        os.replace(tmp, out)
+    try:
+        if stale(out, _DEPS):
+            tmp = out + f".tmp{os.getpid()}"
+            _compile(tmp, extra)
+            os.replace(tmp, out)
+    finally:
+        code = binding.wait() if binding else 0
+    if code:
+        raise subprocess.CalledProcessError(code, "g++ binding.cpp")
+    if binding:
+        os.replace(made, BINDING_PATH)
     return out
 
 

@@ -3,6 +3,7 @@ page tables that it is kept in: the binding of include/spec_kv.h."""
 from __future__ import annotations
 
 import ctypes
+import os
 
 import torch
 
@@ -88,6 +89,7 @@ class KVCache:
                                   k_pages.stride(0) if n else H * S * D,
                                   v_pages.stride(0) if n else H * S * D, n, S, H, D, fmt)
         self.ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
     @classmethod
     def empty(cls, n_pages, n_kv_heads, page_size, head_dim, dtype=None, device="cuda"):
@@ -146,6 +148,29 @@ def _lib():
         from . import lib
         _library = lib()
     return _library
+
+
+_module = None
+
+
+def _native():
+    """The host-side binding (csrc/binding.cpp) of the calls that are one launch long."""
+    global _module
+    if _module is None:
+        import importlib.util
+
+        from . import BINDING_PATH, SpecError
+        if not os.path.exists(BINDING_PATH):
+            raise SpecError(f"{BINDING_PATH} is missing: call build() first")
+        spec = importlib.util.spec_from_file_location(__package__ + "._binding", BINDING_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        lib = _lib()
+        m.bind(SpecError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                            ("spec_status_string", "spec_tree_mask", "spec_tree_accept", "spec_adjust", "spec_kv_compact",
+                             "spec_kv_copy", "spec_kv_resize", "spec_kv_fork")))
+        _module = m
+    return _module
 
 
 def _check(code):
@@ -367,40 +392,10 @@ def spec_kv_compact(cache, page_table, kv_len, path, accepted_len, prefix_len=0,
     accepted_len [B] of spec_tree_accept and kv_len the lengths before the
     step.  One call for every cache of the model.  Updates the cache in place;
     returns row_status [B] when with_status, else None."""
-    dev = cache.device
-    if path.dtype is not _i32:
-        raise TypeError("path must be int32")
-    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
-    if path.dim() != 2 or path.shape[0] != B or path.shape[1] < 1 or path.device != dev or not path.is_contiguous():
-        raise ValueError(f"path must be contiguous [{B}, gamma_max + 1] on {dev}")
-    acc = _int32("accepted_len", accepted_len, B, dev)
-    b = _batch(cache, page_table, kv_len, path.shape[1] - 1, None, 0, None)
-    if _elsewhere(stream, dev):
-        return _on(stream, dev, spec_kv_compact, cache, page_table, kv_len, path, accepted_len, prefix_len, with_status)
-    if prefix_len:
-        b.prefix_len = int(prefix_len)
-        b.prefix_table = b.page_table  # not read: the step is past the prefix
-    st = _status(with_status, B, dev)
-    code = _lib().spec_kv_compact(cache.ref, _byref(b), path.data_ptr(), acc, _ptr(st), _raw_stream(dev.index))
-    if code:
-        _check(code)
-    return st
-
-
-def _pool(refs, page_table, held, page_size, prefix_len):
-    dev, n_pages = refs.device, refs.numel()
-    counts = _int32("refs", refs, n_pages, dev)
-    if page_table.dtype is not _i32:
-        raise TypeError("page_table must be int32")
-    shape = page_table.shape
-    if len(shape) != 2 or page_table.device != dev:
-        raise ValueError(f"page_table must be [B, max_pages] on {dev}")
-    B, mp = shape
-    row, col = page_table.stride()
-    if (B and mp > 1 and col != 1) or (B > 1 and row < mp):
-        raise ValueError("page_table rows must be contiguous and not overlap")
-    return SpecKvPool(B, mp, n_pages, page_size, prefix_len, row if B > 1 else mp, counts, page_table.data_ptr(),
-                      _int32("held", held, B, dev))
+    if stream is not None:
+        return _on(stream, cache.device, spec_kv_compact, cache, page_table, kv_len, path, accepted_len, prefix_len,
+                   with_status)
+    return _native().compact(cache.address, cache.k_pages, page_table, kv_len, path, accepted_len, prefix_len, with_status)
 
 
 def spec_kv_resize(refs, page_table, held, kv_len, n_step, page_size, prefix_len=0, with_status=False, stream=None):
@@ -411,17 +406,10 @@ def spec_kv_resize(refs, page_table, held, kv_len, n_step, page_size, prefix_len
     then the free pages of the lowest numbers are taken, row by row.  No other
     call may use refs meanwhile.  Updates the three in place; returns row_status
     [B] when with_status (ROW_NO_PAGES: the row keeps what it has), else None."""
-    dev = refs.device
-    p = _pool(refs, page_table, held, page_size, prefix_len)
-    lens = _int32("kv_len", kv_len, p.B, dev)
-    if _elsewhere(stream, dev):
-        return _on(stream, dev, spec_kv_resize, refs, page_table, held, kv_len, n_step, page_size, prefix_len,
+    if stream is not None:
+        return _on(stream, refs.device, spec_kv_resize, refs, page_table, held, kv_len, n_step, page_size, prefix_len,
                    with_status)
-    st = _status(with_status, p.B, dev)
-    code = _lib().spec_kv_resize(_byref(p), lens, int(n_step), _ptr(st), _raw_stream(dev.index))
-    if code:
-        _check(code)
-    return st
+    return _native().resize(refs, page_table, held, kv_len, n_step, page_size, prefix_len, with_status)
 
 
 def spec_kv_fork(refs, page_table, held, kv_len, src, dst, page_size, prefix_len=0, with_status=False, stream=None):
@@ -431,20 +419,10 @@ def spec_kv_fork(refs, page_table, held, kv_len, src, dst, page_size, prefix_len
     spec_kv_resize; kv_len [B] int32.  Updates the four in place; returns
     copies [n, 3] int32, what spec_kv_copy is to copy in every cache, and the
     forks' status [n] when with_status."""
-    dev = refs.device
-    p = _pool(refs, page_table, held, page_size, prefix_len)
-    lens = _int32("kv_len", kv_len, p.B, dev)
-    n = src.numel()
-    s, d = _int32("src", src, n, dev), _int32("dst", dst, n, dev)
-    if _elsewhere(stream, dev):
-        return _on(stream, dev, spec_kv_fork, refs, page_table, held, kv_len, src, dst, page_size, prefix_len,
+    if stream is not None:
+        return _on(stream, refs.device, spec_kv_fork, refs, page_table, held, kv_len, src, dst, page_size, prefix_len,
                    with_status)
-    copies = torch.empty(n, 3, dtype=_i32, device=dev)
-    st = _status(with_status, n, dev)
-    code = _lib().spec_kv_fork(_byref(p), lens, s, d, n, copies.data_ptr(), _ptr(st), _raw_stream(dev.index))
-    if code:
-        _check(code)
-    return (copies, st) if with_status else copies
+    return _native().fork(refs, page_table, held, kv_len, src, dst, page_size, prefix_len, with_status)
 
 
 def spec_kv_copy(cache, copies, stream=None):
@@ -452,13 +430,6 @@ def spec_kv_copy(cache, copies, stream=None):
     include/spec_kv.h): for each row (page, new page, tokens) of copies [n, 3]
     int32 the first slots of all heads.  No page may be the target of two rows,
     or the source of one and the target of another.  Updates the cache in place."""
-    dev = cache.device
-    if copies.dtype is not _i32:
-        raise TypeError("copies must be int32")
-    if copies.dim() != 2 or copies.shape[1] != 3 or copies.device != dev or not copies.is_contiguous():
-        raise ValueError(f"copies must be contiguous [n, 3] on {dev}")
-    if _elsewhere(stream, dev):
-        return _on(stream, dev, spec_kv_copy, cache, copies)
-    code = _lib().spec_kv_copy(cache.ref, copies.data_ptr(), copies.shape[0], _raw_stream(dev.index))
-    if code:
-        _check(code)
+    if stream is not None:
+        return _on(stream, cache.device, spec_kv_copy, cache, copies)
+    return _native().copy(cache.address, cache.k_pages, copies)

@@ -305,3 +305,98 @@ def test_tables_in_a_graph(sv):  # noqa: F811
                     x[d, :, :n] = x[s, :, :n]
         for x, y in zip(contents(cache), want):
             assert np.array_equal(x, y)
+
+
+def test_calls_on_a_given_stream(sv):  # noqa: F811
+    """Each call behind a long wait and a write of its inputs on the same stream;
+    what it returns is used on the caller's stream behind a wait for it."""
+    import torch
+    rng = np.random.default_rng(13)
+    B, N, S, n_pages = 5, 33, 16, 60
+    parents = tree_ref.random_parents(rng, B, N - 1)
+    draft, target = rng.integers(0, 3, (B, N - 1)), rng.integers(0, 3, (B, N))
+    own = rng.integers(0, 20, B)
+    cache = make_cache(sv, rng, "e4m3", n_pages, 2, S, 64)[0]
+    lens = i32(np.zeros(B))
+    dev = {k: torch.full_like(i32(v), -7) for k, v in dict(parents=parents, draft=draft, target=target, own=own).items()}
+    real = dict(parents=i32(parents), draft=i32(draft), target=i32(target), own=i32(own))
+    refs, table, held = i32(np.zeros(n_pages)), i32(np.full((B + 1, 8), -1)), i32(np.zeros(B + 1))
+    kv = torch.full((B + 1,), -1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        for k in dev:
+            dev[k].copy_(real[k])
+        kv[:B].copy_(real["own"])
+    mask, depth = sv.spec_tree_mask(dev["parents"], stream=side)
+    acc, nxt, path, tok = sv.spec_tree_accept(dev["target"], dev["draft"], dev["parents"], stream=side)
+    sv.spec_kv_resize(refs, table, held, kv, N, S, stream=side)
+    sv.spec_kv_compact(cache, table[:B], dev["own"], path, acc, stream=side)
+    sv.spec_kv_resize(refs, table, held, kv, 0, S, stream=side)
+    copies = sv.spec_kv_fork(refs, table, held, kv, i32([0]), i32([B]), S, stream=side)
+    sv.spec_kv_copy(cache, copies, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    bits, want = tree_ref.sees(parents, np.full(B, N - 1))
+    assert np.array_equal(np_of(mask), tree_ref.words(bits)) and np.array_equal(np_of(depth), want)
+    for b in range(B):
+        a, t, way = tree_ref.accept(target[b], draft[b], parents[b], N - 1)
+        assert (int(acc[b]), int(nxt[b])) == (a, t) and list(np_of(path)[b, :a + 1]) == way
+    pool = tree_ref.Pool(np.zeros(n_pages, int), np.full((B + 1, 8), -1), [0] * (B + 1), S)
+    state = own.tolist() + [-1]
+    pool.resize(state, N)
+    pool.resize(state, 0)
+    wc, _ = pool.fork(state, [0], [B])
+    assert np_of(copies).tolist() == wc and list(np_of(kv)) == state
+    same(pool, refs, table, held)
+    assert (np_of(lens) == 0).all()
+
+
+def test_calls_from_threads(sv):  # noqa: F811
+    """Calls of several threads, whose checks, outputs and launches come between one another's."""
+    import threading
+    rng = np.random.default_rng(14)
+    runs = [tree_ref.random_parents(rng, 4, 20 + k) for k in range(4)]
+    wrong = []
+
+    def work(k):
+        p, want = i32(runs[k]), tree_ref.words(tree_ref.sees(runs[k], np.full(4, 20 + k))[0])
+        refs, table, held = i32(np.zeros(50)), i32(np.full((3, 8), -1)), i32(np.zeros(3))
+        for step in range(200):
+            mask, depth, st = sv.spec_tree_mask(p, with_status=True)
+            sv.spec_kv_resize(refs, table, held, i32([16 * (step % 5), 20, -1]), 0, 16)
+            if not np.array_equal(np_of(mask), want) or list(np_of(held)) != [step % 5, 2, 0]:
+                wrong.append(k)
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_calls_leave_no_references(sv):  # noqa: F811
+    """What the calls take and give is freed with its last name, also behind errors."""
+    import gc
+    import sys
+
+    import torch
+    p, q, z = i32(np.zeros((2, 3))), i32(np.zeros((2, 4))), torch.zeros((2, 4, 30), device="cuda")
+    seq, n = i32(np.zeros((2, 5))), i32([3, 4])
+    calls = [lambda: sv.spec_tree_mask(p, with_status=True), lambda: sv.spec_tree_accept(q, p, p),
+             lambda: sv.spec_adjust(z, seq, n, p, out=z)]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    gc.collect()
+    before, held = torch.cuda.memory_allocated(), [sys.getrefcount(t) for t in (p, q, z, seq, n)]
+    for _ in range(100):
+        for call in calls:
+            call()
+        for bad in (lambda: sv.spec_tree_mask(p, gamma_per_row=n[:1]), lambda: sv.spec_adjust(z, seq, n),
+                    lambda: sv.spec_tree_accept(q, p, q)):
+            with pytest.raises(ValueError):
+                bad()
+    gc.collect()
+    assert [sys.getrefcount(t) for t in (p, q, z, seq, n)] == held
+    assert torch.cuda.memory_allocated() == before

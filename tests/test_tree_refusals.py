@@ -198,7 +198,18 @@ def test_binding_refuses():
             sv.spec_adjust(**dict(good, **bad))
 
 
-# --------------------------------------- streams, devices and workspaces, on the CPU
+def test_binding_takes_numbers_and_tensors():
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    for bad in (dict(n_step=None), dict(n_step=1.5), dict(page_size="16"), dict(refs=None), dict(kv_len=[0, 0]), dict(held=None)):
+        with pytest.raises(TypeError):
+            sv.spec_kv_resize(**dict(dict(refs=i(5), page_table=i(2, 4), held=i(2), kv_len=i(2), n_step=1, page_size=16), **bad))
+    with pytest.raises(OverflowError):
+        sv.spec_kv_resize(i(5), i(2, 4), i(2), i(2), 1 << 31, 16)
+    with pytest.raises(TypeError):
+        sv.spec_tree_mask([[0]])
+
+
+# ------------------------------------------------- streams and devices, on the CPU
 def calls_on(device="cuda:0", B=2):
     z = lambda *s, dt=torch.int32: OnGpu(torch.zeros(s, dtype=dt), device)  # noqa: E731
     bf = torch.bfloat16
@@ -219,33 +230,46 @@ def calls_on(device="cuda:0", B=2):
 OPS = ["attend_tree", "compact", "copy", "resize", "fork", "mask", "accept", "adjust"]
 
 
+class FakeNative:
+    """The host-side binding: notes the stream that is current when it is called, gives a pair back."""
+
+    def __init__(self, gpu):
+        self.gpu = gpu
+
+    def __getattr__(self, name):
+        def called(*args):
+            assert all(getattr(a, "device", None) is not None or a is None or isinstance(a, (int, bool)) for a in args)
+            self.gpu.calls.append((self.gpu.device, self.gpu.streams.get(self.gpu.device, 0)))
+            return torch.empty(3, dtype=torch.int32, device="cuda:0"), torch.empty(3, dtype=torch.int32, device="cuda:0")
+        return called
+
+
 @pytest.fixture
 def gpu(monkeypatch):
-    for name in ("spec_attend_tree", "spec_kv_compact", "spec_kv_copy", "spec_kv_resize", "spec_kv_fork", "spec_tree_mask",
-                 "spec_tree_accept", "spec_adjust"):
-        monkeypatch.setattr(FakeGpu, name, FakeGpu._called, raising=False)
+    monkeypatch.setattr(FakeGpu, "spec_attend_tree", FakeGpu._called, raising=False)
     monkeypatch.setattr(FakeGpu, "spec_attend_tree_workspace_size", FakeGpu.spec_attend_workspace_size, raising=False)
     fake = FakeGpu(monkeypatch)
-    monkeypatch.setattr(tree, "_raw_stream", lambda index: fake.streams.get(index, 0))
+    native = FakeNative(fake)
+    for m in (kv, tree):
+        monkeypatch.setattr(m, "_native", lambda: native)
     return fake
 
 
 @pytest.mark.parametrize("op", OPS)
 def test_a_given_stream_is_the_one_of_all_tensors(gpu, op):
+    """What a call allocates is the given stream's, and goes back not before the
+    caller's stream is done with it."""
     got = calls_on()[op](stream=Stream(77))
     assert gpu.calls[0][-1] == 77 and all(t.stream == 77 for t in gpu.made)
-    assert all(t is None or t.used_on == [0] for t in (got if isinstance(got, tuple) else (got,)))
+    assert all(t.used_on == [0] for t in got)
     calls_on()[op]()
     assert gpu.calls[1][-1] == 0
 
 
 @pytest.mark.parametrize("op", OPS)
-def test_the_launch_is_on_the_tensors_device(gpu, op):
-    for device, stream in ((1, None), (0, None), (1, Stream(5, "cuda:1"))):
-        gpu.calls.clear()
-        calls_on(f"cuda:{device}")[op](stream=stream)
-        assert gpu.calls[0][0] == device and gpu.calls[0][-1] == (stream.cuda_stream if stream else 0)
-        assert gpu.device == 0
+def test_a_given_streams_device_is_current(gpu, op):
+    calls_on("cuda:1")[op](stream=Stream(5, "cuda:1"))
+    assert gpu.calls[0][0] == 1 and gpu.calls[0][-1] == 5 and gpu.device == 0
 
 
 @pytest.mark.parametrize("op", OPS)
@@ -253,5 +277,20 @@ def test_streams_of_other_devices_and_host_tensors_are_refused(gpu, op):
     with pytest.raises(ValueError):
         calls_on("cuda:1")[op](stream=Stream(5, "cuda:0"))
     with pytest.raises(sv.SpecError):
-        calls_on("cpu")[op]()
+        calls_on("cpu")[op](stream=Stream(5, "cuda:0"))
     assert not gpu.calls
+
+
+def test_host_tensors_are_refused():
+    """Without a given stream the host-side binding itself says so, behind its other checks."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    z = torch.zeros((3, 2, 16, 64), dtype=torch.bfloat16)
+    c = sv.KVCache(z, z)
+    for call in (lambda: sv.spec_kv_compact(c, i(2, 4), i(2), i(2, 3), i(2)), lambda: sv.spec_kv_copy(c, i(4, 3)),
+                 lambda: sv.spec_kv_resize(i(5), i(2, 4), i(2), i(2), 1, 16),
+                 lambda: sv.spec_kv_fork(i(5), i(2, 4), i(2), i(2), i(1), i(1), 16), lambda: sv.spec_tree_mask(i(2, 3)),
+                 lambda: sv.spec_tree_accept(i(2, 4), i(2, 3), i(2, 3)),
+                 lambda: sv.spec_adjust(torch.zeros(2, 1, 9), i(2, 5), i(2)),
+                 lambda: sv.spec_attend_tree(torch.zeros((2, 3, 4, 64), dtype=torch.bfloat16), c, i(2, 4), i(2), i(2, 3, 1))):
+        with pytest.raises(sv.SpecError, match="no CPU path"):
+            call()
