@@ -1,6 +1,7 @@
-// binding.cpp -- argument checks and outputs of the calls that are one launch long
-// (tree.py, and the pages of kv.py): in Python they take 6 to 15 us of the host's
-// time on the GPU's host, which is more than the launch does on the GPU; here 3 to 6.
+// binding.cpp -- argument checks and outputs of the trees' and pages' calls (tree.py,
+// and the later half of kv.py).  They are one launch long, or few: in Python their
+// checks and outputs took 6 to 15 us of the host's time on the GPU's host (the tree's
+// attention 23), which is more than the launches do on the GPU; here they take 2 to 6.
 //
 // The module knows the library by the addresses that bind() is given (it is not
 // linked to it).  Every function takes its arguments in a fixed order, works on the
@@ -16,7 +17,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdarg>
+#include <cstring>
 #include <initializer_list>
 #include <string>
 
@@ -36,6 +39,8 @@ struct Library {
   decltype(&spec_kv_copy) copy;
   decltype(&spec_kv_resize) resize;
   decltype(&spec_kv_fork) fork;
+  decltype(&spec_attend_tree_workspace_size) attend_size;
+  decltype(&spec_attend_tree) attend;
 } lib;
 PyObject *spec_error = nullptr;
 
@@ -112,12 +117,12 @@ struct On {
   }
 };
 
+// f() without the interpreter's lock: it raises nothing itself.
 template <class F>
 void call(F f) {
-  spec_status code;
-  Py_BEGIN_ALLOW_THREADS
-  code = f();
-  Py_END_ALLOW_THREADS
+  PyThreadState *thread = PyEval_SaveThread();
+  const spec_status code = f();
+  PyEval_RestoreThread(thread);
   if (code != SPEC_OK) fail(spec_error, "%s", lib.status_string(code));
 }
 
@@ -152,11 +157,13 @@ PyObject *tree_mask(PyObject *const *a) {
   const Tensor &parents = tensor(a[0], "parents");
   if (parents.dim() != 2) fail(PyExc_ValueError, "parents must be [B, gamma_max]");
   const at::Device dev = parents.device();
-  const int64_t B = parents.size(0), G = parents.size(1), N = G + 1;
+  const int32_t B = size32(parents.size(0)), G = size32(parents.size(1));
+  const int64_t N = static_cast<int64_t>(G) + 1;
   const int32_t *up = ints(a[0], "parents", {B, G}, dev), *gam = ints_or_none(a[1], "gamma_per_row", {B}, dev);
   const On on(dev);
   const Tensor mask = on.empty({B, N, (N + 31) / 32}), depth = on.empty({B, N}), st = truth(a[2]) ? on.empty({B}) : Tensor();
-  call([&] { return lib.tree_mask(size32(B), size32(G), up, gam, out(mask), out(depth), out(st), on.stream()); });
+  void *const stream = on.stream();
+  call([&] { return lib.tree_mask(B, G, up, gam, out(mask), out(depth), out(st), stream); });
   return results({mask, depth, st});
 }
 
@@ -165,16 +172,14 @@ PyObject *tree_accept(PyObject *const *a) {
   const Tensor &target = tensor(a[0], "target_tokens");
   if (target.dim() != 2 || target.size(1) < 1) fail(PyExc_ValueError, "target_tokens must be [B, gamma_max + 1]");
   const at::Device dev = target.device();
-  const int64_t B = target.size(0), N = target.size(1);
+  const int32_t B = size32(target.size(0)), N = size32(target.size(1));
   const int32_t *tgt = ints(a[0], "target_tokens", {B, N}, dev), *tok = ints(a[1], "draft_tokens", {B, N - 1}, dev);
   const int32_t *up = ints(a[2], "parents", {B, N - 1}, dev), *gam = ints_or_none(a[3], "gamma_per_row", {B}, dev);
   const On on(dev);
   const Tensor acc = on.empty({B}), next = on.empty({B}), path = on.empty({B, N}), tokens = on.empty({B, N - 1});
   const Tensor st = truth(a[4]) ? on.empty({B}) : Tensor();
-  call([&] {
-    return lib.tree_accept(size32(B), size32(N - 1), tgt, tok, up, gam, out(acc), out(next), out(path), out(tokens), out(st),
-                           on.stream());
-  });
+  void *const stream = on.stream();
+  call([&] { return lib.tree_accept(B, N - 1, tgt, tok, up, gam, out(acc), out(next), out(path), out(tokens), out(st), stream); });
   return results({acc, next, path, tokens, st});
 }
 
@@ -237,7 +242,8 @@ PyObject *adjust(PyObject *const *a) {
   if (!to.defined()) to = on.empty({B, N, V}, type);
   p.out_row_stride = to.stride(0), p.out_pos_stride = to.stride(1);
   const Tensor st = truth(a[14]) ? on.empty({B}) : Tensor();
-  call([&] { return lib.adjust(logits.const_data_ptr(), &p, to.mutable_data_ptr(), out(st), on.stream()); });
+  void *const stream = on.stream();
+  call([&] { return lib.adjust(logits.const_data_ptr(), &p, to.mutable_data_ptr(), out(st), stream); });
   return results({to, st});
 }
 
@@ -277,7 +283,8 @@ PyObject *compact(PyObject *const *a) {
   const spec_kv_cache *cache = cache_of(a[0]);
   const On on(dev);
   const Tensor st = truth(a[7]) ? on.empty({B}) : Tensor();
-  call([&] { return lib.compact(cache, &b, way, acc, out(st), on.stream()); });
+  void *const stream = on.stream();
+  call([&] { return lib.compact(cache, &b, way, acc, out(st), stream); });
   return results({st});
 }
 
@@ -285,11 +292,12 @@ PyObject *compact(PyObject *const *a) {
 PyObject *copy(PyObject *const *a) {
   const at::Device dev = tensor(a[1], "k_pages").device();
   const Tensor &copies = tensor(a[2], "copies");
-  const int64_t n = copies.dim() == 2 ? copies.size(0) : -1;
+  const int32_t n = copies.dim() == 2 ? size32(copies.size(0)) : -1;
   const int32_t *rows = ints(a[2], "copies", {n, 3}, dev);
   const spec_kv_cache *cache = cache_of(a[0]);
   const On on(dev);
-  call([&] { return lib.copy(cache, rows, size32(n), on.stream()); });
+  void *const stream = on.stream();
+  call([&] { return lib.copy(cache, rows, n, stream); });
   Py_RETURN_NONE;
 }
 
@@ -315,7 +323,8 @@ PyObject *resize(PyObject *const *a) {
   const int32_t *lens = ints(a[3], "kv_len", {p.B}, dev), n = number(a[4]);
   const On on(dev);
   const Tensor st = truth(a[7]) ? on.empty({p.B}) : Tensor();
-  call([&] { return lib.resize(&p, lens, n, out(st), on.stream()); });
+  void *const stream = on.stream();
+  call([&] { return lib.resize(&p, lens, n, out(st), stream); });
   return results({st});
 }
 
@@ -324,12 +333,78 @@ PyObject *fork(PyObject *const *a) {
   at::Device dev(at::kCPU);
   const spec_kv_pool p = pool(a[0], a[1], a[2], a[6], a[7], dev);
   int32_t *lens = ints_out(a[3], "kv_len", {p.B}, dev);
-  const int64_t n = tensor(a[4], "src").numel();
+  const int32_t n = size32(tensor(a[4], "src").numel());
   const int32_t *src = ints(a[4], "src", {n}, dev), *dst = ints(a[5], "dst", {n}, dev);
   const On on(dev);
   const Tensor copies = on.empty({n, 3}), st = truth(a[8]) ? on.empty({n}) : Tensor();
-  call([&] { return lib.fork(&p, lens, src, dst, size32(n), out(copies), out(st), on.stream()); });
+  void *const stream = on.stream();
+  call([&] { return lib.fork(&p, lens, src, dst, n, out(copies), out(st), stream); });
   return results({copies, st});
+}
+
+// --------------------------------------------------------------- attention
+// the cache's address, its k_pages, q, page_table, kv_len, mask, prefix_table, prefix_len, gamma_per_row, scale,
+// workspace, out, with_status
+PyObject *attend_tree(PyObject *const *a) {
+  const at::Device dev = tensor(a[1], "k_pages").device();
+  const spec_kv_cache *cache = cache_of(a[0]);
+  const Tensor &q = tensor(a[2], "q"), &pages = tensor(a[3], "page_table"), &lens = tensor(a[4], "kv_len");
+  if (q.scalar_type() != at::kBFloat16) fail(PyExc_TypeError, "q must be bfloat16");
+  const int64_t D = cache->head_dim;
+  if (q.dim() != 4 || lens.dim() != 1 || q.size(0) != lens.size(0) || q.size(1) < 1 || q.size(3) != D)
+    fail(PyExc_ValueError, "q must be [B, gamma_max + 1, n_heads, head_dim]");
+  if (q.device() != dev) fail(PyExc_ValueError, "q must be on %s", dev.str().c_str());
+  if (D > 1 && q.stride(3) != 1) fail(PyExc_ValueError, "the head_dim axis must be contiguous");
+  const int64_t B = q.size(0), N = q.size(1);
+  const int32_t Hq = size32(q.size(2));
+  if (Hq < 1 || Hq % cache->n_kv_heads) fail(PyExc_ValueError, "n_heads must be a multiple of the cache's n_kv_heads");
+  spec_kv_batch b = {};
+  b.table_row_stride = page_table(pages, B, dev);
+  b.B = size32(B), b.gamma_max = size32(N - 1), b.max_pages = size32(pages.size(1));
+  b.prefix_len = number(a[7]);
+  b.page_table = static_cast<const int32_t *>(pages.const_data_ptr());
+  b.kv_len = ints(a[4], "kv_len", {B}, dev);
+  b.gamma_per_row = ints_or_none(a[8], "gamma_per_row", {B}, dev);
+  if (b.prefix_len > 0) {
+    const int64_t need = (static_cast<int64_t>(b.prefix_len) + cache->page_size - 1) / cache->page_size;
+    const int64_t n = a[6] == Py_None ? -1 : tensor(a[6], "prefix_table").numel();
+    if (n < need) fail(PyExc_ValueError, "prefix_table must hold the prefix's %lld page ids", static_cast<long long>(need));
+    b.prefix_table = ints(a[6], "prefix_table", {n}, dev);
+  }
+  const int32_t *mask = ints(a[5], "mask", {B, N, (N + 31) / 32}, dev);
+  const float scale = a[9] == Py_None ? static_cast<float>(std::pow(static_cast<double>(D), -0.5))
+                                      : static_cast<float>(PyFloat_AsDouble(a[9]));
+  if (PyErr_Occurred()) throw Raised();
+  const On on(dev);
+  Tensor work;
+  if (PyUnicode_Check(a[10])) {
+    if (PyUnicode_CompareWithASCIIString(a[10], "auto")) fail(PyExc_ValueError, "workspace must be 'auto' or a tensor");
+    work = on.empty({static_cast<int64_t>(lib.attend_size(cache, &b, Hq))}, at::kByte);
+  } else {
+    if (a[10] == Py_None || tensor(a[10], "workspace").device() != dev || !THPVariable_Unpack(a[10]).is_contiguous())
+      fail(PyExc_ValueError, "workspace must be 'auto' or a contiguous tensor on %s", dev.str().c_str());
+    work = THPVariable_Unpack(a[10]);
+  }
+  Tensor o, lse;
+  if (a[11] == Py_None) {
+    o = on.empty({B, N, Hq, D}, at::kBFloat16);
+    lse = on.empty({B, N, Hq}, at::kFloat);
+  } else {
+    if (!PyTuple_Check(a[11]) || PyTuple_GET_SIZE(a[11]) != 2) fail(PyExc_TypeError, "out must be a pair of tensors");
+    o = tensor(PyTuple_GET_ITEM(a[11], 0), "out"), lse = tensor(PyTuple_GET_ITEM(a[11], 1), "out");
+    if (o.sizes() != q.sizes() || o.scalar_type() != at::kBFloat16 || !o.is_contiguous() ||
+        lse.sizes() != at::IntArrayRef({B, N, Hq}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous() ||
+        o.device() != dev || lse.device() != dev)
+      fail(PyExc_ValueError, "out must be contiguous bfloat16 and float32 tensors of the results' shapes");
+  }
+  const Tensor st = truth(a[12]) ? on.empty({B}) : Tensor();
+  const int64_t strides[3] = {q.stride(0), q.stride(1), q.stride(2)};
+  void *const stream = on.stream();
+  call([&] {
+    return lib.attend(cache, &b, mask, q.const_data_ptr(), Hq, strides, scale, o.mutable_data_ptr(),
+                      static_cast<float *>(lse.mutable_data_ptr()), out(st), work.mutable_data_ptr(), work.nbytes(), stream);
+  });
+  return results({o, lse, st});
 }
 
 // ------------------------------------------------------------------ module
@@ -385,6 +460,7 @@ PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"copy", fast(entry<copy, 3>), METH_FASTCALL, nullptr},
                          {"resize", fast(entry<resize, 8>), METH_FASTCALL, nullptr},
                          {"fork", fast(entry<fork, 9>), METH_FASTCALL, nullptr},
+                         {"attend_tree", fast(entry<attend_tree, 13>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
 

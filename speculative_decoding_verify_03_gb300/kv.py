@@ -154,7 +154,7 @@ _module = None
 
 
 def _native():
-    """The host-side binding (csrc/binding.cpp) of the calls that are one launch long."""
+    """The host-side binding (csrc/binding.cpp) of the trees' and pages' calls."""
     global _module
     if _module is None:
         import importlib.util
@@ -168,7 +168,8 @@ def _native():
         lib = _lib()
         m.bind(SpecError, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
                             ("spec_status_string", "spec_tree_mask", "spec_tree_accept", "spec_adjust", "spec_kv_compact",
-                             "spec_kv_copy", "spec_kv_resize", "spec_kv_fork")))
+                             "spec_kv_copy", "spec_kv_resize", "spec_kv_fork", "spec_attend_tree_workspace_size",
+                             "spec_attend_tree")))
         _module = m
     return _module
 
@@ -307,12 +308,6 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     stream as well, once that waits for it.  Returns (out [B, gamma_max + 1,
     n_heads, head_dim] bfloat16, lse [B, gamma_max + 1, n_heads] float32), and
     row_status [B] when with_status."""
-    return _attend(q, cache, page_table, kv_len, None, prefix_table, prefix_len, gamma_per_row, scale, workspace, out,
-                   with_status, stream)
-
-
-def _attend(q, cache, page_table, kv_len, mask, prefix_table, prefix_len, gamma_per_row, scale, workspace, out,
-            with_status, stream=None):
     dev = cache.device
     shape = q.shape
     if q.dtype is not _bf16:
@@ -328,19 +323,13 @@ def _attend(q, cache, page_table, kv_len, mask, prefix_table, prefix_len, gamma_
     if Hq < 1 or Hq % cache.n_kv_heads:
         raise ValueError("n_heads must be a multiple of the cache's n_kv_heads")
     b = _batch(cache, page_table, kv_len, N - 1, prefix_table, prefix_len, gamma_per_row)
-    if mask is not None:
-        if mask.dtype is not _i32:
-            raise TypeError("mask must be int32")
-        if mask.shape != (B, N, -(-N // 32)) or mask.device != dev or not mask.is_contiguous():
-            raise ValueError(f"mask must be contiguous [{B}, {N}, {-(-N // 32)}] on {dev}")
     if _elsewhere(stream, dev):
-        return _on(stream, dev, _attend, q, cache, page_table, kv_len, mask, prefix_table, prefix_len, gamma_per_row,
+        return _on(stream, dev, spec_attend, q, cache, page_table, kv_len, prefix_table, prefix_len, gamma_per_row,
                    scale, workspace, out, with_status)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")
-        size = _lib().spec_attend_workspace_size if mask is None else _lib().spec_attend_tree_workspace_size
-        workspace = torch.empty(size(cache.ref, _byref(b), Hq), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(_lib().spec_attend_workspace_size(cache.ref, _byref(b), Hq), dtype=torch.uint8, device=dev)
     elif workspace is None or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be 'auto' or a contiguous tensor on {dev}")
     if out is None:
@@ -352,13 +341,9 @@ def _attend(q, cache, page_table, kv_len, mask, prefix_table, prefix_len, gamma_
                 lse.dtype is not _f32 or not lse.is_contiguous() or o.device != dev or lse.device != dev):
             raise ValueError("out must be contiguous bfloat16 and float32 tensors of the results' shapes")
     st = _status(with_status, B, dev)
-    rest = (q.data_ptr(), Hq, _byref(_Strides(*qs[:3])), D ** -0.5 if scale is None else float(scale), o.data_ptr(),
-            lse.data_ptr(), _ptr(st), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _raw_stream(dev.index))
-    if mask is None:
-        code = _lib().spec_attend(cache.ref, _byref(b), *rest)
-    else:
-        code = _lib().spec_attend_tree(cache.ref, _byref(b), mask.data_ptr(), *rest)
+    code = _lib().spec_attend(cache.ref, _byref(b), q.data_ptr(), Hq, _byref(_Strides(*qs[:3])),
+                              D ** -0.5 if scale is None else float(scale), o.data_ptr(), lse.data_ptr(), _ptr(st),
+                              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev.index))
     if code:
         _check(code)
     return (o, lse, st) if with_status else (o, lse)
@@ -379,10 +364,11 @@ def spec_attend_tree(q, cache, page_table, kv_len, mask, prefix_table=None, pref
     gamma_max + 1, ceil((gamma_max + 1) / 32)] int32: spec_tree_mask's, or any
     other.  A query that sees nothing gives 0 and -inf.  workspace: a tensor of
     attend_tree_workspace_bytes, or "auto"."""
-    if mask is None:
-        raise TypeError("mask must be an int32 tensor")
-    return _attend(q, cache, page_table, kv_len, mask, prefix_table, prefix_len, gamma_per_row, scale, workspace, out,
-                   with_status, stream)
+    if stream is not None:
+        return _on(stream, cache.device, spec_attend_tree, q, cache, page_table, kv_len, mask, prefix_table, prefix_len,
+                   gamma_per_row, scale, workspace, out, with_status)
+    return _native().attend_tree(cache.address, cache.k_pages, q, page_table, kv_len, mask, prefix_table, prefix_len,
+                                 gamma_per_row, scale, workspace, out, with_status)
 
 
 def spec_kv_compact(cache, page_table, kv_len, path, accepted_len, prefix_len=0, with_status=False, stream=None):

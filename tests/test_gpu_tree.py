@@ -337,3 +337,21 @@ def test_attend_tree_in_a_graph_and_on_a_stream(sv):  # noqa: F811
         got = sv.spec_attend_tree(q, s["cache"], table, lens, mask, out=into, workspace=ws, stream=side, **kw)
         side.synchronize()
         assert got[0] is into[0] and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_attend_tree_workspaces_and_outputs_are_checked(sv):  # noqa: F811
+    import torch
+    s = tree_case(sv, 71, "bf16", 2, 5, 4, 2, 64, 16, 0, [20, 3])
+    want = call(sv, s)
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for bad, error in ((dict(workspace=None), ValueError), (dict(workspace="mine"), ValueError), (dict(workspace=small), sv.SpecError),
+                       (dict(workspace=small.cpu()), ValueError), (dict(out=want[0]), TypeError),
+                       (dict(out=(want[0], want[0])), ValueError), (dict(out=(want[0].float(), want[1])), ValueError),
+                       (dict(scale=float("nan")), sv.SpecError), (dict(scale=-1.0), sv.SpecError)):
+        with pytest.raises(error):
+            call(sv, s, **bad)
+    size = sv.attend_tree_workspace_bytes(s["cache"], sv.SpecKvBatch(B=2, gamma_max=4, max_pages=s["table"].shape[1]), 4)
+    for ws in (torch.empty(size, dtype=torch.uint8, device="cuda"), torch.empty(size // 4, dtype=torch.int32, device="cuda")):
+        got = call(sv, s, workspace=ws, out=(torch.empty_like(want[0]), torch.empty_like(want[1])))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(call(sv, s, scale=0.125)[0], want[0])  # 64 ** -0.5

@@ -158,6 +158,15 @@ def test_binding_refuses():
             sv.spec_attend_tree(z(2, 3, 4, 64), c, i(2, 4), i(2), m)
     with pytest.raises(TypeError):
         sv.spec_attend_tree(z(2, 3, 4, 64), c, i(2, 4), i(2), i(2, 3, 1).long())
+    good = dict(q=z(2, 3, 4, 64), page_table=i(2, 4), kv_len=i(2), mask=i(2, 3, 1))
+    for bad in (dict(q=z(2, 3, 3, 64)), dict(q=z(2, 3, 4, 80)), dict(q=z(3, 3, 4, 64)), dict(q=z(2, 0, 4, 64), mask=i(2, 0, 0)),
+                dict(q=z(2, 3, 64, 4).transpose(2, 3)), dict(page_table=i(3, 4)), dict(page_table=i(4, 2).t()), dict(kv_len=i(2, 1)),
+                dict(gamma_per_row=i(3)), dict(prefix_len=3), dict(prefix_len=17, prefix_table=i(1))):
+        with pytest.raises(ValueError):
+            sv.spec_attend_tree(cache=c, **dict(good, **bad))
+    for bad in (dict(q=z(2, 3, 4, 64).float()), dict(page_table=i(2, 4).long()), dict(scale="1"), dict(prefix_table=[0], prefix_len=1)):
+        with pytest.raises(TypeError):
+            sv.spec_attend_tree(cache=c, **dict(good, **bad))
     for bad in (dict(path=i(3, 4)), dict(path=i(4, 2).t()), dict(accepted_len=i(3)), dict(kv_len=i(2, 1)), dict(path=i(2, 0))):
         a = dict(page_table=i(2, 4), kv_len=i(2), path=i(2, 4), accepted_len=i(2))
         a.update(bad)
@@ -238,7 +247,7 @@ class FakeNative:
 
     def __getattr__(self, name):
         def called(*args):
-            assert all(getattr(a, "device", None) is not None or a is None or isinstance(a, (int, bool)) for a in args)
+            assert all(getattr(a, "device", None) is not None or a is None or isinstance(a, (int, str)) for a in args)
             self.gpu.calls.append((self.gpu.device, self.gpu.streams.get(self.gpu.device, 0)))
             return torch.empty(3, dtype=torch.int32, device="cuda:0"), torch.empty(3, dtype=torch.int32, device="cuda:0")
         return called
