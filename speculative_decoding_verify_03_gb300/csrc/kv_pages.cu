@@ -591,7 +591,7 @@ extern "C" spec_status spec_kv_compact(const spec_kv_cache *cache, const spec_kv
   if (P.w.N > SPEC_TREE_MAX) return SPEC_ERR_UNSUPPORTED;
   if (P.w.B == 0) return SPEC_OK;
   if (!path || !accepted_len || reinterpret_cast<uintptr_t>(path) % 4 ||
-      reinterpret_cast<uintptr_t>(accepted_len) % 4)
+      reinterpret_cast<uintptr_t>(accepted_len) % 4 || reinterpret_cast<uintptr_t>(row_status) % 4)
     return SPEC_ERR_INVALID_ARG;
   P.k = static_cast<uint8_t *>(cache->k_pages);
   P.v = static_cast<uint8_t *>(cache->v_pages);
@@ -638,7 +638,8 @@ extern "C" spec_status spec_kv_resize(const spec_kv_pool *pool, const int32_t *k
   if (n_step < 0) return SPEC_ERR_INVALID_ARG;
   if (n_step > 1 << 30) return SPEC_ERR_UNSUPPORTED;
   if (pool->B == 0) return SPEC_OK;
-  if (!kv_len || reinterpret_cast<uintptr_t>(kv_len) % 4) return SPEC_ERR_INVALID_ARG;
+  if (!kv_len || (reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(row_status)) % 4)
+    return SPEC_ERR_INVALID_ARG;
   R.len = kv_len;
   R.n = n_step;
   R.status = row_status;
@@ -659,7 +660,8 @@ extern "C" spec_status spec_kv_fork(const spec_kv_pool *pool, int32_t *kv_len, c
   if (n > kv::kMaxB) return SPEC_ERR_UNSUPPORTED;
   if (n == 0) return SPEC_OK;
   const uintptr_t all = reinterpret_cast<uintptr_t>(kv_len) | reinterpret_cast<uintptr_t>(src) |
-                        reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(copies);
+                        reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(copies) |
+                        reinterpret_cast<uintptr_t>(fork_status);
   if (!src || !dst || !copies || all % 4 || (pool->B > 0 && !kv_len)) return SPEC_ERR_INVALID_ARG;
   F.len = kv_len;
   F.src = src;

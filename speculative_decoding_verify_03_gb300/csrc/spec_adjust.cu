@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(AJ_NT) adjust_kernel(const __grid_constant__ J
   using E = Elem<F32>;
   using T = typename E::T;
   constexpr int VEC = E::VEC, U = AJ_UNROLL, S = AJ_SPARSE;
-  extern __shared__ uint32_t sm[];
+  extern __shared__ __align__(16) uint32_t sm[];
   __shared__ uint32_t listed, next;  // tokens on the list; next part of the stream
   const spec_adjust_params &a = P.a;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -135,10 +135,10 @@ __global__ void __launch_bounds__(AJ_NT) adjust_kernel(const __grid_constant__ J
     if (counts) {
       const int32_t *seq = a.seq + b * a.seq_row_stride;
       auto see = [&](int t, int s) {  // token t of the sequence's place s
-        t -= v0;
-        if (static_cast<uint32_t>(t) >= static_cast<uint32_t>(n)) return;
-        if (s < prompt) atomicOr(count + t, kPrompt);
-        else atomicAdd(count + t, 1u);
+        const uint32_t x = static_cast<uint32_t>(t) - v0;
+        if (x >= static_cast<uint32_t>(n)) return;
+        if (s < prompt) atomicOr(count + x, kPrompt);
+        else atomicAdd(count + x, 1u);
       };
       // four tokens at a time from the first multiple of 16 bytes on, four such loads in flight
       constexpr int K = 4;
@@ -157,14 +157,14 @@ __global__ void __launch_bounds__(AJ_NT) adjust_kernel(const __grid_constant__ J
         }
       }
       for (int j = tid; j < g; j += nc) {
-        const int t = __ldg(a.draft_tokens + static_cast<int64_t>(b) * a.gamma_max + j) - v0;
-        drafts[j] = t;
-        if (static_cast<uint32_t>(t) < static_cast<uint32_t>(n)) atomicOr(count + t, kDraft);
+        const uint32_t t = static_cast<uint32_t>(__ldg(a.draft_tokens + static_cast<int64_t>(b) * a.gamma_max + j)) - v0;
+        drafts[j] = static_cast<int32_t>(t);
+        if (t < static_cast<uint32_t>(n)) atomicOr(count + t, kDraft);
       }
     }
     for (int j = tid; j < a.n_bias; j += nc) {
-      const int t = __ldg(a.bias_ids + static_cast<int64_t>(b) * a.n_bias + j) - v0;
-      if (static_cast<uint32_t>(t) < static_cast<uint32_t>(n)) atomicMax(bias + t, static_cast<uint32_t>(j + 1));
+      const uint32_t t = static_cast<uint32_t>(__ldg(a.bias_ids + static_cast<int64_t>(b) * a.n_bias + j)) - v0;
+      if (t < static_cast<uint32_t>(n)) atomicMax(bias + t, static_cast<uint32_t>(j + 1));
     }
     meet();
     for (int x0 = tid & ~31; x0 < n; x0 += nc) {  // 32 tokens' places side by side, so that their accesses are too

@@ -83,6 +83,7 @@ def test_compact_and_copy_arguments(L):
     assert L.spec_kv_copy(c, None, 1, None) == L.spec_kv_copy(c, P + 1, 1, None) == L.spec_kv_copy(c, P, -1, None) == 1
     assert L.spec_kv_copy(None, P, 1, None) == 1 and L.spec_kv_copy(c, P, (1 << 20) + 1, None) == 2
     assert L.spec_kv_copy(c, None, 0, None) == 0
+    assert L.spec_kv_compact(c, b, P, P, P + 2, None) == 1  # row_status
 
 
 def _pool(**kw):
@@ -110,6 +111,7 @@ def test_pool_arguments(L):
     fork = lambda len_=P, s=P, d=P, n=1, c=P: L.spec_kv_fork(_pool(), len_, s, d, n, c, None, None)  # noqa: E731
     assert fork(len_=None) == fork(s=None) == fork(d=None) == fork(c=None) == fork(n=-1) == fork(s=P + 1) == 1
     assert fork(n=4097) == 2 and fork(n=0, s=None, d=None, c=None) == 0
+    assert L.spec_kv_resize(_pool(), P, 1, P + 1, None) == L.spec_kv_fork(_pool(), P, P, P, 1, P, P + 2, None) == 1  # status
 
 
 def test_tree_arguments(L):
