@@ -6,10 +6,11 @@
 //   out = sum_s 2^(lse2_s - m) o_s / sum_s 2^(lse2_s - m),
 //   lse = ln 2 (m + log2 sum_s 2^(lse2_s - m)),  m = max_s lse2_s,
 // in the order of the slots (reproducible).  The partial results were written
-// just before and are read from L2.  Measured: 256 x 9 x 32
-// rows of 128, two results and more each, 56 us (the bytes alone from HBM: 14 us):
-// the chain from a row's slots to its loads; every CTA also checks all page ids
-// of its sequence.
+// just before and are read from L2.  Where a row's results are, and its weights, take
+// some hundred instructions: done by every lane for its warp's row they were 627 a row
+// and 75 % of the issue slots.  Where there are many rows, a lane does them for a row of
+// its own, and the warp then adds up rows, two at a time.  Where there are few, a row's
+// chain of loads counts: eight in flight, the first before the weights are known.
 #include "kv_span.h"
 #include "spec_tree.h"
 
@@ -18,6 +19,21 @@ namespace {
 using namespace kv;
 
 constexpr int MG_NT = 256;
+constexpr int MG_AHEAD = 8;  // results of the lanes' rows in flight
+constexpr int MG_SOME = 4;   // of one row, where there are many rows
+
+// n / d for n < 2^31: with 2^s < d <= 2^(s + 1) and mul = floor(2^(32 + s) / d) + 1 the
+// high word of n mul, s bits down, is exact (n (mul d - 2^(32 + s)) < 2^(32 + s)).
+struct Divisor {
+  uint32_t mul = 0, shift = 0;  // mul 0: d is 1
+  Divisor() = default;
+  explicit Divisor(uint32_t d) {
+    if (d == 1) return;
+    while ((2ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>((1ull << (32 + shift)) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return mul ? __umulhi(n, mul) >> shift : n; }
+};
 
 struct MP {
   View w;
@@ -27,12 +43,32 @@ struct MP {
   float *lse;
   int32_t *status;
   int32_t G, Hq, D;
-  int32_t rto, rtp, co, cp, ko, kp;  // rows per item, CTAs and key tokens of a tile, own and prefix
+  int32_t rto, rtp, co, cp;        // rows per item and CTAs, own and prefix
+  int32_t tp, ko_log2;             // key tiles of the prefix; tokens of an own tile
+  Divisor by_G, by_Hq, by_rto, by_rtp;
   const uint32_t *lost_own;          // as plan.lost, of the own items
 };
 
-// LPR lanes per row, four elements each: 16 for heads of 64, else a warp.
-template <int LPR>
+// The CTAs c0 .. c0 + n - 1 that worked on tiles x .. y of W, as owner() says, by an
+// estimate that is off by one at most: C < 2^10, so the float's error is below 2^-11.
+struct Owners {
+  uint32_t c0, n;
+};
+__device__ __forceinline__ Owners owners(uint32_t x, uint32_t y, uint32_t W, uint32_t C) {
+  static_assert(kMaxGrid < 1 << 10, "estimate");
+  const float f = __fdividef(static_cast<float>(C), static_cast<float>(W));
+  auto one = [&](uint32_t z) {
+    uint32_t q = static_cast<uint32_t>(static_cast<float>(z + 1) * f);
+    const int64_t r = static_cast<int64_t>(static_cast<uint64_t>(z + 1) * C - 1 - static_cast<uint64_t>(q) * W);
+    return r < 0 ? q - 1 : r >= W ? q + 1 : q;
+  };
+  const uint32_t c0 = one(x);
+  return {c0, one(y) - c0 + 1};
+}
+
+// LPR lanes per row, four elements each: 16 for heads of 64, else a warp.  They take RW
+// rows; what the plan says of a row, and its weights, are worked out by a lane each.
+template <int LPR, int RW>
 __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP P) {
   const View &w = P.w;
   const int b = blockIdx.y, lane = threadIdx.x % LPR;
@@ -62,80 +98,136 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
   if (P.status && blockIdx.x == 0 && threadIdx.x == 0) P.status[b] = st;
 
   const int D = P.D, G = P.G;
-  const int row = blockIdx.x * (MG_NT / LPR) + threadIdx.x / LPR;
-  const bool there = row < w.N * P.Hq;
-  const int i = row / P.Hq, h = row - i * P.Hq;
-  const int head = h / G, r = i * G + h - head * G;
-  // Partial results: those of the prefix item, then those of the own item, at
-  // lse index lo0 + s * rt (and D times that, the outputs).
-  int np = 0, all = 0;
-  int64_t lp = 0, lo = 0;
-  if (!st && there && i < n) {
-    if (w.prefix) {
-      const int tp = (w.prefix + P.kp - 1) / P.kp;
-      const int nj = (rows + P.rtp - 1) / P.rtp;
-      const uint32_t W = static_cast<uint32_t>(nj) * w.Hkv * tp, C = min(static_cast<uint32_t>(P.cp), W);
-      const uint32_t k = prow + r, y = k / P.rtp, item = head * nj + y;
-      const uint32_t c0 = owner(item * tp, W, C);
-      np = owner(item * tp + tp - 1, W, C) - c0 + 1;
-      lp = static_cast<int64_t>(item + c0) * P.rtp + (k - y * P.rtp);
+  const int row0 = (blockIdx.x * (MG_NT / LPR) + threadIdx.x / LPR) * RW, row = row0 + lane % RW;
+  // The lane's row has `all` partial results, np of them of the prefix item (places
+  // ip, ip + rtp, ..), then those of the own item (io + np rto, ..).
+  uint32_t np = 0, all = 0, ip = 0, io = 0;
+  {
+    const int i = P.by_Hq(row), h = row - i * P.Hq;
+    const int head = P.by_G(h), r = i * G + h - head * G;
+    if (!st && row < w.N * P.Hq && i < n) {
+      if (w.prefix) {
+        const uint32_t nj = P.by_rtp(rows + P.rtp - 1), W = nj * w.Hkv * P.tp;
+        const uint32_t k = prow + r, y = P.by_rtp(k), item = head * nj + y;
+        const Owners c = owners(item * P.tp, item * P.tp + P.tp - 1, W, min(static_cast<uint32_t>(P.cp), W));
+        np = c.n;
+        ip = (item + c.c0) * P.rtp + (k - y * P.rtp);
+      }
+      const int to = (own + n + (1 << P.ko_log2) - 1) >> P.ko_log2, nj = P.by_rto(n * G + P.rto - 1);
+      const uint32_t y = P.by_rto(r), j = head * nj + y, x = tile0 + j * to;
+      const Owners c = owners(x, x + to - 1, Wo, min(static_cast<uint32_t>(P.co), Wo));
+      all = np + c.n;
+      io = (item0 + j + c.c0 - np) * P.rto + (r - y * P.rto);
     }
-    const int to = (own + n + P.ko - 1) / P.ko, nj = (n * G + P.rto - 1) / P.rto;
-    const uint32_t C = min(static_cast<uint32_t>(P.co), Wo);
-    const int y = r / P.rto;
-    const uint32_t j = head * nj + y, x = tile0 + j * to;
-    const uint32_t c0 = owner(x, Wo, C);
-    all = np + owner(x + to - 1, Wo, C) - c0 + 1;
-    lo = static_cast<int64_t>(item0 + j + c0) * P.rto + (r - y * P.rto);
   }
   const bool on = lane * 4 < D;
-  const unsigned most = __reduce_max_sync(~0u, static_cast<unsigned>(all));  // of the warp's rows
-  float m = -INFINITY, sum = 0.0f;
-  float4 acc = {0, 0, 0, 0};
-  // LPR of them at a time: a lane each for the weights, then the outputs, whose
-  // loads do not depend on one another.
-  for (int s0 = 0; s0 < static_cast<int>(most); s0 += LPR) {
-    const int s = s0 + lane;
-    float v = -INFINITY;
-    if (s < all) v = s < np ? P.ql[lp + static_cast<int64_t>(s) * P.rtp] : P.pl[lo + static_cast<int64_t>(s - np) * P.rto];
-    float nm = v;
+  auto of = [](uint32_t x, int r) { return RW == 1 ? x : __shfl_sync(~0u, x, r, LPR); };  // row r's
+  auto lse_of = [&](uint32_t s, uint32_t np, uint32_t ip, uint32_t io) {  // of partial result s
+    return s < np ? P.ql[ip + s * P.rtp] : P.pl[io + s * P.rto];
+  };
+  auto load = [&](uint32_t s, uint32_t np, uint32_t ip, uint32_t io) {
+    const float *src = s < np ? P.qo + static_cast<uint64_t>(ip + s * P.rtp) * D : P.po + static_cast<uint64_t>(io + s * P.rto) * D;
+    return __ldcg(reinterpret_cast<const float4 *>(src + lane * 4));
+  };
+  auto add = [](float4 &acc, float f, const float4 &x) {
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  };
+  auto weight = [](float v, float m) { return v == -INFINITY ? 0.0f : ex2(v - m); };
+  auto put = [&](int row, const float4 &acc, float f) {
+    if (row >= w.N * P.Hq || !on) return;
+    __nv_bfloat16 *to = P.out + (static_cast<int64_t>(b) * w.N * P.Hq + row) * D + lane * 4;
+    *reinterpret_cast<__nv_bfloat162 *>(to) = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+    *reinterpret_cast<__nv_bfloat162 *>(to + 2) = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+  };
+  auto put_lse = [&](int row, float m, float sum) {
+    if (row >= w.N * P.Hq || !P.lse) return;
+    const float l = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
+    P.lse[static_cast<int64_t>(b) * w.N * P.Hq + row] = st ? __int_as_float(0x7fffffff) : l;
+  };
+  auto over = [&](float sum) { return st ? __int_as_float(0x7fffffff) : sum == 0.0f ? 0.0f : 1.0f / sum; };
+
+  float4 x[MG_AHEAD];
+  if (RW > 1 && !__any_sync(~0u, all > MG_SOME)) {
+    // a lane each for a row's weights, then MG_AHEAD / MG_SOME rows' outputs at a time
+    float c[MG_SOME], m = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int o = LPR / 2; o; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, o));
-    nm = fmaxf(nm, m);  // a NaN does not become the maximum
-    const float a = nm == -INFINITY ? 1.0f : ex2(m - nm), c = v == -INFINITY ? 0.0f : ex2(v - nm);
-    acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
-    sum *= a;
-    m = nm;
-    const int k = min(LPR, static_cast<int>(most) - s0);
-#pragma unroll 2
-    for (int j = 0; j < k; ++j) {
-      const float f = __shfl_sync(~0u, c, j, LPR);
-      const int t = s0 + j;
-      float4 x = {0, 0, 0, 0};
-      if (on && t < all) {
-        const float *src = t < np ? P.qo + (lp + static_cast<int64_t>(t) * P.rtp) * D
-                                  : P.po + (lo + static_cast<int64_t>(t - np) * P.rto) * D;
-        x = __ldcg(reinterpret_cast<const float4 *>(src + lane * 4));
+    for (uint32_t j = 0; j < MG_SOME; ++j) c[j] = j < all ? lse_of(j, np, ip, io) : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < MG_SOME; ++j) m = fmaxf(m, c[j]);  // a NaN does not become the maximum
+#pragma unroll
+    for (int j = 0; j < MG_SOME; ++j) sum += c[j] = weight(c[j], m);
+    if (lane < RW) put_lse(row, m, sum);
+    const float f = over(sum);
+    constexpr int R = MG_AHEAD / MG_SOME;
+#pragma unroll 1
+    for (int r0 = 0; r0 < RW; r0 += R) {
+      uint32_t n[R];
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        const uint32_t p = of(np, r0 + u), q = of(ip, r0 + u), o = of(io, r0 + u), its = of(all, r0 + u);
+        n[u] = on ? its : 0;
+#pragma unroll
+        for (uint32_t j = 0; j < MG_SOME; ++j)
+          if (j < n[u]) x[u * MG_SOME + j] = load(j, p, q, o);
       }
-      sum += f;
-      acc.x = fmaf(f, x.x, acc.x);
-      acc.y = fmaf(f, x.y, acc.y);
-      acc.z = fmaf(f, x.z, acc.z);
-      acc.w = fmaf(f, x.w, acc.w);
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        float4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (uint32_t j = 0; j < MG_SOME; ++j) {
+          const float g = __shfl_sync(~0u, c[j], r0 + u, LPR);
+          if (j < n[u]) add(acc, g, x[u * MG_SOME + j]);
+        }
+        put(row0 + r0 + u, acc, __shfl_sync(~0u, f, r0 + u, LPR));
+      }
     }
+    return;
   }
-  if (!there) return;
-  float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-  float l = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.6931471805599453f;
-  if (st) f = l = __int_as_float(0x7fffffff);
-  const int64_t at = static_cast<int64_t>(b) * w.N * P.Hq + row;
-  if (on) {
-    const __nv_bfloat162 lo2 = __floats2bfloat162_rn(acc.x * f, acc.y * f);
-    const __nv_bfloat162 hi2 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-    *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4) = lo2;
-    *reinterpret_cast<__nv_bfloat162 *>(P.out + at * D + lane * 4 + 2) = hi2;
+  // LPR partial results of a row at a time: a lane each for the weights, then the
+  // outputs, MG_AHEAD loads in flight together, the first of them before the weights.
+#pragma unroll 1
+  for (int rr = 0; rr < RW; ++rr) {
+    const uint32_t p = of(np, rr), q = of(ip, rr), o = of(io, rr), its = of(all, rr);
+    const uint32_t most = __reduce_max_sync(~0u, its);  // of the warp's rows
+    float m = -INFINITY, sum = 0.0f;
+    float4 acc = {0, 0, 0, 0};
+    for (uint32_t s0 = 0; s0 < most; s0 += LPR) {
+      const uint32_t s = s0 + lane, k = min(static_cast<uint32_t>(LPR), most - s0);
+      auto ahead = [&](uint32_t j0) {  // four at a time
+#pragma unroll
+        for (uint32_t u = 0; u < MG_AHEAD; ++u) {
+          if (u % 4 == 0 && j0 + u >= k) break;
+          x[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (on && s0 + j0 + u < its) x[u] = load(s0 + j0 + u, p, q, o);
+        }
+      };
+      const float v = s < its ? lse_of(s, p, q, o) : -INFINITY;
+      ahead(0);
+      float nm = v;
+#pragma unroll
+      for (int d = LPR / 2; d; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(~0u, nm, d));
+      nm = fmaxf(nm, m);
+      const float a = nm == -INFINITY ? 1.0f : ex2(m - nm), c = weight(v, nm);
+      acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
+      sum *= a;
+      m = nm;
+      for (uint32_t j0 = 0; j0 < k; j0 += MG_AHEAD) {
+        if (j0) ahead(j0);
+#pragma unroll
+        for (uint32_t u = 0; u < MG_AHEAD; ++u) {
+          if (j0 + u >= k) break;
+          const float g = __shfl_sync(~0u, c, j0 + u, LPR);
+          sum += g;
+          add(acc, g, x[u]);
+        }
+      }
+    }
+    put(row0 + rr, acc, over(sum));
+    if (lane == 0) put_lse(row0 + rr, m, sum);
   }
-  if (lane == 0 && P.lse) P.lse[at] = l;
 }
 
 // Row warps (of 16 rows) of an item: an item costs its rows, padding included,
@@ -184,7 +276,8 @@ struct Layout {
   int wo, wp;               // row warps of own and prefix items
   bool dense, dense_own;
   int ro, ko, rp, kp;       // rows and key tokens of a tile, own and prefix
-  int64_t tiles_o, tiles_p; // key tiles at most
+  int64_t items_o, items_p; // items and key tiles at most
+  int64_t tiles_o, tiles_p;
   size_t plan, po, pl, qo, ql, bytes;
 };
 
@@ -208,6 +301,7 @@ bool lay_out(const View &w, int D, int G, bool tree, Layout &L) {
   L.tiles_p = ip * ((w.prefix + static_cast<int64_t>(L.kp) - 1) / L.kp);
   if (io > INT32_MAX / 2 || ip > INT32_MAX / 2 || L.tiles_o > INT32_MAX || L.tiles_p > INT32_MAX)
     return false;
+  L.items_o = io, L.items_p = ip;
   const size_t so = static_cast<size_t>(io + (L.dense_own ? kMaxDense : kMaxGrid)) * L.ro;
   const size_t sp = ip ? static_cast<size_t>(ip + (L.dense ? kMaxDense : kMaxGrid)) * L.rp : 0;
   L.plan = 0;
@@ -281,7 +375,10 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
   MP m = {};
   m.w = P.w;
   m.plan = P.plan;
-  m.G = G, m.Hq = n_heads, m.D = D, m.rto = L.ro, m.rtp = L.rp, m.ko = L.ko, m.kp = L.kp;
+  m.G = G, m.Hq = n_heads, m.D = D, m.rto = L.ro, m.rtp = L.rp;
+  m.by_G = Divisor(G), m.by_Hq = Divisor(n_heads), m.by_rto = Divisor(L.ro), m.by_rtp = Divisor(L.rp);
+  m.tp = static_cast<int>((P.w.prefix + static_cast<int64_t>(L.kp) - 1) / L.kp);
+  while (1 << m.ko_log2 < L.ko) ++m.ko_log2;
   m.out = static_cast<__nv_bfloat16 *>(out);
   m.lse = lse;
   m.status = row_status;
@@ -318,14 +415,26 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const int per = MG_NT / (D == 64 ? 16 : 32);  // rows per CTA
-  cfg.gridDim = dim3((P.w.N * n_heads + per - 1) / per, P.w.B);
+  const int64_t rows = static_cast<int64_t>(P.w.N) * n_heads;  // of a sequence
+  const int64_t all = rows * P.w.B;
+  // partial results of a row, about
+  const int64_t some = (P.w.prefix ? 1 + m.cp / L.items_p : 0) + 1 + m.co / L.items_o;
+  // Rows of a warp (of half a warp with heads of 64).  Measured, 32 heads of 128 over 8,
+  // in us for the call, 1 / 4 / 8 rows: 4096 rows 17.6 / 17.6 / 17.6 (16 trees of 8
+  // nodes, 300 tokens), 8192 26.5 / 24.2 / 24.7, 16384 35.4 / 28.0 / 30.2, 32768 110 /
+  // 95.3 / 93.8 (1000 tokens); 16 heads of 64: 8192 20.8 / 19.7 / 21.2, 32768 160 / 154 /
+  // 158.  Rows of more than MG_SOME results come one by one: 1 / 4 for 11 of them and
+  // 10240 rows 90 / 91, for 5 and 11520 36.7 / 39.7.
+  const int rw = some > MG_SOME || all <= 152 * 48 ? 1 : all <= 152 * 192 * (D == 64 ? 2 : 1) ? 4 : 8;
+  const int per = MG_NT / (D == 64 ? 16 : 32) * rw;  // rows per CTA
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per), P.w.B);
   cfg.blockDim = dim3(MG_NT);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = D == 64 ? cudaLaunchKernelEx(&cfg, merge_kernel<16>, m)
-                                : cudaLaunchKernelEx(&cfg, merge_kernel<32>, m);
+  auto *merge = D == 64 ? rw == 1 ? merge_kernel<16, 1> : rw == 4 ? merge_kernel<16, 4> : merge_kernel<16, 8>
+                        : rw == 1 ? merge_kernel<32, 1> : rw == 4 ? merge_kernel<32, 4> : merge_kernel<32, 8>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, merge, m);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
