@@ -19,8 +19,7 @@ namespace {
 using namespace kv;
 
 constexpr int MG_NT = 256;
-constexpr int MG_AHEAD = 8;  // results of the lanes' rows in flight
-constexpr int MG_SOME = 4;   // of one row, where there are many rows
+constexpr int MG_AHEAD = 8;  // partial results in flight
 
 // n / d for n < 2^31: with 2^s < d <= 2^(s + 1) and mul = floor(2^(32 + s) / d) + 1 the
 // high word of n mul, s bits down, is exact (n (mul d - 2^(32 + s)) < 2^(32 + s)).
@@ -67,8 +66,9 @@ __device__ __forceinline__ Owners owners(uint32_t x, uint32_t y, uint32_t W, uin
 }
 
 // LPR lanes per row, four elements each: 16 for heads of 64, else a warp.  They take RW
-// rows; what the plan says of a row, and its weights, are worked out by a lane each.
-template <int LPR, int RW>
+// rows; what the plan says of a row, and its weights, are worked out by a lane each, the
+// weights where none of the rows has more than SOME partial results.
+template <int LPR, int RW, int SOME>
 __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP P) {
   const View &w = P.w;
   const int b = blockIdx.y, lane = threadIdx.x % LPR;
@@ -150,18 +150,18 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
   auto over = [&](float sum) { return st ? __int_as_float(0x7fffffff) : sum == 0.0f ? 0.0f : 1.0f / sum; };
 
   float4 x[MG_AHEAD];
-  if (RW > 1 && !__any_sync(~0u, all > MG_SOME)) {
-    // a lane each for a row's weights, then MG_AHEAD / MG_SOME rows' outputs at a time
-    float c[MG_SOME], m = -INFINITY, sum = 0.0f;
+  if (RW > 1 && !__any_sync(~0u, all > SOME)) {
+    // a lane each for a row's weights, then the outputs of one row or two at a time
+    float c[SOME], m = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (uint32_t j = 0; j < MG_SOME; ++j) c[j] = j < all ? lse_of(j, np, ip, io) : -INFINITY;
+    for (uint32_t j = 0; j < SOME; ++j) c[j] = j < all ? lse_of(j, np, ip, io) : -INFINITY;
 #pragma unroll
-    for (int j = 0; j < MG_SOME; ++j) m = fmaxf(m, c[j]);  // a NaN does not become the maximum
+    for (int j = 0; j < SOME; ++j) m = fmaxf(m, c[j]);  // a NaN does not become the maximum
 #pragma unroll
-    for (int j = 0; j < MG_SOME; ++j) sum += c[j] = weight(c[j], m);
+    for (int j = 0; j < SOME; ++j) sum += c[j] = weight(c[j], m);
     if (lane < RW) put_lse(row, m, sum);
     const float f = over(sum);
-    constexpr int R = MG_AHEAD / MG_SOME;
+    constexpr int R = MG_AHEAD / SOME;
 #pragma unroll 1
     for (int r0 = 0; r0 < RW; r0 += R) {
       uint32_t n[R];
@@ -170,16 +170,16 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
         const uint32_t p = of(np, r0 + u), q = of(ip, r0 + u), o = of(io, r0 + u), its = of(all, r0 + u);
         n[u] = on ? its : 0;
 #pragma unroll
-        for (uint32_t j = 0; j < MG_SOME; ++j)
-          if (j < n[u]) x[u * MG_SOME + j] = load(j, p, q, o);
+        for (uint32_t j = 0; j < SOME; ++j)
+          if (j < n[u]) x[u * SOME + j] = load(j, p, q, o);
       }
 #pragma unroll
       for (int u = 0; u < R; ++u) {
         float4 acc = {0, 0, 0, 0};
 #pragma unroll
-        for (uint32_t j = 0; j < MG_SOME; ++j) {
+        for (uint32_t j = 0; j < SOME; ++j) {
           const float g = __shfl_sync(~0u, c[j], r0 + u, LPR);
-          if (j < n[u]) add(acc, g, x[u * MG_SOME + j]);
+          if (j < n[u]) add(acc, g, x[u * SOME + j]);
         }
         put(row0 + r0 + u, acc, __shfl_sync(~0u, f, r0 + u, LPR));
       }
@@ -246,15 +246,15 @@ int row_warps(int64_t rows) {
 // from the 65th on the span kernel reads the keys again.  Measured, 8 heads of 128
 // in e4m3, replayed calls, span / dense kernel in us:
 //   prefix   16 rows      64 rows      80 rows      320 rows
-//      500   14.2 / 15.8  17.7 / 16.7  19.4 / 16.9  35.6 / 31.6
-//     1000   17.7 / 17.4  26.7 / 18.4  23.1 / 18.9  43.5 / 37.1
-//     2000   24.3 / 21.1  33.8 / 27.5  35.0 / 27.5  48.7 / 39.3
-//     4096   40.7 / 28.0  46.9 / 33.2  41.0 / 30.3  58.5 / 47.2
-//     8192   42.1 / 31.7  50.7 / 32.9  47.5 / 33.3  76.3 / 54.6
+//      500   11.5 / 14.4  14.7 / 14.9  16.1 / 15.0  29.0 / 29.3
+//     1000   13.1 / 14.8  22.0 / 15.5  18.0 / 15.6  35.3 / 30.7
+//     2000   15.5 / 16.3  24.5 / 22.7  25.6 / 22.7  40.2 / 32.9
+//     4096   24.4 / 22.3  30.8 / 24.7  29.5 / 24.5  50.4 / 39.8
+//     8192   26.7 / 26.0  34.5 / 27.3  34.6 / 27.5  67.9 / 49.2
 // Heads of 64 and bfloat16 caches cross over at 500 to 1000 tokens too.  So the
 // prefix's length says more than the rows do; the rule is one of rows because the
-// two kernels round differently (include/spec_kv.h).  It costs up to 18 us below 65
-// rows, where the prefix is long, and gains everywhere above.
+// two kernels round differently (include/spec_kv.h).  It costs up to 7 us below 65
+// rows, where the prefix is long, and 2 us at most above, where it is short.
 constexpr int64_t kDenseRows = 65;
 
 // Query rows of a sequence's key/value head from which a tree's own tokens go to the
@@ -262,13 +262,13 @@ constexpr int64_t kDenseRows = 65;
 // key/value heads of 128 in e4m3, sequences x tokens, replayed calls, span / dense
 // kernel in us:
 //   rows   1 x 100   1 x 8000   8 x 500   8 x 4000   64 x 100   64 x 1000
-//     48   12 / 14    47 / 31   21 / 24    50 / 48    36 / 44     87 / 93
-//     64   13 / 14    45 / 31   29 / 26    54 / 48    42 / 48    106 / 99
-//     80   12 / 14    42 / 31   28 / 26    69 / 48    54 / 53    149 / 104
-//    128   13 / 15    43 / 32   32 / 27    84 / 49    81 / 75    206 / 129
-//    256   14 / 18    57 / 36   45 / 37   152 / 62   157 / 125   398 / 186
+//     48   11 / 13    29 / 22   17 / 20    43 / 43    28 / 37     80 / 86
+//     64   11 / 13    29 / 22   25 / 24    50 / 46    30 / 37     94 / 87
+//     80   11 / 13    32 / 22   25 / 25    66 / 46    41 / 40    138 / 91
+//    128   12 / 13    35 / 23   32 / 25    85 / 47    60 / 52    185 / 106
+//    256   12 / 17    48 / 27   38 / 31   146 / 56   117 / 81    356 / 143
 // Heads of 64 cross over between 64 and 104 rows, bfloat16 caches as these do.  From
-// here on the dense kernel loses 4 us at most, where the context is short.
+// here on the dense kernel loses 5 us at most, where the context is short.
 constexpr int64_t kDenseTreeRows = 65;
 static_assert(2 * kMaxDense <= kMaxGrid, "plan: words for the CTAs of both dense launches");
 
@@ -423,17 +423,18 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
   // in us for the call, 1 / 4 / 8 rows: 4096 rows 17.6 / 17.6 / 17.6 (16 trees of 8
   // nodes, 300 tokens), 8192 26.5 / 24.2 / 24.7, 16384 35.4 / 28.0 / 30.2, 32768 110 /
   // 95.3 / 93.8 (1000 tokens); 16 heads of 64: 8192 20.8 / 19.7 / 21.2, 32768 160 / 154 /
-  // 158.  Rows of more than MG_SOME results come one by one: 1 / 4 for 11 of them and
-  // 10240 rows 90 / 91, for 5 and 11520 36.7 / 39.7.
-  const int rw = some > MG_SOME || all <= 152 * 48 ? 1 : all <= 152 * 192 * (D == 64 ? 2 : 1) ? 4 : 8;
+  // 158.  With some five results a row, 1 / 4 rows of up to eight: 10240 rows behind a
+  // prefix of 1000 62.1 / 59.1, 8192 rows of 4 trees over 4000 43.2 / 41.9.
+  const int rw = all <= 152 * 48 ? 1 : some > 4 || all <= 152 * 192 * (D == 64 ? 2 : 1) ? 4 : 8;
   const int per = MG_NT / (D == 64 ? 16 : 32) * rw;  // rows per CTA
   cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per), P.w.B);
   cfg.blockDim = dim3(MG_NT);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  auto *merge = D == 64 ? rw == 1 ? merge_kernel<16, 1> : rw == 4 ? merge_kernel<16, 4> : merge_kernel<16, 8>
-                        : rw == 1 ? merge_kernel<32, 1> : rw == 4 ? merge_kernel<32, 4> : merge_kernel<32, 8>;
+  auto pick = [&](auto *one, auto *four, auto *four8, auto *eight) { return rw == 1 ? one : rw == 8 ? eight : some > 4 ? four8 : four; };
+  auto *merge = D == 64 ? pick(merge_kernel<16, 1, 4>, merge_kernel<16, 4, 4>, merge_kernel<16, 4, 8>, merge_kernel<16, 8, 4>)
+                        : pick(merge_kernel<32, 1, 4>, merge_kernel<32, 4, 4>, merge_kernel<32, 4, 8>, merge_kernel<32, 8, 4>);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, merge, m);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
