@@ -355,3 +355,31 @@ def test_attend_tree_workspaces_and_outputs_are_checked(sv):  # noqa: F811
         got = call(sv, s, workspace=ws, out=(torch.empty_like(want[0]), torch.empty_like(want[1])))
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert torch.equal(call(sv, s, scale=0.125)[0], want[0])  # 64 ** -0.5
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("case", [(64, 16, 32, 4, 80, 16, 0), (120, 16, 32, 8, 64, 16, 0), (64, 5, 32, 8, 128, 32, 500),
+                                  (30, 9, 32, 8, 96, 64, 0)], ids=str)
+def test_attend_tree_many_rows(sv, fmt, case):  # noqa: F811
+    """Several rows of a warp in the merge: with as many partial results as most rows
+    have, with many (one sequence is long), of sequences with an error, past gamma_b."""
+    import torch
+    B, N = case[:2]
+    rng = np.random.default_rng(6)
+    lens = rng.integers(0, 60, B)
+    lens[2] = 2500
+    g = rng.integers(0, N, B)
+    s = tree_case(sv, 72, fmt, *case, lens, gammas=g)
+    want = reference(s)
+    least = (int(s["lens"].max()) + N) * 2.0 ** -33 * 3.5 if fmt == "e4m3" else 0.0  # as in check
+    s["g"] = g.copy()
+    s["g"][3] = N
+    s["table"][7, 0] = 1 << 30
+    s["lens"][7] = s["prefix"] + 5
+    got = call(sv, s)
+    status = np_of(got[2])
+    assert status[3] == 16 and status[7] == sv.ROW_BAD_PAGE and (np.delete(status, [3, 7]) == 0).all()
+    for b in (3, 7):
+        assert torch.isnan(got[0][b]).all() and torch.isnan(got[1][b]).all()
+    good = np.delete(np.arange(B), [3, 7])
+    check_attend([x[i32(good).long()] for x in got[:2]], [x[good] for x in want], fmt, g[good], least=least)
