@@ -13,17 +13,20 @@
 // without the cluster's barriers.  Then the counts are read, 32 a thread, and the
 // free pages numbered by sums over the warp, the CTA and the cluster, in the
 // order of the page ids: page of number k goes to the row in whose sum k falls.
+// The counts go to the CTAs in turns of 1024 (in eight long pieces the lowest free
+// pages were a few CTAs' work alone: 64 x 1024 of them 12 us in place of 7).
 // Nothing depends on the order of atomics: they add to counts, or or bits.
 //
 // Bound: the chain of loads and cluster barriers; copies by memory.  Measured (replayed
 // calls): four entries each of 256 accepted paths, 8 heads of 128 in bfloat16, 5.7 us.
-// 512 rows' room for nine tokens (287 pages of 98304) and back 11.5 us for both calls, 2.8
-// where there is nothing to do; 64 x 1024 pages of 262144 and back 27 us.  31 forks each
-// of 8 rows of 23 .. 31 pages of 128 tokens and back 20 us, the copies of their last pages
+// 512 rows' room for nine tokens (287 pages of 98304) and back 10.7 us for both calls, 2.8
+// where there is nothing to do; 64 x 1024 pages of 262144 and back 19 us.  31 forks each
+// of 8 rows of 23 .. 31 pages of 128 tokens and back 18 us, the copies of their last pages
 // (62 MB in and out) 8.0 us, 7.8 TB/s: what was read just before is in L2.
 #include <cooperative_groups.h>
 
 #include <atomic>
+#include <type_traits>
 #include <utility>
 
 #include "kv_common.cuh"
@@ -172,10 +175,12 @@ struct Pool {
 };
 
 struct TableShared {
-  uint16_t list[TB_NT * TB_EACH];  // free pages of the CTA's part of a round
+  uint16_t list[TB_NT * TB_EACH];  // free pages of the CTA's parts of a round: warp, place in its 1024 counts
   unsigned long long warp2[TB_NT / 32];
-  uint32_t warp[TB_NT / 32];
-  uint32_t found[2];  // free pages of this CTA's part of a round, by the round's parity
+  uint32_t count[2][TB_NT / 32];  // free pages of the warps' parts of a round, by the round's parity
+  uint32_t first[TB_NT / 32];     // their numbers in the round
+  uint32_t number[TB_NT / 32];    // what a warp's places on the list are behind their pages' numbers
+  uint32_t all;                   // free pages of the round
 };
 
 // Who works on the tables: the whole cluster, or its first CTA.
@@ -239,13 +244,32 @@ __device__ __forceinline__ int before(const uint32_t *cum, int n, uint32_t x) {
   }
   return l;
 }
+// The same for several x, whose loads do not wait for one another.
+template <int K>
+__device__ __forceinline__ void before(const uint32_t *cum, int n, const uint32_t (&x)[K], int (&i)[K]) {
+#pragma unroll
+  for (int u = 0; u < K; ++u) i[u] = 0;
+  for (int s = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; s; s >>= 1)
+#pragma unroll
+    for (int u = 0; u < K; ++u)
+      if (i[u] + s < n && cum[i[u] + s] <= x[u]) i[u] += s;
+}
 
-// Of the thread's 32 counts in round `at` (the first count of the round), those
-// that are of free pages: bit 4 u + k is count at + 1024 warp + 128 u + 4 lane + k
-// (warps numbered over the cluster).
-__device__ uint32_t free_bits(const Pool &P, int64_t at, unsigned rank) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t i0 = at + (static_cast<int64_t>(rank) * (TB_NT / 32) + warp) * 1024 + 4 * lane;
+// f(K, i) for i = from, from + K stride, .. below n: for i, i + stride, .. as far as they
+// are below n; K is one where no thread has more, since a group costs what all of it does.
+template <int K, class F>
+__device__ __forceinline__ void in_groups(uint32_t from, uint32_t stride, uint32_t n, F f) {
+  if (n <= stride) {
+    if (from < n) f(std::integral_constant<int, 1>{}, from);
+  } else {
+    for (uint32_t i = from; i < n; i += K * stride) f(std::integral_constant<int, K>{}, i);
+  }
+}
+
+// Of the thread's 32 counts from count i0 on (the warp's part: 1024 counts), those
+// that are of free pages: bit 4 u + k is count i0 + 128 u + 4 lane + k.
+__device__ uint32_t free_bits(const Pool &P, int64_t i0) {
+  i0 += 4 * (threadIdx.x & 31);
   uint32_t bits = 0;
   if (P.vec && i0 + 7 * 128 + 4 <= P.n_pages) {
     int4 x[8];
@@ -267,42 +291,65 @@ __device__ uint32_t free_bits(const Pool &P, int64_t at, unsigned rank) {
   return bits;
 }
 
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ uint32_t sum_to(uint32_t x) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(~0u, x, o);
+    if ((threadIdx.x & 31) >= o) x += t;
+  }
+  return x;
+}
+
 // Takes the lowest free pages for the rows of cum (n + 1 sums of what they need):
 // give(row, k, page) for the k-th page of each row that is served, that is whose
 // sum is within what the pool has.  Returns the number of free pages, or any
 // number from the rows' sum on.  All CTAs of the team call it, after a team's
-// barrier behind the last change of a count.
+// barrier behind the last change of a count.  A round's parts of 1024 counts go to
+// the CTAs in turn, so that each has its share of the pages that are given: the
+// lowest ones are in the first parts.
 template <class F>
 __device__ uint32_t take_pages(const Pool &P, const uint32_t *cum, int n, const Team &team, TableShared &S, F give) {
-  const unsigned rank = team.rank;
+  const unsigned rank = team.rank, ctas = team.ctas;
   const int64_t round = team.round();
   const uint32_t total = cum[n];
   if (total == 0) return 0;
   const int rounds = static_cast<int>((P.n_pages + round - 1) / round);
-  const int lane = threadIdx.x & 31;
-  uint32_t bits = 0, at0 = 0, base = 0, all = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t bits = 0;           // the thread's free pages of the round,
+  uint32_t size = 0, first = 0;  // those of the CTA's warp `lane`, the number of the first of them in the round
   int turn = 0;
-  // round r: the free pages of the thread, their number before the thread's warp in
-  // this CTA, of this CTA, and before it in the round; returns that of the whole round
-  auto count = [&](int r) -> uint32_t {
-    bits = free_bits(P, r * round, rank);
-    uint32_t here = 0;
-    at0 = __shfl_sync(~0u, cta_sum<uint32_t>(__popc(bits), S.warp, &all), 0);
-    base = 0;
-    if (team.ctas == 1) return all;
-    cg::cluster_group cl = cg::this_cluster();
-    uint32_t *slot = &S.found[turn++ & 1];
-    if (threadIdx.x == 0) *slot = all;
-    cl.sync();
-    uint32_t x[TB_CTAS];
-#pragma unroll
-    for (unsigned c = 0; c < TB_CTAS; ++c) x[c] = *cl.map_shared_rank(slot, c);
-#pragma unroll
-    for (unsigned c = 0; c < TB_CTAS; ++c) {
-      if (c < rank) base += x[c];
-      here += x[c];
+  auto count = [&](int r) -> uint32_t {  // free pages of round r
+    bits = free_bits(P, r * round + (static_cast<int64_t>(warp) * ctas + rank) * 1024);
+    uint32_t *mine = S.count[turn++ & 1];
+    const uint32_t c = __reduce_add_sync(~0u, __popc(bits));
+    if (lane == 0) mine[warp] = c;
+    if (ctas == 1) {
+      __syncthreads();
+      size = mine[lane];
+      const uint32_t to = sum_to(size);
+      first = to - size;
+      return __shfl_sync(~0u, to, 31);
     }
-    return here;
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    if (warp == 0) {  // the parts' order: warps, then CTAs
+      uint32_t x[TB_CTAS], all = 0, ahead = 0;
+#pragma unroll
+      for (unsigned c = 0; c < TB_CTAS; ++c) x[c] = *cl.map_shared_rank(mine + lane, c);
+#pragma unroll
+      for (unsigned c = 0; c < TB_CTAS; ++c) {
+        if (c < rank) ahead += x[c];
+        all += x[c];
+      }
+      const uint32_t to = sum_to(all);
+      S.first[lane] = to - all + ahead;
+      if (lane == 31) S.all = to;
+    }
+    __syncthreads();
+    size = mine[lane];
+    first = S.first[lane];
+    return S.all;
   };
   uint32_t found = 0;
   int counted = 0;
@@ -312,40 +359,53 @@ __device__ uint32_t take_pages(const Pool &P, const uint32_t *cum, int n, const 
   uint32_t sum = 0;
   for (int r = 0; r < rounds && sum < limit; ++r) {
     const uint32_t here = counted == 1 ? found : count(r);  // one round: as counted
-    // a warp's pages in the order of u, lane, k: sums over the lanes for each u,
-    // four of them in a word (32 x 4 counts fit eight bits)
-    uint32_t lo = 0, hi = 0;
+    // The warps' places on the CTA's list, for those that are given.
+    const uint32_t number = sum + first, given = number < limit ? min(limit - number, size) : 0;
+    const uint32_t to = sum_to(given);
+    if (warp == 0) S.number[lane] = number - (to - given);
+    const uint32_t mine = __shfl_sync(~0u, to, 31);  // of the CTA
+    const uint32_t base = __shfl_sync(~0u, to - given, warp), end = base + __shfl_sync(~0u, given, warp);
+    if (base < end) {
+      // a warp's pages in the order of u, lane, k: sums over the lanes for each u,
+      // four of them in a word (32 x 4 counts fit eight bits)
+      uint32_t lo = 0, hi = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      lo |= __popc(bits >> (4 * u) & 15) << (8 * u);
-      hi |= __popc(bits >> (16 + 4 * u) & 15) << (8 * u);
-    }
-    uint32_t el = lo, eh = hi;
+      for (int u = 0; u < 4; ++u) {
+        lo |= __popc(bits >> (4 * u) & 15) << (8 * u);
+        hi |= __popc(bits >> (16 + 4 * u) & 15) << (8 * u);
+      }
+      uint32_t el = sum_to(lo), eh = sum_to(hi);
+      const uint32_t al = __shfl_sync(~0u, el, 31), ah = __shfl_sync(~0u, eh, 31);
+      el -= lo, eh -= hi;
+      uint32_t at = base;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t tl = __shfl_up_sync(~0u, el, o), th = __shfl_up_sync(~0u, eh, o);
-      if (lane >= o) el += tl, eh += th;
-    }
-    const uint32_t al = __shfl_sync(~0u, el, 31), ah = __shfl_sync(~0u, eh, 31);
-    el -= lo, eh -= hi;
-    // the CTA's free pages in their order, as numbers within its part of the round,
-    // so that the threads can take them side by side
-    const uint32_t first = sum + base, mine = first < limit ? min(limit - first, all) : 0;  // of the CTA
-    uint32_t at = at0;  // of the warp
-#pragma unroll 1
-    for (int u = 0; u < 8 && at < mine; ++u) {
-      uint32_t k = at + ((u < 4 ? el : eh) >> (8 * (u & 3)) & 255);
-      for (uint32_t m = bits >> (4 * u) & 15; m && k < mine; m &= m - 1, ++k)
-        S.list[k] = static_cast<uint16_t>((threadIdx.x >> 5) * 1024 + 128 * u + 4 * lane + __ffs(m) - 1);
-      at += (u < 4 ? al : ah) >> (8 * (u & 3)) & 255;
+      for (int u = 0; u < 8; ++u) {
+        uint32_t k = at + ((u < 4 ? el : eh) >> (8 * (u & 3)) & 255);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const bool is = bits >> (4 * u + v) & 1;
+          if (is && k < end) S.list[k] = static_cast<uint16_t>(warp * 1024 + 128 * u + 4 * lane + v);
+          k += is;
+        }
+        at += (u < 4 ? al : ah) >> (8 * (u & 3)) & 255;
+      }
     }
     __syncthreads();
-    const int64_t i0 = r * round + static_cast<int64_t>(rank) * TB_NT * TB_EACH;
-    int row = -1;
-    for (uint32_t k = threadIdx.x; k < mine; k += TB_NT) {
-      if (row < 0 || first + k >= cum[row + 1]) row = before(cum, n, first + k);
-      give(row, first + k - cum[row], static_cast<int32_t>(i0 + S.list[k]));
-    }
+    in_groups<4>(threadIdx.x, TB_NT, mine, [&](auto K_, uint32_t k0) {
+      constexpr int K = decltype(K_)::value;
+      uint32_t x[K];
+      int id[K], row[K];
+#pragma unroll
+      for (int u = 0; u < K; ++u) {
+        const uint32_t k = min(k0 + u * TB_NT, mine - 1), e = S.list[k];
+        x[u] = k + S.number[e >> 10];
+        id[u] = static_cast<int>(r * round + (static_cast<int64_t>(e >> 10) * ctas + rank) * 1024 + (e & 1023));
+      }
+      before(cum, n, x, row);
+#pragma unroll
+      for (int u = 0; u < K; ++u)
+        if (k0 + u * TB_NT < mine) give(row[u], x[u] - cum[row[u]], id[u]);
+    });
     __syncthreads();
     sum += here;
   }
@@ -397,29 +457,25 @@ __global__ void __cluster_dims__(TB_CTAS, 1, 1) __launch_bounds__(TB_NT) resize_
     team.ctas = 1;
   }
   if (gone[B]) {
-    const uint32_t np = static_cast<uint32_t>(P.n_pages);
-    int row = -1;
-    uint32_t end = 0;
-    const uint32_t stride = team.ctas * TB_NT;
-    for (uint32_t x0 = team.rank * TB_NT + tid; x0 < gone[B]; x0 += 4 * stride) {
-      int id[4], of[4];
+    const uint32_t np = static_cast<uint32_t>(P.n_pages), many = gone[B], stride = team.ctas * TB_NT;
+    in_groups<8>(team.rank * TB_NT + tid, stride, many, [&](auto K_, uint32_t x0) {
+      constexpr int K = decltype(K_)::value;
+      uint32_t x[K];
+      int id[K], of[K];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t x = x0 + u * stride;
-        of[u] = -1;
-        if (x >= gone[B]) continue;
-        if (row < 0 || x >= end) row = before(gone, B, x), end = gone[row + 1];
-        // the last gone[row + 1] - gone[row] entries of the row
-        of[u] = row;
-        id[u] = P.table[row * P.tstride + has[row] - static_cast<int>(end - x)];
-      }
+      for (int u = 0; u < K; ++u) x[u] = min(x0 + u * stride, many - 1);
+      before(gone, B, x, of);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (of[u] < 0) continue;
+      for (int u = 0; u < K; ++u)  // the last gone[row + 1] - gone[row] entries of the row
+        if (x0 + u * stride < many)
+          id[u] = P.table[of[u] * P.tstride + has[of[u]] - static_cast<int>(gone[of[u] + 1] - x[u])];
+#pragma unroll
+      for (int u = 0; u < K; ++u) {
+        if (x0 + u * stride >= many) continue;
         if (static_cast<uint32_t>(id[u]) < np) atomicSub(P.refs + id[u], 1);
         else if (R.status) atomicOr(R.status + of[u], SPEC_ROW_BAD_PAGE);
       }
-    }
+    });
     team.sync();  // the counts
   }
   const uint32_t found = take_pages(P, cum, B, team, S, [&](int row, uint32_t k, int32_t id) {
@@ -514,28 +570,30 @@ __global__ void __cluster_dims__(TB_CTAS, 1, 1) __launch_bounds__(TB_NT) fork_ke
       atomicOr(F.status + j, SPEC_ROW_BAD_PAGE);
     }
   });
-  int j = -1;
-  const uint32_t stride = team.ctas * TB_NT;
-  for (uint32_t x0 = team.rank * TB_NT + tid; x0 < shared[n]; x0 += 4 * stride) {
-    int id[4], of[4];
+  const uint32_t stride = team.ctas * TB_NT, many = shared[n];
+  in_groups<4>(team.rank * TB_NT + tid, stride, many, [&](auto K_, uint32_t x0) {
+    constexpr int K = decltype(K_)::value;
+    uint32_t x[K];
+    int id[K], of[K];
+    bool on[K];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t x = x0 + u * stride;
-      of[u] = -1;
-      if (x >= shared[n]) continue;
-      if (j < 0 || x >= shared[j + 1]) j = before(shared, n, x);
-      if (cum[j + 1] > cum[j] && cum[j + 1] > found) continue;
-      of[u] = j;
-      id[u] = P.table[F.src[j] * P.tstride + static_cast<int>(x - shared[j])];
+    for (int u = 0; u < K; ++u) x[u] = min(x0 + u * stride, many - 1);
+    before(shared, n, x, of);
+#pragma unroll
+    for (int u = 0; u < K; ++u) {
+      const uint32_t to = cum[of[u] + 1];
+      on[u] = x0 + u * stride < many && !(to > cum[of[u]] && to > found);
+      x[u] -= shared[of[u]];
+      if (on[u]) id[u] = P.table[F.src[of[u]] * P.tstride + static_cast<int>(x[u])];
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (of[u] < 0) continue;
-      P.table[F.dst[of[u]] * P.tstride + static_cast<int>(x0 + u * stride - shared[of[u]])] = id[u];
+    for (int u = 0; u < K; ++u) {
+      if (!on[u]) continue;
+      P.table[F.dst[of[u]] * P.tstride + static_cast<int>(x[u])] = id[u];
       if (static_cast<uint32_t>(id[u]) < np) atomicAdd(P.refs + id[u], 1);
       else if (F.status) atomicOr(F.status + of[u], SPEC_ROW_BAD_PAGE);
     }
-  }
+  });
   for (int k = team.rank * TB_NT + tid; k < n; k += team.ctas * TB_NT) {
     if (!fine[k]) continue;
     const uint32_t take = cum[k + 1] - cum[k];
