@@ -9,8 +9,9 @@
 // just before and are read from L2.  Where a row's results are, and its weights, take
 // some hundred instructions: done by every lane for its warp's row they were 627 a row
 // and 75 % of the issue slots.  Where there are many rows, a lane does them for a row of
-// its own, and the warp then adds up rows, two at a time.  Where there are few, a row's
-// chain of loads counts: eight in flight, the first before the weights are known.
+// its own, and the warp then adds up rows, two at a time: 256 x 9 x 32 rows of 128, two to
+// four results each, 28 us in place of 57.  Where there are few, a row's chain of loads
+// counts: eight in flight, the first before the weights are known.
 #include "kv_span.h"
 #include "spec_tree.h"
 

@@ -45,10 +45,10 @@
 // with own items).
 //
 // Measured: 256 x 9 queries of 32 heads (9216 rows a key/value head of 128) over
-// 8192 e4m3 tokens 287 us, 1077 TFLOP/s, 57 % of the products' rate: tensor pipe 46 %
+// 8192 e4m3 tokens 285 us, 1085 TFLOP/s, 57 % of the products' rate: tensor pipe 46 %
 // active, 58 % of the issue slots used (over bfloat16 tokens a call takes 7 % less: the
 // conversions).  16 trees of 64 nodes of 32 heads over
-// 2000..8192 tokens 108 us, 781 TFLOP/s: 34 tiles and two items a CTA, whose ends show.
+// 2000..8192 tokens 105 us, 800 TFLOP/s: 34 tiles and two items a CTA, whose ends show.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -188,6 +188,29 @@ def test_resize_many_pages(sv):  # noqa: F811
     assert int((np_of(r) <= 0).sum()) == free
 
 
+@pytest.mark.parametrize("n_pages,busy,B,off", [(600001, 0.95, 50, 0), (262144, 0.0, 64, 0), (262145, 0.6, 9, 3), (40000, 0.5, 300, 0)])
+def test_resize_by_many_ctas(sv, n_pages, busy, B, off):  # noqa: F811
+    """Thousands of pages for a call, from a pool that is mostly taken, empty, or taken in long runs."""
+    import torch
+    rng = np.random.default_rng(n_pages)
+    refs = (rng.random(n_pages) < busy).astype(int)
+    if B == 300:  # runs
+        refs = np.repeat(rng.random(n_pages // 500) < busy, 500).astype(int)
+    free = int((refs == 0).sum())
+    wide = 2 * free // B + 1
+    table, held = np.full((B, wide), -1), [0] * B
+    pool = tree_ref.Pool(refs, table, held, 16)
+    r = torch.zeros(n_pages + off, dtype=torch.int32, device="cuda")[off:]
+    r.copy_(i32(refs))
+    t, h = i32(table), i32(held)
+    for top in (free // B // 2, 2 * free // B, free // B, 0):  # what there is, too many, fewer again, nothing
+        lens = rng.integers(0, 16 * top + 1, B) if top else np.full(B, -1)
+        st = sv.spec_kv_resize(r, t, h, i32(lens), 0, 16, with_status=True)
+        assert list(np_of(st)) == pool.resize(lens.tolist(), 0)
+        same(pool, r, t, h)
+    assert int((np_of(r) <= 0).sum()) == free
+
+
 def test_resize_errors(sv):  # noqa: F811
     rng = np.random.default_rng(10)
     S, wide = 16, 6
