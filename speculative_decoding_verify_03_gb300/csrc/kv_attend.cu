@@ -12,6 +12,8 @@
 // its own, and the warp then adds up rows, two at a time: 256 x 9 x 32 rows of 128, two to
 // four results each, 28 us in place of 57.  Where there are few, a row's chain of loads
 // counts: eight in flight, the first before the weights are known.
+#include <algorithm>
+
 #include "kv_span.h"
 #include "spec_tree.h"
 
@@ -45,6 +47,7 @@ struct MP {
   int32_t G, Hq, D;
   int32_t rto, rtp, co, cp;        // rows per item and CTAs, own and prefix
   int32_t tp, ko_log2;             // key tiles of the prefix; tokens of an own tile
+  uint32_t item;                   // trees: what an own item costs beside its tiles
   Divisor by_G, by_Hq, by_rto, by_rtp;
   const uint32_t *lost_own;          // as plan.lost, of the own items
 };
@@ -88,7 +91,8 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
   // what the plan says of the sequence, before the barriers wait for anything
   uint32_t prow = 0, rows = 0;
   if (w.prefix) prow = P.plan.rows[b], rows = P.plan.rows[w.B];
-  const uint32_t Wo = P.plan.tiles[w.B], tile0 = P.plan.tiles[b], item0 = P.plan.items[b];
+  const uint32_t item0 = P.plan.items[b], tiles = P.plan.tiles[w.B], cost = cost_of_item(tiles, P.co, w.B, P.item);
+  const uint32_t Wo = tiles + cost * P.plan.items[w.B], tile0 = P.plan.tiles[b] + cost * item0;
   int lost = 0;
   if (P.plan.lost)
     for (int c = threadIdx.x; c < P.cp; c += MG_NT) lost |= P.plan.lost[c];
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(MG_NT) merge_kernel(const __grid_constant__ MP
         ip = (item + c.c0) * P.rtp + (k - y * P.rtp);
       }
       const int to = (own + n + (1 << P.ko_log2) - 1) >> P.ko_log2, nj = P.by_rto(n * G + P.rto - 1);
-      const uint32_t y = P.by_rto(r), j = head * nj + y, x = tile0 + j * to;
+      const uint32_t y = P.by_rto(r), j = head * nj + y, x = tile0 + j * (to + cost) + cost;
       const Owners c = owners(x, x + to - 1, Wo, min(static_cast<uint32_t>(P.co), Wo));
       all = np + c.n;
       io = (item0 + j + c.c0 - np) * P.rto + (r - y * P.rto);
@@ -263,11 +267,11 @@ constexpr int64_t kDenseRows = 65;
 // key/value heads of 128 in e4m3, sequences x tokens, replayed calls, span / dense
 // kernel in us:
 //   rows   1 x 100   1 x 8000   8 x 500   8 x 4000   64 x 100   64 x 1000
-//     48   11 / 13    29 / 22   17 / 20    43 / 43    28 / 37     80 / 86
-//     64   11 / 13    29 / 22   25 / 24    50 / 46    30 / 37     94 / 87
-//     80   11 / 13    32 / 22   25 / 25    66 / 46    41 / 40    138 / 91
-//    128   12 / 13    35 / 23   32 / 25    85 / 47    60 / 52    185 / 106
-//    256   12 / 17    48 / 27   38 / 31   146 / 56   117 / 81    356 / 143
+//     48   12 / 13    30 / 23   17 / 19    41 / 42    29 / 39     83 / 87
+//     64   12 / 13    29 / 23   23 / 23    50 / 44    32 / 39     96 / 88
+//     80   12 / 13    32 / 23   27 / 24    66 / 45    39 / 41    141 / 92
+//    128   12 / 14    35 / 23   29 / 24    85 / 45    62 / 55    185 / 108
+//    256   12 / 17    49 / 27   39 / 28   148 / 52   116 / 85    359 / 144
 // Heads of 64 cross over between 64 and 104 rows, bfloat16 caches as these do.  From
 // here on the dense kernel loses 5 us at most, where the context is short.
 constexpr int64_t kDenseTreeRows = 65;
@@ -300,7 +304,7 @@ bool lay_out(const View &w, int D, int G, bool tree, Layout &L) {
   const int64_t cap = (static_cast<int64_t>(w.max_pages) << w.ps_log2);
   L.tiles_o = io * ((cap + L.ko - 1) / L.ko);
   L.tiles_p = ip * ((w.prefix + static_cast<int64_t>(L.kp) - 1) / L.kp);
-  if (io > INT32_MAX / 2 || ip > INT32_MAX / 2 || L.tiles_o > INT32_MAX || L.tiles_p > INT32_MAX)
+  if (io > INT32_MAX / 2 || ip > INT32_MAX / 2 || L.tiles_o + std::max<int64_t>(SP_ITEM, DN_ITEM) * io > INT32_MAX || L.tiles_p > INT32_MAX)
     return false;
   L.items_o = io, L.items_p = ip;
   const size_t so = static_cast<size_t>(io + (L.dense_own ? kMaxDense : kMaxGrid)) * L.ro;
@@ -380,6 +384,7 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
   m.by_G = Divisor(G), m.by_Hq = Divisor(n_heads), m.by_rto = Divisor(L.ro), m.by_rtp = Divisor(L.rp);
   m.tp = static_cast<int>((P.w.prefix + static_cast<int64_t>(L.kp) - 1) / L.kp);
   while (1 << m.ko_log2 < L.ko) ++m.ko_log2;
+  m.item = !tree ? 0 : L.dense_own ? DN_ITEM : SP_ITEM;
   m.out = static_cast<__nv_bfloat16 *>(out);
   m.lse = lse;
   m.status = row_status;

@@ -212,11 +212,16 @@ __global__ void __launch_bounds__(DN_NT, 1) dense_kernel(const __grid_constant__
   const uint32_t tmem = S.tmem;
   volatile uint32_t *dead = &S.dead;
   const int nj = (rows + DN_ROWS - 1) / DN_ROWS;          // prefix: items of a key/value head
-  const uint32_t W = OWN ? rows : static_cast<uint32_t>((w.prefix + DN_TILE - 1) / DN_TILE) * nj * w.Hkv;
+  const uint32_t cost = OWN ? cost_of_item(rows, gridDim.x, B, DN_ITEM) : 0;
+  const uint32_t W = OWN ? rows + cost * items : static_cast<uint32_t>((w.prefix + DN_TILE - 1) / DN_TILE) * nj * w.Hkv;
   const uint32_t ctas = min(gridDim.x, W);
-  const bool idle = blockIdx.x >= ctas;
-  const uint32_t lo = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(W) * blockIdx.x / ctas);
-  const uint32_t hi = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(W) * (blockIdx.x + 1) / ctas);
+  bool idle = blockIdx.x >= ctas;
+  uint32_t lo = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(W) * blockIdx.x / ctas);
+  uint32_t hi = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(W) * (blockIdx.x + 1) / ctas);
+  if (OWN && cost) {
+    lo = tile_at(w, cum, cum1, cost, DN_TILE, lo), hi = tile_at(w, cum, cum1, cost, DN_TILE, hi);
+    idle |= lo >= hi;
+  }
   const int tiles = static_cast<int>(hi - lo);
   // --- the first tile, and the next one
   auto shape = [&](DenseAt &x) {

@@ -205,14 +205,18 @@ __global__ void __launch_bounds__(32 * WR *WT, SpanCfg<D, E4M3, WR, WT>::MIN_CTA
   }
   const uint32_t rows_all = cum0[B];  // prefix: query rows of a key/value head
   const int pnt = (w.prefix + kTile - 1) / kTile, pnj = (rows_all + RT - 1) / RT;
-  const uint32_t W = pre ? static_cast<uint32_t>(pnt) * pnj * w.Hkv : cum0[B];
-  const uint32_t ctas = min(gridDim.x, W);  // every one of them has a tile
-  if (blockIdx.x >= ctas) {
+  // trees: places, tiles and what an item costs beside its own
+  const uint32_t cost = TREE ? cost_of_item(cum0[B], gridDim.x, B, SP_ITEM) : 0;
+  const uint32_t W = pre ? static_cast<uint32_t>(pnt) * pnj * w.Hkv : cum0[B] + cost * cum1[B];
+  const uint32_t ctas = min(gridDim.x, W);
+  const bool idle = blockIdx.x >= ctas;
+  uint32_t lo = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(W) * blockIdx.x / ctas);
+  uint32_t hi = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(W) * (blockIdx.x + 1) / ctas);
+  if (TREE && cost) lo = tile_at(w, cum0, cum1, cost, kTile, lo), hi = tile_at(w, cum0, cum1, cost, kTile, hi);
+  if (idle || (TREE && lo >= hi)) {
     wait_for_first(P);
     return;
   }
-  const uint32_t lo = static_cast<uint32_t>(static_cast<uint64_t>(W) * blockIdx.x / ctas);
-  const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(W) * (blockIdx.x + 1) / ctas);
 
   auto before = [&](uint32_t x) {  // largest b with cum0[b] <= x (x < cum0[B])
     int l = 0, r = B;

@@ -127,6 +127,35 @@ __device__ __forceinline__ void wait_for_first(const SpanParams &p) {
   if (p.behind) cudaGridDependencySynchronize();
 }
 
+// Trees: what an own item costs beside its tiles, in tiles, when work is shared out among
+// the CTAs of the span kernel and of the dense one; nothing where every tile can have a
+// CTA of its own, or all items are one sequence's and alike.  Measured, us for the call, with 0 / 1 / 2 / 3 (dense: / 4), 32 heads of
+// 128 over 8 in e4m3: span kernel, 16 trees of 8 nodes over 1..2000 tokens 41 / 31 / 28 /
+// 29, 256 over 1..500 138 / 116 / 108 / 110, 8 of 16 over 8000 87 / 85 / 85 / 88; dense
+// kernel, 16 of 40 over 1..2000 80 / 47 / 43 / 42 / 44, 64 of 40 over 1..500 104 / 84 / 76 /
+// 76 / 78, 16 of 64 over 2000..8192 111 / 109 / 108 / 106 / 104.
+constexpr uint32_t SP_ITEM = 2, DN_ITEM = 3;
+__host__ __device__ __forceinline__ uint32_t cost_of_item(uint32_t tiles, uint32_t ctas, int B, uint32_t cost) {
+  return tiles > ctas && B > 1 ? cost : 0;
+}
+// An item's places are its cost, then its tiles.  The first tile at or behind place x, with
+// cum0 the tiles before each sequence and cum1 its items.
+__device__ __forceinline__ uint32_t tile_at(const View &w, const uint32_t *cum0, const uint32_t *cum1, uint32_t cost, int tokens,
+                                            uint32_t x) {
+  if (x >= cum0[w.B] + cost * cum1[w.B]) return cum0[w.B];
+  int b = 0, r = w.B;
+  while (r - b > 1) {
+    const int m = (b + r) >> 1;
+    if (cum0[m] + cost * cum1[m] <= x) b = m;
+    else r = m;
+  }
+  int own, n;
+  row_shape(w, b, own, n);
+  const uint32_t nt = (own + n + tokens - 1) / tokens;
+  const uint32_t y = x - cum0[b] - cost * cum1[b], j = y / (nt + cost), t = y - j * (nt + cost);
+  return cum0[b] + j * nt + (t > cost ? t - cost : 0);
+}
+
 // The dense kernel: prefix items of DN_ROWS rows, tiles of 128 tokens.
 constexpr int DN_ROWS = 256;
 constexpr int kMaxDense = 152;  // CTAs of the dense kernel at most: one on each multiprocessor

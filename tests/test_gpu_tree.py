@@ -383,3 +383,17 @@ def test_attend_tree_many_rows(sv, fmt, case):  # noqa: F811
         assert torch.isnan(got[0][b]).all() and torch.isnan(got[1][b]).all()
     good = np.delete(np.arange(B), [3, 7])
     check_attend([x[i32(good).long()] for x in got[:2]], [x[good] for x in want], fmt, g[good], least=least)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "bf16"])
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,prefix", [(200, 4, 16, 16, 64, 0), (60, 40, 16, 4, 64, 20), (41, 70, 8, 8, 80, 0),
+                                                 (50, 17, 32, 4, 128, 0), (2, 300, 64, 32, 64, 0)])
+def test_attend_tree_items_of_few_tiles(sv, fmt, B, N, Hq, Hkv, D, prefix):  # noqa: F811
+    """More tiles than CTAs, of items that hold one or two: where items count for more
+    than their tiles some CTAs have nothing to do.  One long sequence, empty ones."""
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 40, B)
+    lens[B // 2], lens[::9] = 1500, 0
+    g = rng.integers(0, N, B)
+    g[0], g[-1] = N - 1, 0
+    check(sv, tree_case(sv, 73, fmt, B, N, Hq, Hkv, D, 16, prefix, lens, gammas=g), fmt)
