@@ -48,7 +48,8 @@
 // 8192 e4m3 tokens 285 us, 1085 TFLOP/s, 57 % of the products' rate: tensor pipe 46 %
 // active, 58 % of the issue slots used (over bfloat16 tokens a call takes 7 % less: the
 // conversions).  16 trees of 64 nodes of 32 heads over
-// 2000..8192 tokens 105 us, 800 TFLOP/s: 34 tiles and two items a CTA, whose ends show.
+// 2000..8192 tokens 100 us, 840 TFLOP/s: 34 tiles and two items a CTA, whose ends show (an
+// item costs about three tiles beside its own, DN_ITEM).
 #pragma once
 
 #include <cuda_fp16.h>

@@ -44,7 +44,7 @@
 // 344 us (100 TFLOP/s of what its queries see; each row tile walks all keys).
 // Trees (TREE): up to 64 rows a key/value head.  All rows see what is before the step;
 // in the tiles that hold the step's tokens a row's 64 bits say which of them it sees.
-// 48 trees of 2..15 nodes of 16 heads of 64 behind 1001 + 0..300 bfloat16 tokens: 21 us.
+// 48 trees of 2..15 nodes of 16 heads of 64 behind 1001 + 0..300 bfloat16 tokens: 18 us.
 #pragma once
 
 #include <cuda_fp16.h>
