@@ -1,12 +1,13 @@
 // kv_common.cuh -- shared by the key/value-cache operators: argument checks
 // of the cache and batch descriptors, the resolved (device-side) form of
-// both, and small device helpers.
+// both, the opt-in for shared memory, and small device helpers.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "spec_kv.h"
@@ -79,6 +80,20 @@ inline spec_status make_view(const spec_kv_cache *c, const spec_kv_batch *b, boo
   w.Hkv = c->n_kv_heads;
   w.ps_log2 = lg;
   return SPEC_OK;
+}
+
+constexpr int kDevices = 64;
+
+// The kernel may use `most` bytes of dynamic shared memory: set once per device, whatever
+// the launch at hand needs (beside static shared memory less than 48 KB may be too much
+// without it).
+inline bool allow_shared(const void *f, int most, std::atomic<bool> *ready) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
+  if (ready[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return false;
+  ready[dev].store(true, std::memory_order_release);
+  return true;
 }
 
 // ------------------------------------------------------------------ device

@@ -25,7 +25,6 @@
 // (62 MB in and out) 8.0 us, 7.8 TB/s: what was read just before is in L2.
 #include <cooperative_groups.h>
 
-#include <atomic>
 #include <type_traits>
 #include <utility>
 
@@ -608,18 +607,6 @@ __global__ void __cluster_dims__(TB_CTAS, 1, 1) __launch_bounds__(TB_NT) fork_ke
   if (team.ctas > 1 && cum[n]) team.sync();
 }
 
-constexpr int kDevices = 64;
-
-// The kernel may use `most` bytes of shared memory: set once per device.
-bool allow_shared(const void *f, int most, std::atomic<bool> *ready) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
-  if (ready[dev].load(std::memory_order_acquire)) return true;
-  if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return false;
-  ready[dev].store(true, std::memory_order_release);
-  return true;
-}
-
 spec_status check_pool(const spec_kv_pool *p, Pool &P) {
   if (!p || p->B < 0 || p->max_pages < 0 || p->n_pages < 0 || p->page_size < 1 || p->prefix_len < 0 ||
       p->table_row_stride < p->max_pages)
@@ -702,8 +689,8 @@ extern "C" spec_status spec_kv_resize(const spec_kv_pool *pool, const int32_t *k
   R.n = n_step;
   R.status = row_status;
   const int smem = sizeof(TableShared) + (3 * pool->B + 2) * 4;
-  static std::atomic<bool> ready[kDevices] = {};
-  if (!allow_shared(reinterpret_cast<const void *>(resize_kernel), sizeof(TableShared) + (3 * kv::kMaxB + 2) * 4, ready)) return SPEC_ERR_CUDA;
+  static std::atomic<bool> ready[kv::kDevices] = {};
+  if (!kv::allow_shared(reinterpret_cast<const void *>(resize_kernel), sizeof(TableShared) + (3 * kv::kMaxB + 2) * 4, ready)) return SPEC_ERR_CUDA;
   resize_kernel<<<TB_CTAS, TB_NT, smem, static_cast<cudaStream_t>(stream)>>>(R);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
@@ -728,8 +715,8 @@ extern "C" spec_status spec_kv_fork(const spec_kv_pool *pool, int32_t *kv_len, c
   F.copies = copies;
   F.status = fork_status;
   const int smem = sizeof(TableShared) + (2 * (n + 1) + pool->B + n) * 4 + n;
-  static std::atomic<bool> ready[kDevices] = {};
-  if (!allow_shared(reinterpret_cast<const void *>(fork_kernel), sizeof(TableShared) + (4 * kv::kMaxB + 2) * 4 + kv::kMaxB, ready)) return SPEC_ERR_CUDA;
+  static std::atomic<bool> ready[kv::kDevices] = {};
+  if (!kv::allow_shared(reinterpret_cast<const void *>(fork_kernel), sizeof(TableShared) + (4 * kv::kMaxB + 2) * 4 + kv::kMaxB, ready)) return SPEC_ERR_CUDA;
   fork_kernel<<<TB_CTAS, TB_NT, smem, static_cast<cudaStream_t>(stream)>>>(F);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

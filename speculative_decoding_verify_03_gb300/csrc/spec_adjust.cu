@@ -24,15 +24,16 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cstdint>
 
-#include "spec_kv.h"
+#include "kv_common.cuh"
 #include "spec_tree.h"
 
 namespace {
 
 constexpr int AJ_NT = 256;           // threads per CTA
 constexpr int AJ_SLICE = 8192;       // tokens of a slice at most
+constexpr int AJ_DRAFTS = 4096;      // drafts of a sequence at most, where they are counted
+constexpr int AJ_SMEM = AJ_SLICE * 10 + AJ_DRAFTS * 4;  // dynamic shared memory of a CTA at most
 constexpr int AJ_COUNT = 128;        // of them counting, while the others begin with the stream;
 constexpr int AJ_LONG = 16384;       // all of them for sequences of this length
 constexpr int AJ_UNROLL = 4;         // loads of a thread in flight together: of the stream,
@@ -280,7 +281,7 @@ extern "C" spec_status spec_adjust(const void *logits, const spec_adjust_params 
     return SPEC_ERR_INVALID_ARG;
   const int N = a.gamma_max + 1;
   if (a.gamma_max >= 1 << 20 || a.capacity >= 1 << 30 || a.n_bias > 65534 || a.B > 1 << 20 || (a.tree_mask && N > SPEC_TREE_MAX) ||
-      (a.gamma_max > 4096 && (a.repetition || a.presence || a.frequency)))
+      (a.gamma_max > AJ_DRAFTS && (a.repetition || a.presence || a.frequency)))
     return SPEC_ERR_UNSUPPORTED;
   if (a.B == 0) return SPEC_OK;
   const uintptr_t es = a.dtype == SPEC_F32 ? 4 : 2;
@@ -326,12 +327,11 @@ extern "C" spec_status spec_adjust(const void *logits, const spec_adjust_params 
   P.groups = (N + P.npos - 1) / P.npos;
   const int64_t grid = have * P.groups;
   if (grid > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
-  const int smem = P.slice * (a.n_bias ? 8 : 4) + P.slice * 2 + std::min(a.gamma_max, 4096) * 4;
+  const int smem = P.slice * (a.n_bias ? 8 : 4) + P.slice * 2 + std::min(a.gamma_max, AJ_DRAFTS) * 4;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto *k = a.dtype == SPEC_F32 ? adjust_kernel<true> : adjust_kernel<false>;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) != cudaSuccess)
-    return SPEC_ERR_CUDA;
+  static std::atomic<bool> ready[2][kv::kDevices] = {};
+  if (!kv::allow_shared(reinterpret_cast<const void *>(k), AJ_SMEM, ready[a.dtype == SPEC_F32])) return SPEC_ERR_CUDA;
   k<<<static_cast<unsigned>(grid), AJ_NT, smem, s>>>(P);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
