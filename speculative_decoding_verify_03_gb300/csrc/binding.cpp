@@ -358,6 +358,7 @@ PyObject *attend_tree(PyObject *const *a) {
   if (D > 1 && q.stride(3) != 1) fail(PyExc_ValueError, "the head_dim axis must be contiguous");
   const int64_t B = q.size(0), N = q.size(1);
   const int32_t Hq = size32(q.size(2));
+  if (cache->n_kv_heads < 1 || cache->page_size < 1) fail(PyExc_ValueError, "the cache's pages must hold a head and a slot at least");
   if (Hq < 1 || Hq % cache->n_kv_heads) fail(PyExc_ValueError, "n_heads must be a multiple of the cache's n_kv_heads");
   spec_kv_batch b = {};
   b.table_row_stride = page_table(pages, B, dev);

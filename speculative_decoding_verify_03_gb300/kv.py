@@ -131,6 +131,8 @@ def _batch(cache, page_table, kv_len, gamma_max, prefix_table, prefix_len, gamma
     gamma = None if gamma_per_row is None else _int32("gamma_per_row", gamma_per_row, B, dev)
     pt, prefix_len = None, int(prefix_len)
     if prefix_len > 0:
+        if cache.page_size < 1:
+            raise ValueError("the cache's pages must hold a slot at least")
         need = -(-prefix_len // cache.page_size)
         if prefix_table is None or prefix_table.dim() != 1 or prefix_table.shape[0] < need:
             raise ValueError(f"prefix_table must hold the prefix's {need} page ids")
@@ -320,6 +322,8 @@ def spec_attend(q, cache, page_table, kv_len, prefix_table=None, prefix_len=0, g
     if qs[3] != 1:
         raise ValueError("the head_dim axis must be contiguous")
     B, N, Hq, D = shape
+    if cache.n_kv_heads < 1:
+        raise ValueError("the cache's pages must hold a head at least")
     if Hq < 1 or Hq % cache.n_kv_heads:
         raise ValueError("n_heads must be a multiple of the cache's n_kv_heads")
     b = _batch(cache, page_table, kv_len, N - 1, prefix_table, prefix_len, gamma_per_row)
