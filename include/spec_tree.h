@@ -109,10 +109,11 @@ typedef struct {
 
 /*
  * out may be logits itself (in place: only what changes is then read and
- * written), or a tensor that does not overlap it.  Positions past gamma_b are
- * copied as they are.  A row with an error (SPEC_ROW_BAD_GAMMA,
- * SPEC_ROW_BAD_PENALTY, SPEC_ROW_BAD_LENGTH (1 << 7): seq_len outside [0,
- * capacity], prompt_len outside [0, seq_len]) gives NaN in all its positions.
+ * written), or a tensor that has no element in common with it (refused
+ * otherwise).  Positions past gamma_b are copied as they are.  A row with an
+ * error (SPEC_ROW_BAD_GAMMA, SPEC_ROW_BAD_PENALTY, SPEC_ROW_BAD_LENGTH (1 << 7):
+ * seq_len outside [0, capacity], prompt_len outside [0, seq_len]) gives NaN in
+ * all its positions.
  * Both tensors need their element's alignment; rows of both that are equally
  * far from a multiple of 16 bytes run faster.
  */

@@ -267,6 +267,46 @@ __global__ void __launch_bounds__(AJ_NT) adjust_kernel(const __grid_constant__ J
 
 bool aligned(const void *p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
+// Rows of V elements that begin at p big + q small, p < nb, q < ns, and do not overlap: the
+// ns inner ones are all within `big` elements.
+struct Rows {
+  int64_t big, nb, small, ns, V;
+  // Whether a row that begins at t has an element in common with one of them (with
+  // `both`, of those with negative p and q too): of p and of q only the two multiples
+  // next to what is left of t can be.
+  bool meet(int64_t t, bool both) const {
+    auto next_to = [&](int64_t t, int64_t step, int64_t n, auto f) {
+      if (n == 1) return f(0);
+      const int64_t k = t / step - (t % step < 0);
+      auto in = [&](int64_t k) { return k < n && k >= (both ? 1 - n : 0) && f(k); };
+      return in(k) || in(k + 1);
+    };
+    return next_to(t, big, nb, [&](int64_t p) {
+      const int64_t u = nb > 1 ? t - p * big : t;
+      return next_to(u, small, ns, [&](int64_t q) {
+        const int64_t d = ns > 1 ? u - q * small : u;
+        return d < V && d > -V;
+      });
+    });
+  }
+};
+
+// Whether some row of the logits has an element in common with some row of the output,
+// which begins `at` elements behind them and whose rows do not overlap.
+bool overlap(const spec_adjust_params &a, int64_t at) {
+  const int64_t B = a.B, N = static_cast<int64_t>(a.gamma_max) + 1, V = a.V;
+  const int64_t lr = B > 1 ? a.logits_row_stride : 0, lp = N > 1 ? a.logits_pos_stride : 0;
+  const int64_t rs = B > 1 ? a.out_row_stride : 0, ps = N > 1 ? a.out_pos_stride : 0;
+  if (at >= (B - 1) * lr + (N - 1) * lp + V || -at >= (B - 1) * rs + (N - 1) * ps + V) return false;
+  const bool in_row = N == 1 || (B > 1 && rs >= (N - 1) * ps + V);  // positions within a row's stride
+  const Rows out = in_row ? Rows{rs, B, ps, N, V} : Rows{ps, N, rs, B, V};
+  if (lr == rs && lp == ps) return out.meet(-at, true);  // differences of two rows of the same kind
+  for (int64_t b = 0; b < (lr ? B : 1); ++b)
+    for (int64_t i = 0; i < (lp ? N : 1); ++i)
+      if (out.meet(b * lr + i * lp - at, false)) return true;
+  return false;
+}
+
 }  // namespace
 
 extern "C" spec_status spec_adjust(const void *logits, const spec_adjust_params *params, void *out,
@@ -306,6 +346,8 @@ extern "C" spec_status spec_adjust(const void *logits, const spec_adjust_params 
   if (P.same && ((a.B > 1 && a.logits_row_stride != a.out_row_stride) ||
                  (a.gamma_max > 0 && a.logits_pos_stride != a.out_pos_stride)))
     return SPEC_ERR_INVALID_ARG;
+  const int64_t apart = static_cast<int64_t>(y - x) / static_cast<int64_t>(es);
+  if (!P.same && overlap(a, apart)) return SPEC_ERR_INVALID_ARG;
   P.W = (N + 31) / 32;
   const uintptr_t off = (x ^ y) | static_cast<uintptr_t>(a.B > 1 ? (a.logits_row_stride - a.out_row_stride) * static_cast<int64_t>(es) : 0) |
                         static_cast<uintptr_t>(a.gamma_max > 0 ? (a.logits_pos_stride - a.out_pos_stride) * static_cast<int64_t>(es) : 0);
