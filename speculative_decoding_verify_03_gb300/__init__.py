@@ -107,31 +107,42 @@ def _compile(out: str, extra=()):
                 os.remove(o)
 
 
-def _binding_cmd(out: str) -> list:
-    """One g++ command that compiles the host-side binding (PyTorch's own headers and libraries)."""
+def _binding_cmd(out: str):
+    """One g++ command that compiles the host-side binding (PyTorch's own headers and libraries),
+    or None where PyTorch, g++, or Python's or CUDA's headers are not there: the library does
+    without them."""
+    import shutil
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except (ImportError, OSError):
+        return None
     home = os.path.dirname(torch.__file__)
     libs = os.path.join(home, "lib")
+    python = sysconfig.get_paths()["include"]
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    if not (shutil.which("g++") and os.path.exists(os.path.join(python, "Python.h")) and
+            os.path.exists(os.path.join(cuda, "cuda_runtime_api.h"))):
+        return None
     include = [os.path.join(_ROOT, "include"), os.path.join(home, "include"),
-               os.path.join(home, "include", "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
+               os.path.join(home, "include", "torch", "csrc", "api", "include"), python, cuda]
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
             *(x for path in include for x in ("-I", path)), _BINDING_SOURCE, "-L", libs, "-ltorch_python", "-ltorch_cpu",
             "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}", "-o", out]
 
 
 def build(force: bool = False, out: str = None, extra=()) -> str:
-    """Compile libspecverify.so in-tree for sm_103a, and the host-side binding
-    beside it (each skipped when up to date)."""
+    """Compile libspecverify.so in-tree for sm_103a, which takes nvcc alone, and
+    the host-side binding beside it where there is what that takes (each skipped
+    when up to date).  Neither waits for the other's success."""
     def stale(path, deps):
         return force or not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
 
-    binding = None
+    binding, made = None, BINDING_PATH + f".tmp{os.getpid()}"
     if out is None and stale(BINDING_PATH, [_BINDING_SOURCE] + _HEADERS):
-        made = BINDING_PATH + f".tmp{os.getpid()}"
-        binding = subprocess.Popen(_binding_cmd(made))
+        cmd = _binding_cmd(made)
+        binding = subprocess.Popen(cmd) if cmd else None
     out = out or LIB_PATH
     try:
         if stale(out, _DEPS):
@@ -140,10 +151,12 @@ def build(force: bool = False, out: str = None, extra=()) -> str:
             os.replace(tmp, out)
     finally:
         code = binding.wait() if binding else 0
+        if binding and code == 0:
+            os.replace(made, BINDING_PATH)
+        elif os.path.exists(made):
+            os.remove(made)
     if code:
         raise subprocess.CalledProcessError(code, "g++ binding.cpp")
-    if binding:
-        os.replace(made, BINDING_PATH)
     return out
 
 

@@ -163,7 +163,7 @@ def _native():
 
         from . import BINDING_PATH, SpecError
         if not os.path.exists(BINDING_PATH):
-            raise SpecError(f"{BINDING_PATH} is missing: call build() first")
+            raise SpecError(f"{BINDING_PATH} is missing: call build() first (it takes PyTorch, g++ and Python's headers)")
         spec = importlib.util.spec_from_file_location(__package__ + "._binding", BINDING_PATH)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
