@@ -16,7 +16,7 @@ import threading
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
-BINDING_PATH = os.path.join(_HERE, "_binding.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")  # binding_path() adds what it is made for
 _BINDING_SOURCE = os.path.join(_HERE, "csrc", "binding.cpp")
 _SOURCES = [os.path.join(_HERE, "csrc", f) for f in ("spec_verify.cu", "spec_strip.cu", "spec_row.cu",
                                                       "spec_commit.cu", "spec_law.cu",
@@ -107,6 +107,17 @@ def _compile(out: str, extra=()):
                 os.remove(o)
 
 
+def binding_path() -> str:
+    """Where the host-side binding is.  It is made for one PyTorch and one Python, whose
+    interfaces it is compiled against, and its name says so: after an upgrade it is another
+    file, which is not there until build() makes it."""
+    import sysconfig
+
+    import torch
+    stem, end = os.path.splitext(BINDING_PATH)
+    return f"{stem}.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}{end}"
+
+
 def _binding_cmd(out: str):
     """One g++ command that compiles the host-side binding (PyTorch's own headers and libraries),
     or None where PyTorch, g++, or Python's or CUDA's headers are not there: the library does
@@ -139,8 +150,14 @@ def build(force: bool = False, out: str = None, extra=()) -> str:
     def stale(path, deps):
         return force or not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
 
-    binding, made = None, BINDING_PATH + f".tmp{os.getpid()}"
-    if out is None and stale(BINDING_PATH, [_BINDING_SOURCE] + _HEADERS):
+    binding = path = None
+    if out is None:
+        try:
+            path = binding_path()
+        except (ImportError, OSError):
+            pass  # no PyTorch
+    made = f"{path}.tmp{os.getpid()}"
+    if path and stale(path, [_BINDING_SOURCE] + _HEADERS):
         cmd = _binding_cmd(made)
         binding = subprocess.Popen(cmd) if cmd else None
     out = out or LIB_PATH
@@ -152,7 +169,7 @@ def build(force: bool = False, out: str = None, extra=()) -> str:
     finally:
         code = binding.wait() if binding else 0
         if binding and code == 0:
-            os.replace(made, BINDING_PATH)
+            os.replace(made, path)
         elif os.path.exists(made):
             os.remove(made)
     if code:

@@ -161,10 +161,11 @@ def _native():
     if _module is None:
         import importlib.util
 
-        from . import BINDING_PATH, SpecError
-        if not os.path.exists(BINDING_PATH):
-            raise SpecError(f"{BINDING_PATH} is missing: call build() first (it takes PyTorch, g++ and Python's headers)")
-        spec = importlib.util.spec_from_file_location(__package__ + "._binding", BINDING_PATH)
+        from . import SpecError, binding_path
+        path = binding_path()
+        if not os.path.exists(path):
+            raise SpecError(f"{path} is missing: call build() first (it takes PyTorch, g++ and Python's headers)")
+        spec = importlib.util.spec_from_file_location(__package__ + "._binding", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         lib = _lib()

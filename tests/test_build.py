@@ -95,3 +95,25 @@ def test_no_binding_is_an_error_at_its_first_use(tree, monkeypatch):
     monkeypatch.setattr(kv, "_module", None)
     with pytest.raises(m.SpecError, match="build"):
         m.spec_tree_mask(torch.zeros((2, 3), dtype=torch.int32))
+
+
+@pytest.mark.parametrize("change", ["torch", "python"])
+def test_a_binding_made_for_another_torch_or_python_is_not_taken(tree, monkeypatch, change):
+    """It is compiled against their interfaces, whatever the age of its own sources."""
+    import torch
+
+    from speculative_decoding_verify_03_gb300 import kv
+    path, gxx = tree
+    gxx(0)
+    m.build()
+    first = glob.glob(str(path / "_binding*"))
+    assert len(first) == 1
+    if change == "torch":
+        monkeypatch.setattr(torch, "__version__", "9.9.9")
+    else:
+        monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-999")
+    monkeypatch.setattr(kv, "_module", None)
+    with pytest.raises(m.SpecError, match="build"):
+        m.spec_tree_mask(torch.zeros((2, 3), dtype=torch.int32))
+    m.build()
+    assert len(glob.glob(str(path / "_binding*"))) == 2
