@@ -278,8 +278,9 @@ PyObject *compact(PyObject *const *a) {
   b.B = size32(B), b.gamma_max = size32(N - 1), b.max_pages = size32(pages.size(1));
   b.prefix_len = number(a[6]);
   b.page_table = static_cast<const int32_t *>(pages.const_data_ptr());
-  b.prefix_table = b.prefix_len > 0 ? b.page_table : nullptr;  // not read: the step is past the prefix
   b.kv_len = ints(a[3], "kv_len", {B}, dev);
+  // not read, the step is past the prefix; a table without columns has no address
+  b.prefix_table = b.prefix_len > 0 ? b.kv_len : nullptr;
   const int32_t *way = ints(a[4], "path", {B, N}, dev), *acc = ints(a[5], "accepted_len", {B}, dev);
   const spec_kv_cache *cache = cache_of(a[0]);
   const On on(dev);

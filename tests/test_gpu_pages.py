@@ -423,3 +423,16 @@ def test_calls_leave_no_references(sv):  # noqa: F811
     gc.collect()
     assert [sys.getrefcount(t) for t in (p, q, z, seq, n)] == held
     assert torch.cuda.memory_allocated() == before
+
+
+def test_compact_of_tables_without_columns(sv):  # noqa: F811
+    """Sequences that hold the shared prefix alone and accepted nothing: nothing moves."""
+    cache = make_cache(sv, np.random.default_rng(15), "bf16", 4, 2, 16, 64)[0]
+    want = contents(cache)
+    args = i32(np.zeros((2, 0))), i32([40, 40]), i32([[0, 1, -1], [0, 1, 2]])
+    st = sv.spec_kv_compact(cache, *args, i32([0, 0]), prefix_len=40, with_status=True)
+    assert list(np_of(st)) == [0, 0]
+    st = sv.spec_kv_compact(cache, *args, i32([0, 1]), prefix_len=40, with_status=True)
+    assert list(np_of(st)) == [0, tree_ref.BAD_LENGTH]
+    for x, y in zip(contents(cache), want):
+        assert np.array_equal(x, y)
