@@ -52,8 +52,9 @@ struct MP {
   const uint32_t *lost_own;          // as plan.lost, of the own items
 };
 
-// The CTAs c0 .. c0 + n - 1 that worked on tiles x .. y of W, as owner() says, by an
-// estimate that is off by one at most: C < 2^10, so the float's error is below 2^-11.
+// The CTAs c0 .. c0 + n - 1 that worked on the tiles at places x .. y of W (kv_span.h): CTA
+// ((z + 1) C - 1) / W on the one at z, by an estimate that is off by one at most: C < 2^10, so
+// the float's error is below 2^-11.
 struct Owners {
   uint32_t c0, n;
 };
@@ -273,7 +274,9 @@ constexpr int64_t kDenseRows = 65;
 //    128   12 / 14    35 / 23   29 / 24    85 / 45    62 / 55    185 / 108
 //    256   12 / 17    49 / 27   39 / 28   148 / 52   116 / 85    359 / 144
 // Heads of 64 cross over between 64 and 104 rows, bfloat16 caches as these do.  From
-// here on the dense kernel loses 5 us at most, where the context is short.
+// here on the dense kernel loses 5 us at most, where the context is short.  Below, the
+// span kernel loses up to 8 us where it is long; as with prefixes, the rule is one of rows
+// because the two kernels round differently (include/spec_kv.h says from which on).
 constexpr int64_t kDenseTreeRows = 65;
 static_assert(2 * kMaxDense <= kMaxGrid, "plan: words for the CTAs of both dense launches");
 
@@ -430,7 +433,8 @@ spec_status attend(const spec_kv_cache *cache, const spec_kv_batch *batch, const
   // nodes, 300 tokens), 8192 26.5 / 24.2 / 24.7, 16384 35.4 / 28.0 / 30.2, 32768 110 /
   // 95.3 / 93.8 (1000 tokens); 16 heads of 64: 8192 20.8 / 19.7 / 21.2, 32768 160 / 154 /
   // 158.  With some five results a row, 1 / 4 rows of up to eight: 10240 rows behind a
-  // prefix of 1000 62.1 / 59.1, 8192 rows of 4 trees over 4000 43.2 / 41.9.
+  // prefix of 1000 62.1 / 59.1, 8192 rows of 4 trees over 4000 43.2 / 41.9.  (152: a GB300's
+  // multiprocessors; on others the rule is right and measured for none.)
   const int rw = all <= 152 * 48 ? 1 : some > 4 || all <= 152 * 192 * (D == 64 ? 2 : 1) ? 4 : 8;
   const int per = MG_NT / (D == 64 ? 16 : 32) * rw;  // rows per CTA
   cfg.gridDim = dim3(static_cast<unsigned>((rows + per - 1) / per), P.w.B);

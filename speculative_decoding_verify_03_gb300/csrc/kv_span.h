@@ -5,10 +5,14 @@
 // key/value head, over one list of pages.  Own items: the rows (i, g) of
 // sequence b, r = i * G + g, over the sequence's own tokens.  Prefix items:
 // rows of all sequences together, over the shared prefix.  The key tiles (64
-// tokens) of all items, in item order, are numbered 0 .. W - 1; CTA c of C <= W
-// works on tiles [W c / C, W (c + 1) / C) whatever the items' lengths, and
+// tokens; 128 in the dense kernel) of all items are set out in item order on
+// places 0 .. W - 1: side by side, or, for the own items of trees, with a few
+// places before each item's tiles for what it costs beside them (cost_of_item).
+// CTA c of C <= W works on the tiles whose places are in [W c / C, W (c + 1) / C),
+// whatever the items' lengths (where that is no tile, the CTA is idle), and
 // leaves one partial result for each item that it touches in slot item + c
-// (consecutive CTAs of one item: consecutive slots).
+// (consecutive CTAs of one item: consecutive slots).  The tile at place x is
+// worked on by CTA ((x + 1) C - 1) / W, the largest c with W c / C <= x.
 #pragma once
 
 #include <atomic>
@@ -24,7 +28,7 @@ struct Plan {            // device arrays of B + 1 words
   uint32_t *tiles;       // own: key tiles of the sequences before b
   uint32_t *items;       // own: items of the sequences before b
   uint32_t *rows;        // prefix: query rows (per key/value head) before b
-  uint32_t *lost;        // prefix, per CTA: a wait gave up (null: no kernel with waits ran)
+  uint32_t *lost;        // per CTA of a dense launch: a wait gave up (null: none ran)
 };
 
 struct SpanParams {
@@ -129,11 +133,11 @@ __device__ __forceinline__ void wait_for_first(const SpanParams &p) {
 
 // Trees: what an own item costs beside its tiles, in tiles, when work is shared out among
 // the CTAs of the span kernel and of the dense one; nothing where every tile can have a
-// CTA of its own, or all items are one sequence's and alike.  Measured, us for the call, with 0 / 1 / 2 / 3 (dense: / 4), 32 heads of
-// 128 over 8 in e4m3: span kernel, 16 trees of 8 nodes over 1..2000 tokens 41 / 31 / 28 /
-// 29, 256 over 1..500 138 / 116 / 108 / 110, 8 of 16 over 8000 87 / 85 / 85 / 88; dense
-// kernel, 16 of 40 over 1..2000 80 / 47 / 43 / 42 / 44, 64 of 40 over 1..500 104 / 84 / 76 /
-// 76 / 78, 16 of 64 over 2000..8192 111 / 109 / 108 / 106 / 104.
+// CTA of its own, or all items are one sequence's and alike.  Measured, us for the call,
+// with 0 / 1 / 2 / 3 (dense: / 4), 32 heads of 128 over 8 in e4m3: span kernel, 16 trees of 8
+// nodes over 1..2000 tokens 41 / 31 / 28 / 29, 256 over 1..500 138 / 116 / 108 / 110, 8 of 16
+// over 8000 87 / 85 / 85 / 88; dense kernel, 16 of 40 over 1..2000 80 / 47 / 43 / 42 / 44, 64
+// of 40 over 1..500 104 / 84 / 76 / 76 / 78, 16 of 64 over 2000..8192 111 / 109 / 108 / 106 / 104.
 constexpr uint32_t SP_ITEM = 2, DN_ITEM = 3;
 __host__ __device__ __forceinline__ uint32_t cost_of_item(uint32_t tiles, uint32_t ctas, int B, uint32_t cost) {
   return tiles > ctas && B > 1 ? cost : 0;
@@ -156,7 +160,8 @@ __device__ __forceinline__ uint32_t tile_at(const View &w, const uint32_t *cum0,
   return cum0[b] + j * nt + (t > cost ? t - cost : 0);
 }
 
-// The dense kernel: prefix items of DN_ROWS rows, tiles of 128 tokens.
+// The dense kernel: items of DN_ROWS rows (of the prefix, or own ones of trees), tiles
+// of 128 tokens.
 constexpr int DN_ROWS = 256;
 constexpr int kMaxDense = 152;  // CTAs of the dense kernel at most: one on each multiprocessor
 static_assert(kMaxDense <= kMaxGrid, "plan");
@@ -165,11 +170,5 @@ cudaError_t dense_bf16(const SpanParams &, int D, int64_t tiles, int *grid, cuda
 // The same over the own tokens of trees.
 cudaError_t dense_tree_e4m3(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
 cudaError_t dense_tree_bf16(const SpanParams &, int D, int64_t tiles, int *grid, cudaStream_t);
-
-// The CTA that works on tile x of W (C <= W CTAs): the largest c with W c / C <= x.
-__host__ __device__ __forceinline__ uint32_t owner(uint32_t x, uint32_t W, uint32_t C) {
-  if (W < (1u << 22)) return ((x + 1) * C - 1) / W;  // C <= 640: no overflow
-  return static_cast<uint32_t>(((static_cast<uint64_t>(x) + 1) * C - 1) / W);
-}
 
 }  // namespace kv

@@ -19,7 +19,10 @@
 // penalties, biases and a mask for every row 114 us, 5.5 TB/s, 81 % of a copy's rate;
 // 64 x 5 rows of 50304 in float32 29 us (a plain copy of them 22.6); one
 // row of 50304 3.6 us.  More warps a multiprocessor (fewer registers) or wider slices
-// lose: 123 to 170 us for the first.
+// lose: 123 to 170 us for the first.  That every slice reads the whole sequence shows where
+// those are long: sequences of 200 / 2000 / 8000 / 65536 tokens, penalties alone, one row of
+// 50304 3.7 / 4.4 / 7.5 / 19.6 us, 64 x 5 of 50304 26 / 27 / 40 / 111, 32 x 31 of 152064 106 / 140 /
+// 180 / 341; the same in place 4.0 / 4.4 / 7.7 / 19.0, 15 / 20 / 32 / 86, 22 / 44 / 97 / 249.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -357,6 +360,7 @@ extern "C" spec_status spec_adjust(const void *logits, const spec_adjust_params 
   // one CTA a multiprocessor; then positions, down to one.  Measured, in us, 64 x 5 rows of
   // 50304 in float32 with 8 / 16 / 24 CTAs wanted: 30.5 / 29.1 / 42.9; of 1024
   // tokens at least: 30.4 / 33.6 / 37.0; 32 x 31 rows of 152064 in bfloat16: 123 / 114 / 114.
+  // (152: a GB300's multiprocessors.)
   const int64_t want = 152 * 16;
   int64_t slices = std::min<int64_t>((want + a.B - 1) / a.B, (a.V + 2047) / 2048);
   if (slices * a.B < 152) slices = std::min<int64_t>((152 + a.B - 1) / a.B, (a.V + 511) / 512);
