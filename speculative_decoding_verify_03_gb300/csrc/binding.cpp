@@ -393,8 +393,10 @@ PyObject *attend_tree(PyObject *const *a) {
     o = on.empty({B, N, Hq, D}, at::kBFloat16);
     lse = on.empty({B, N, Hq}, at::kFloat);
   } else {
-    if (!PyTuple_Check(a[11]) || PyTuple_GET_SIZE(a[11]) != 2) fail(PyExc_TypeError, "out must be a pair of tensors");
-    o = tensor(PyTuple_GET_ITEM(a[11], 0), "out"), lse = tensor(PyTuple_GET_ITEM(a[11], 1), "out");
+    const bool list = PyList_Check(a[11]);
+    if (!(list || PyTuple_Check(a[11])) || PySequence_Size(a[11]) != 2) fail(PyExc_TypeError, "out must be a pair of tensors");
+    o = tensor(list ? PyList_GET_ITEM(a[11], 0) : PyTuple_GET_ITEM(a[11], 0), "out");
+    lse = tensor(list ? PyList_GET_ITEM(a[11], 1) : PyTuple_GET_ITEM(a[11], 1), "out");
     if (o.sizes() != q.sizes() || o.scalar_type() != at::kBFloat16 || !o.is_contiguous() ||
         lse.sizes() != at::IntArrayRef({B, N, Hq}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous() ||
         o.device() != dev || lse.device() != dev)

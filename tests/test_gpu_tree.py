@@ -397,3 +397,16 @@ def test_attend_tree_items_of_few_tiles(sv, fmt, B, N, Hq, Hkv, D, prefix):  # n
     g = rng.integers(0, N, B)
     g[0], g[-1] = N - 1, 0
     check(sv, tree_case(sv, 73, fmt, B, N, Hq, Hkv, D, 16, prefix, lens, gammas=g), fmt)
+
+
+def test_attend_tree_into_a_list(sv):  # noqa: F811
+    """The pair of results may be a list, as spec_attend takes it."""
+    import torch
+    s = tree_case(sv, 74, "bf16", 2, 5, 4, 2, 64, 16, 0, [20, 3])
+    want = call(sv, s)
+    into = [torch.empty_like(want[0]), torch.empty_like(want[1])]
+    got = call(sv, s, out=into)
+    assert got[0] is into[0] and got[1] is into[1] and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for bad in (into[:1], into + into[:1], [into[0], None], {}):
+        with pytest.raises(TypeError):
+            call(sv, s, out=bad)
